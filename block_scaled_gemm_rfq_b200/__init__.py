@@ -25,6 +25,7 @@ __all__ = [
     "mxfp8_codes_bytes", "quantize_mxfp8", "gemm_mxfp8", "quantize_mxfp8_alloc", "gemm_mxfp8_alloc",
     "QuantizedTensor", "quantize_mxfp4_alloc", "quantize_weight_alloc", "gemm_alloc", "linear_alloc",
     "EXPORTED_SYMBOLS", "OUT_F32", "OUT_BF16", "mma_rate_probe", "MMA_PROBE_MAX_ITERATIONS",
+    "linear_ce_workspace_bytes", "linear_ce", "linear_ce_backward", "linear_ce_alloc", "linear_ce_backward_alloc",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -45,6 +46,7 @@ EXPORTED_SYMBOLS = (
     "rfq_linear_static_workspace", "rfq_linear_fused", "rfq_debug_fused_split", "rfq_quantize_mxfp4_t",
     "rfq_gemm_yt", "rfq_linear_dgrad", "rfq_linear_wgrad_workspace_bytes", "rfq_linear_wgrad",
     "rfq_mxfp8_codes_bytes", "rfq_quantize_mxfp8", "rfq_gemm_mxfp8", "rfq_mma_rate_probe",
+    "rfq_linear_ce_workspace_bytes", "rfq_linear_ce", "rfq_linear_ce_backward",
 )
 
 # Largest iteration count of the tensor-core rate probe (RFQ_MMA_PROBE_MAX_ITERATIONS).
@@ -102,6 +104,9 @@ def load_library():
                 "rfq_gemm_mxfp8": (I, [P, P, P, P, I64, I64, I64, P, I, P]),
                 "rfq_mma_rate_probe": (I, [I, I64, P, I64, ctypes.POINTER(ctypes.c_double),
                                            ctypes.POINTER(ctypes.c_int), P]),
+                "rfq_linear_ce_workspace_bytes": (SZ, [I64, I64, I64, I, I]),
+                "rfq_linear_ce": (I, [P, P, P, I64, I64, I64, I64, P, P, P, SZ, P]),
+                "rfq_linear_ce_backward": (I, [P, P, P, P, P, I64, I64, I64, I64, P, P, P, SZ, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(lib, name)
@@ -125,6 +130,54 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _need(where, t, shape, dtype, device):
+    """Refuse a tensor that is not what the C call will read: its type, shape, packing or device."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise RFQError(1, f"{where}: want a contiguous {dtype} tensor {shape} on {device}, got {t.dtype} "
+                          f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+class _On:
+    """The launch's device and stream: the tensors' device is made current for the call, and without
+    a stream the current stream of that device is taken."""
+
+    __slots__ = ("guard", "stream")
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise RFQError(1, f"tensors on {device}: a CUDA device is needed")
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _need_workspace(where, ws, device):
+    import torch
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
+        raise RFQError(1, f"{where}: the workspace is a contiguous uint8 tensor on {device}")
+
+
+def _torch_stream(stream, device):
+    """`stream` as a context for allocations: memory that the call takes belongs to the stream it runs on."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 # ----------------------------------------------------------------------------- sizes
@@ -266,6 +319,53 @@ def gemm_mxfp8(qx_codes, qx_scales, qw_codes, qw_scales, M, N, K, y, stream=None
     y_type = OUT_BF16 if y.dtype == torch.bfloat16 else OUT_F32
     _check(load_library().rfq_gemm_mxfp8(_ptr(qx_codes), _ptr(qx_scales), _ptr(qw_codes), _ptr(qw_scales),
                                          M, N, K, _ptr(y), y_type, _stream(stream)), "rfq_gemm_mxfp8")
+
+
+def linear_ce_workspace_bytes(T: int, D: int, V: int, want_dh: bool = False, want_dw: bool = False) -> int:
+    """rfq_linear_ce_workspace_bytes: workspace of rfq_linear_ce and, where a gradient is wanted, of its backward."""
+    return int(load_library().rfq_linear_ce_workspace_bytes(T, D, V, int(bool(want_dh)), int(bool(want_dw))))
+
+
+def linear_ce(h, w, labels, loss, lse, workspace, ignore_index=-100, stream=None):
+    """rfq_linear_ce: per-row softmax cross entropy of h [T, D] . w [V, D]^T (bf16) against labels [T]
+    (int64) without the logits; loss and lse are fp32 [T]."""
+    import torch
+    T, D = h.shape
+    V = w.shape[0]
+    dev = h.device
+    _need("rfq_linear_ce: h", h, (T, D), torch.bfloat16, dev)
+    _need("rfq_linear_ce: w", w, (V, D), torch.bfloat16, dev)
+    _need("rfq_linear_ce: labels", labels, (T,), torch.int64, dev)
+    _need("rfq_linear_ce: loss", loss, (T,), torch.float32, dev)
+    _need("rfq_linear_ce: lse", lse, (T,), torch.float32, dev)
+    _need_workspace("rfq_linear_ce", workspace, dev)
+    with _On(dev, stream) as st:
+        _check(load_library().rfq_linear_ce(h.data_ptr(), w.data_ptr(), labels.data_ptr(), T, D, V, ignore_index,
+                                            loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                            st), "rfq_linear_ce")
+
+
+def linear_ce_backward(h, w, labels, lse, dloss, dh, dw, workspace, ignore_index=-100, stream=None):
+    """rfq_linear_ce_backward: dh [T, D] and dw [V, D] (bf16; either may be None) of the loss whose
+    gradient by row is dloss [T] fp32; lse as written by linear_ce."""
+    import torch
+    T, D = h.shape
+    V = w.shape[0]
+    dev = h.device
+    _need("rfq_linear_ce_backward: h", h, (T, D), torch.bfloat16, dev)
+    _need("rfq_linear_ce_backward: w", w, (V, D), torch.bfloat16, dev)
+    _need("rfq_linear_ce_backward: labels", labels, (T,), torch.int64, dev)
+    _need("rfq_linear_ce_backward: lse", lse, (T,), torch.float32, dev)
+    _need("rfq_linear_ce_backward: dloss", dloss, (T,), torch.float32, dev)
+    if dh is not None:
+        _need("rfq_linear_ce_backward: dh", dh, (T, D), torch.bfloat16, dev)
+    if dw is not None:
+        _need("rfq_linear_ce_backward: dw", dw, (V, D), torch.bfloat16, dev)
+    _need_workspace("rfq_linear_ce_backward", workspace, dev)
+    with _On(dev, stream) as st:
+        _check(load_library().rfq_linear_ce_backward(
+            h.data_ptr(), w.data_ptr(), labels.data_ptr(), lse.data_ptr(), dloss.data_ptr(), T, D, V, ignore_index,
+            _ptr(dh), _ptr(dw), workspace.data_ptr(), workspace.numel(), st), "rfq_linear_ce_backward")
 
 
 def check_device_error(stream=None):
@@ -412,3 +512,27 @@ def mma_rate_probe(variant, iterations, cycles, stream=None):
                                              ctypes.byref(flops), ctypes.byref(sms), _stream(stream)),
            "rfq_mma_rate_probe")
     return flops.value, sms.value
+
+
+def linear_ce_alloc(h, w, labels, ignore_index=-100, stream=None):
+    """rfq_linear_ce into new tensors: (loss, lse), fp32 [T] each, allocated on the stream the call runs on."""
+    import torch
+    T, D = h.shape
+    with _torch_stream(stream, h.device):
+        loss = torch.empty(T, dtype=torch.float32, device=h.device)
+        lse = torch.empty(T, dtype=torch.float32, device=h.device)
+        ws = _empty_u8(linear_ce_workspace_bytes(T, D, w.shape[0]), h.device)
+    linear_ce(h, w, labels, loss, lse, ws, ignore_index, stream)
+    return loss, lse
+
+
+def linear_ce_backward_alloc(h, w, labels, lse, dloss, want_dh=True, want_dw=True, ignore_index=-100, stream=None):
+    """rfq_linear_ce_backward into new tensors: (dh, dw), None in the place of a gradient that is not wanted."""
+    import torch
+    T, D = h.shape
+    with _torch_stream(stream, h.device):
+        dh = torch.empty_like(h) if want_dh else None
+        dw = torch.empty_like(w) if want_dw else None
+        ws = _empty_u8(linear_ce_workspace_bytes(T, D, w.shape[0], want_dh, want_dw), h.device)
+    linear_ce_backward(h, w, labels, lse, dloss, dh, dw, ws, ignore_index, stream)
+    return dh, dw

@@ -25,6 +25,7 @@ std::mutex g_init_mutex;
 void* g_encode_tiled = nullptr;
 std::atomic<int> g_skip_fill{-1};
 
+bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 rfq_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? RFQ_OK : RFQ_ERR_CUDA; }
@@ -175,6 +176,19 @@ rfq_status_t fused_impl(const void* x, int64_t M, int64_t K, const void* qwc, co
   if (!aligned16(x) || !aligned16(qwc) || !aligned16(qws)) return RFQ_ERR_MISALIGNED;
   return from_cuda(rfq::launch_linear_fused(x, M, K, qwc, qws, N, y, y_type == RFQ_OUT_BF16, use_residual != 0, sms,
                                             g_encode_tiled, stream));
+}
+
+// Output head: rows and vocabulary up to 2^24, width a multiple of 8 up to 2^16 (the tile
+// counts of every product then fit 32 bits).
+constexpr int64_t kCeMaxRows = int64_t(1) << 24;
+constexpr int64_t kCeMaxWidth = int64_t(1) << 16;
+bool ce_shape_ok(int64_t T, int64_t D, int64_t V) {
+  return T >= 0 && T <= kCeMaxRows && V >= 1 && V <= kCeMaxRows && D >= 8 && D <= kCeMaxWidth && (D % 8) == 0;
+}
+
+rfq_status_t check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (workspace == nullptr || bytes < need) return RFQ_ERR_WORKSPACE;
+  return aligned_to(workspace, 256) ? RFQ_OK : RFQ_ERR_MISALIGNED;
 }
 
 }  // namespace
@@ -344,6 +358,55 @@ rfq_status_t rfq_gemm_mxfp8(const void* qx_codes, const void* qx_scales, const v
                                           y_type == RFQ_OUT_BF16, sms, g_encode_tiled, stream));
 }
 
+size_t rfq_linear_ce_workspace_bytes(int64_t T, int64_t D, int64_t V, int want_dh, int want_dw) {
+  if (!ce_shape_ok(T, D, V) || T == 0) return 0;
+  const size_t f = rfq::ce_forward_workspace(T, V);
+  const size_t b = want_dh || want_dw ? rfq::ce_backward_workspace(T, D, V, want_dh != 0) : 0;
+  return f > b ? f : b;
+}
+
+rfq_status_t rfq_linear_ce(const void* h_bf16, const void* w_bf16, const int64_t* labels, int64_t T, int64_t D,
+                           int64_t V, int64_t ignore_index, float* loss, float* lse, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  if (T < 0 || D < 0 || V < 0) return RFQ_ERR_INVALID_ARG;
+  if (!ce_shape_ok(T, D, V)) return RFQ_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return RFQ_OK;
+  if (!h_bf16 || !w_bf16 || !labels || !loss || !lse) return RFQ_ERR_INVALID_ARG;
+  if (!aligned16(h_bf16) || !aligned16(w_bf16) || !aligned_to(labels, 8) || !aligned_to(loss, 4) || !aligned_to(lse, 4))
+    return RFQ_ERR_MISALIGNED;
+  rfq_status_t st = check_workspace(workspace, workspace_bytes, rfq::ce_forward_workspace(T, V));
+  if (st != RFQ_OK) return st;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RFQ_OK) return st;
+  return from_cuda(rfq::launch_ce_forward(h_bf16, w_bf16, labels, T, D, V, ignore_index, loss, lse, workspace, sms,
+                                          g_encode_tiled, stream));
+}
+
+rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, const int64_t* labels, const float* lse,
+                                    const float* dloss, int64_t T, int64_t D, int64_t V, int64_t ignore_index,
+                                    void* dh_bf16, void* dw_bf16, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream) {
+  if (T < 0 || D < 0 || V < 0) return RFQ_ERR_INVALID_ARG;
+  if (!ce_shape_ok(T, D, V)) return RFQ_ERR_UNSUPPORTED_SHAPE;
+  if (!dh_bf16 && !dw_bf16) return RFQ_OK;
+  if ((dh_bf16 && !aligned16(dh_bf16)) || (dw_bf16 && !aligned16(dw_bf16))) return RFQ_ERR_MISALIGNED;
+  int sms = 0;
+  rfq_status_t st;
+  if (T == 0) {
+    if (!dw_bf16) return RFQ_OK;
+    if ((st = current_device(&sms)) != RFQ_OK) return st;
+    return from_cuda(cudaMemsetAsync(dw_bf16, 0, static_cast<size_t>(V) * static_cast<size_t>(D) * 2u, stream));
+  }
+  if (!h_bf16 || !w_bf16 || !labels || !lse || !dloss) return RFQ_ERR_INVALID_ARG;
+  if (!aligned16(h_bf16) || !aligned16(w_bf16) || !aligned_to(labels, 8) || !aligned_to(lse, 4) || !aligned_to(dloss, 4))
+    return RFQ_ERR_MISALIGNED;
+  st = check_workspace(workspace, workspace_bytes, rfq::ce_backward_workspace(T, D, V, dh_bf16 != nullptr));
+  if (st != RFQ_OK) return st;
+  if ((st = current_device(&sms)) != RFQ_OK) return st;
+  return from_cuda(rfq::launch_ce_backward(h_bf16, w_bf16, labels, lse, dloss, T, D, V, ignore_index, dh_bf16, dw_bf16,
+                                           workspace, sms, g_encode_tiled, stream));
+}
+
 rfq_status_t rfq_mma_rate_probe(int variant, int64_t iterations, unsigned long long* cycles, int64_t cycles_len,
                                 double* flops, int* sms_used, cudaStream_t stream) {
   if (variant < 0 || variant > 2 || iterations < 1 || iterations > RFQ_MMA_PROBE_MAX_ITERATIONS || !cycles ||
@@ -373,8 +436,11 @@ rfq_status_t rfq_check_device_error(cudaStream_t stream, int* detail) {
   unsigned int f = 0;
   if (rfq::read_and_clear_quant_error(&q) != cudaSuccess) return RFQ_ERR_CUDA;
   if (rfq::read_and_clear_fused_error(&f) != cudaSuccess) return RFQ_ERR_CUDA;
+  unsigned int c = 0;
+  if (rfq::read_and_clear_ce_error(&c) != cudaSuccess) return RFQ_ERR_CUDA;
   if (v == 0) v = q;
   if (v == 0) v = f;
+  if (v == 0) v = c;
   if (detail) *detail = static_cast<int>(v);
   return v ? RFQ_ERR_TIMEOUT : RFQ_OK;
 }

@@ -1,0 +1,709 @@
+// rfq_ce.cu -- softmax cross entropy at the output head, without the logits.
+//
+// With z = h . w^T (h [T][D] hidden states, w [V][D] the head, both bf16) and one label
+// y_t per row,
+//
+//     lse_t  = log sum_v exp z_tv            loss_t = lse_t - z_{t,y_t}
+//     dz_tv  = dloss_t (exp(z_tv - lse_t) - [v = y_t])
+//     dh     = dz . w                         dw     = dz^T . h
+//
+// A logits matrix would be T x V; here a [256 x 256] tile of it exists only as the fp32
+// accumulator of the tensor cores (TMEM).  Forward: the epilogue reduces each tile row to
+// (max, sum of exponentials) over 128 columns and a second kernel joins those parts.
+// Backward: for one piece of the vocabulary at a time the logits are computed again,
+// turned into dz with the known lse, rounded to bf16 into a workspace of bounded size,
+// and multiplied with w (dh, accumulated over the pieces in fp32) and h (dw, complete).
+//
+// All four products run in one persistent, warp-specialized kernel on tcgen05 kind::f16
+// MMAs; what differs is how the operands lie in shared memory (along K, or along M/N for
+// the products that contract over a matrix's rows: no transposed copy is made) and the
+// epilogue:
+//   kLogits  A = h (K-major)          B = w piece (K-major)     row statistics
+//   kGrad    A = h (K-major)          B = w piece (K-major)     dz in bf16
+//   kHidden  A = dz (K-major)         B = w piece (N-major)     dh, fp32 sums or bf16
+//   kHead    A = dz (M-major)         B = h (N-major)           dw in bf16
+//
+// Roles (per CTA): warp 0 TMA producer, warp 1 MMA issuer (leader CTA of a pair),
+// warps 2..9 epilogue.  Two 256-column accumulators, so that the epilogue of a tile runs
+// under the mainloop of the next.  CTA pairs (256 x 256 tiles) above 128 rows, single
+// CTAs (128 x 256) up to 128, where the rest of a pair's rows would be padding.
+// Every wait on an mbarrier is bounded (rfq_ptx.cuh).  No TMA multicast.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "rfq_internal.h"
+#include "rfq_ptx.cuh"
+#include "rfq_tmap.h"
+
+namespace rfq {
+
+__device__ unsigned int g_ce_error = 0;
+
+namespace {
+
+enum Mode { kLogits = 0, kGrad = 1, kHidden = 2, kHead = 3 };
+
+constexpr int kBM = 128;                 // rows of the output per CTA
+constexpr int kBN = 256;                 // columns of the output per tile
+constexpr int kBK = 64;                  // contraction elements per stage (128 bytes)
+constexpr int kThreads = 320;            // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
+constexpr uint32_t kTmemCols = 512;      // two accumulators of 256 fp32 columns
+constexpr uint32_t kSmemLimit = 232448;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int kPair>
+struct Layout {
+  static constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KiB
+  static constexpr uint32_t kBTile = (kBN / kPair) * kBK * 2;     // 32 KiB (single) or 16 KiB (pair)
+  static constexpr uint32_t kStage = kATile + kBTile;
+  static constexpr uint32_t kBarrierBytes = 256;
+  static constexpr int kStages = static_cast<int>((kSmemLimit - 1024 - kBarrierBytes) / kStage);   // 4 or 7
+  static constexpr uint32_t kSmem = kStages * kStage + kBarrierBytes + 1024;
+  static_assert(kStage % 1024 == 0, "stage buffers must keep 1 KiB alignment");
+  static_assert(kSmem <= kSmemLimit, "exceeds the 227 KiB shared-memory limit");
+  static_assert((2 * kStages + 5) * 8 + 8 <= kBarrierBytes, "barrier area too small");
+};
+
+struct Maps {
+  CUtensorMap a, b;
+};
+
+struct Params {
+  int M, N;               // rows and columns of the product
+  int num_kt;             // k-tiles of the whole contraction
+  int kt_per_split;       // k-tiles of one split
+  int num_mb, num_nb;     // tiles along M (of kBM * kPair rows) and N
+  int group;              // row tiles that pass over the columns together
+  int num_tiles;          // num_mb * num_nb * splits
+  // kLogits, kGrad
+  const int64_t* labels;  // [M]
+  int64_t ignore;
+  int64_t vocab;
+  int64_t v0;             // first vocabulary entry of the piece
+  float2* stats;          // [2 * num_nb][M]: (max * log2 e, sum of 2^(z log2 e - that))
+  float* target;          // [M]: logit of the label
+  const float* lse;       // [M]
+  const float* dloss;     // [M]
+  const float* gmax;      // largest finite |dloss|
+  __nv_bfloat16* dz;      // [M][ld_dz]
+  int64_t ld_dz;
+  // kHidden: fp32 sums [split][M][N], or (out != nullptr) bf16 straight away
+  float* acc;
+  int accumulate;
+  // kHidden (one piece, one split) and kHead
+  __nv_bfloat16* out;     // [M][N]
+};
+
+// Shared-memory operand descriptors (128-byte swizzle).  K-major: rows of 128 bytes, 8-row
+// groups 1024 bytes apart.  M/N-major: chunks of 64 M/N elements x kBK contraction rows of
+// 128 bytes; 8 contraction rows are 1024 bytes (stride offset), the next 64 M/N elements one
+// chunk (8 KiB) further (leading offset).
+constexpr uint32_t kChunk = 64u * kBK * 2u;
+template <bool kMnMajor>
+__device__ __forceinline__ uint64_t operand_desc(const void* p) {
+  const uint64_t addr = smem_addr(p);
+  const uint64_t lbo = kMnMajor ? (kChunk >> 4) : 1u;
+  return ((addr >> 4) & 0x3FFFull) | (lbo << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Start-address step (16-byte units) of the 16 contraction elements of one MMA.
+template <bool kMnMajor>
+constexpr uint64_t kDescStep = kMnMajor ? (16u * 128u) >> 4 : 32u >> 4;
+
+template <int kPair, bool kAMn, bool kBMn>
+__device__ __forceinline__ constexpr uint32_t mma_idesc() {
+  return (1u << 4)                               // D: fp32
+         | (1u << 7) | (1u << 10)                // A, B: bf16
+         | (uint32_t(kAMn) << 15) | (uint32_t(kBMn) << 16)
+         | (uint32_t(kBN >> 3) << 17) | (uint32_t((kBM * kPair) >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct Tile {
+  int split, mb, nb, kt0, kt1;
+};
+// Tiles run over splits, then groups of `group` row tiles, then column tiles, row tile
+// fastest: the CTAs at work share few column tiles of B (the head's rows, which are far
+// larger than L2) and one group of rows of A, which L2 holds.
+__device__ __forceinline__ Tile tile_at(const Params& p, int tile) {
+  Tile t;
+  const int per_split = p.num_mb * p.num_nb;
+  t.split = tile / per_split;
+  const int r = tile - t.split * per_split;
+  const int in_group = p.group * p.num_nb;
+  const int g = r / in_group;
+  const int rr = r - g * in_group;
+  const int rows = min(p.group, p.num_mb - g * p.group);
+  t.nb = rr / rows;
+  t.mb = g * p.group + (rr - t.nb * rows);
+  t.kt0 = t.split * p.kt_per_split;
+  t.kt1 = min(p.num_kt, t.kt0 + p.kt_per_split);
+  return t;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+template <int kPair, int kMode>
+__global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_constant__ Maps maps, const Params p) {
+  using L = Layout<kPair>;
+  constexpr bool kAMn = kMode == kHead;
+  constexpr bool kBMn = kMode == kHidden || kMode == kHead;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kStages * L::kStage);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* acc_full = empty + L::kStages;    // [2]
+  uint64_t* acc_empty = acc_full + 2;         // [2]
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = kPair == 2 ? cluster_cta_rank() : 0u;
+  const bool leader = rank == 0;
+  const int unit = static_cast<int>(blockIdx.x) / kPair;
+  const int num_units = static_cast<int>(gridDim.x) / kPair;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8 * kPair);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+  }
+  if (warp == 1) {
+    tmem_alloc_g<kPair>(tmem_slot, kTmemCols);
+    tmem_relinquish_g<kPair>();
+  }
+  tc_fence_before();
+  if (kPair == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  griddep_launch_dependents();
+  griddep_wait();   // every input may come from the kernel before
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      uint32_t stage = 0, phase = 0, filled = 0, last_parity = 0;
+      for (int tile = unit; tile < p.num_tiles; tile += num_units) {
+        const Tile t = tile_at(p, tile);
+        const int row_a = (t.mb * kPair + static_cast<int>(rank)) * kBM;
+        const int row_b = t.nb * kBN + static_cast<int>(rank) * (kBN / kPair);
+        for (int kt = t.kt0; kt < t.kt1; ++kt) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, &g_ce_error, kErrWaitEmpty)) goto producer_done;
+          {
+            uint8_t* sa = smem + stage * L::kStage;
+            uint8_t* sb = sa + L::kATile;
+            const uint32_t bar = kPair == 2 ? map_to_cta(smem_addr(&full[stage]), 0) : 0u;
+            if (leader) mbar_arrive_expect_tx(&full[stage], L::kStage * kPair);
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+              if constexpr (kPair == 2) tma_load_2d_pair(dst, map, bar, x, y);
+              else tma_load_2d(dst, map, &full[stage], x, y);
+            };
+            if constexpr (kAMn) {
+#pragma unroll
+              for (int c = 0; c < kBM / 64; ++c) load(sa + c * kChunk, &maps.a, row_a + 64 * c, kt * kBK);
+            } else {
+              load(sa, &maps.a, kt * kBK, row_a);
+            }
+            if constexpr (kBMn) {
+#pragma unroll
+              for (int c = 0; c < kBN / kPair / 64; ++c) load(sb + c * kChunk, &maps.b, row_b + 64 * c, kt * kBK);
+            } else {
+              load(sb, &maps.b, kt * kBK, row_b);
+            }
+          }
+          filled |= 1u << stage;
+          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == static_cast<uint32_t>(L::kStages)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    producer_done:
+      // Teardown: every copy armed on this CTA's barriers must have landed.
+      if (leader)
+        for (int s = 0; s < L::kStages; ++s)
+          if (filled & (1u << s)) {
+            int never = 0;
+            mbar_wait(&full[s], (last_parity >> s) & 1u, &never, &g_ce_error, kErrWaitDrain);
+          }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc = mma_idesc<kPair, kAMn, kBMn>();
+      uint32_t stage = 0, phase = 0, buf = 0, acc_phase = 0;
+      bool ok = true;
+      for (int tile = unit; tile < p.num_tiles && ok; tile += num_units) {
+        const Tile t = tile_at(p, tile);
+        if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, &g_ce_error, kErrWaitAccEmpty)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + buf * kBN;
+        for (int kt = t.kt0; kt < t.kt1; ++kt) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, &g_ce_error, kErrWaitFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint8_t* sa = smem + stage * L::kStage;
+          const uint64_t da = operand_desc<kAMn>(sa);
+          const uint64_t db = operand_desc<kBMn>(sa + L::kATile);
+#pragma unroll
+          for (uint32_t q = 0; q < kBK / 16; ++q)
+            mma_bf16_g<kPair>(acc, da + q * kDescStep<kAMn>, db + q * kDescStep<kBMn>, idesc,
+                              (kt != t.kt0 || q != 0) ? 1u : 0u);
+          tc_commit_g<kPair>(&empty[stage]);
+          if (++stage == static_cast<uint32_t>(L::kStages)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_g<kPair>(&acc_full[buf]);
+        buf ^= 1u;
+        if (buf == 0) acc_phase ^= 1u;
+      }
+      if (!ok) {
+        // Teardown after an abort: wait for the MMAs already issued.
+        tc_commit_g<kPair>(drain);
+        int never = 0;
+        mbar_wait(drain, 0, &never, &g_ce_error, kErrWaitDrain);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    // 8 warps: two per TMEM lane quadrant, each owning 128 of the 256 columns; a thread
+    // holds 128 columns of one row, so row reductions need no exchange between lanes.
+    const int quad = warp & 3;
+    const int half = (warp - 2) >> 2;
+    uint32_t buf = 0, acc_phase = 0;
+    float gmax = 0.f;
+    if constexpr (kMode != kLogits) gmax = *p.gmax;
+    for (int tile = unit; tile < p.num_tiles; tile += num_units) {
+      const Tile t = tile_at(p, tile);
+      const int row = (t.mb * kPair + static_cast<int>(rank)) * kBM + quad * 32 + lane;
+      const int col0 = t.nb * kBN + half * 128;
+      if (!mbar_wait(&acc_full[buf], acc_phase, abort_flag, &g_ce_error, kErrWaitAccFull, 2 * kWaitLimitNs)) break;
+      tc_fence_after();
+      __syncwarp();   // rows past the end leave the loop body early
+      uint32_t v[4][32];
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN + half * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_load_32x32b_x32(taddr + 32 * c, v[c]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair == 2) mbar_arrive_remote(map_to_cta(smem_addr(&acc_empty[buf]), 0));
+        else mbar_arrive(&acc_empty[buf]);
+      }
+      buf ^= 1u;
+      if (buf == 0) acc_phase ^= 1u;
+      if (row >= p.M) continue;
+
+      if constexpr (kMode == kLogits) {
+        const int64_t label = p.labels[row] - p.v0 - col0;   // position inside this thread's columns, if 0..127
+        const int cols = min(128, p.N - col0);               // may be <= 0 in the last column tile
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          const float z = __uint_as_float(v[i >> 5][i & 31]);
+          if (i < cols) m = fmaxf(m, z);
+        }
+        const float c = (m == -INFINITY ? 0.f : m) * kLog2e;
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          const float e = i < cols ? ex2(fmaf(__uint_as_float(v[i >> 5][i & 31]), kLog2e, -c)) : 0.f;
+          if ((i & 3) == 0) s0 += e;
+          else if ((i & 3) == 1) s1 += e;
+          else if ((i & 3) == 2) s2 += e;
+          else s3 += e;
+        }
+        // A part without columns (or of nothing but -inf) is (-inf, 0): it joins as nothing.
+        p.stats[static_cast<int64_t>(2 * t.nb + half) * p.M + row] =
+            make_float2(m == -INFINITY ? -INFINITY : c, (s0 + s1) + (s2 + s3));
+        if (label >= 0 && label < cols && label + p.v0 + col0 < p.vocab) {
+          float z = 0.f;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i == label) z = __uint_as_float(v[i >> 5][i & 31]);
+          p.target[row] = z;
+        }
+      } else if constexpr (kMode == kGrad) {
+        const int64_t label = p.labels[row];
+        const int64_t at = label - p.v0 - col0;
+        const bool counted = label != p.ignore;
+        float g = p.dloss[row];
+        g = gmax > 0.f ? g / gmax : g;          // gmax == 0: every finite entry is zero
+        if (label < 0 || label >= p.vocab) g = NAN;
+        const float l2 = p.lse[row] * kLog2e;
+        __nv_bfloat16* dst = p.dz + static_cast<int64_t>(row) * p.ld_dz + col0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float d[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = 8 * i + e;
+            float q = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), kLog2e, -l2));
+            if (k == at) q -= 1.f;
+            d[e] = counted ? q * g : 0.f;
+          }
+          if (col0 + 8 * i < p.N)
+            *reinterpret_cast<uint4*>(dst + 8 * i) =
+                make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+        }
+      } else if constexpr (kMode == kHidden) {
+        if (p.out == nullptr) {
+          float* dst = p.acc + (static_cast<int64_t>(t.split) * p.M + row) * p.N + col0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (col0 + 4 * i < p.N) {
+              float4 f = make_float4(__uint_as_float(v[i >> 3][(4 * i) & 31]), __uint_as_float(v[i >> 3][(4 * i + 1) & 31]),
+                                     __uint_as_float(v[i >> 3][(4 * i + 2) & 31]), __uint_as_float(v[i >> 3][(4 * i + 3) & 31]));
+              if (p.accumulate) {
+                const float4 o = *reinterpret_cast<const float4*>(dst + 4 * i);
+                f.x += o.x;
+                f.y += o.y;
+                f.z += o.z;
+                f.w += o.w;
+              }
+              *reinterpret_cast<float4*>(dst + 4 * i) = f;
+            }
+          }
+        }
+      }
+      if constexpr (kMode == kHidden || kMode == kHead) {
+        if (kMode == kHead || p.out != nullptr) {
+          __nv_bfloat16* dst = p.out + static_cast<int64_t>(row) * p.N + col0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (col0 + 8 * i < p.N) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int k = 8 * i + 2 * e;
+                w[e] = pack_bf16(__uint_as_float(v[k >> 5][k & 31]) * gmax, __uint_as_float(v[(k + 1) >> 5][(k + 1) & 31]) * gmax);
+              }
+              *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  if (kPair == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_g<kPair>(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of each row: C = max c, lse = C ln 2 + log sum s 2^(c - C).  One block per
+// 32 rows, 32 strands over the parts; the last steps in double, so that a loss that is a
+// small difference of large logits keeps the precision of the fp32 logits.
+__global__ void __launch_bounds__(1024) rfq_ce_join_kernel(const float2* stats, const float* target, const int64_t* labels,
+                                                           int M, int parts, int64_t ignore, int64_t vocab, float* loss,
+                                                           float* lse) {
+  __shared__ float sc[32][33], ss[32][33];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x, strand = threadIdx.y;
+  const int row = blockIdx.x * 32 + lane;
+  float c = -INFINITY, s = 0.f;
+  if (row < M) {
+#pragma unroll 4
+    for (int k = strand; k < parts; k += 32) {
+      const float2 q = stats[static_cast<int64_t>(k) * M + row];
+      const float top = fmaxf(c, q.x);
+      const float base = top == -INFINITY ? 0.f : top;
+      s = s * ex2(c - base) + q.y * ex2(q.x - base);
+      c = top;
+    }
+  }
+  sc[strand][lane] = c;
+  ss[strand][lane] = s;
+  __syncthreads();
+  if (strand == 0 && row < M) {
+    float top = -INFINITY;
+    for (int k = 0; k < 32; ++k) top = fmaxf(top, sc[k][lane]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    for (int k = 0; k < 32; ++k) sum += ss[k][lane] * ex2(sc[k][lane] - base);
+    const double l = static_cast<double>(base) * 0.69314718055994530942 + log(static_cast<double>(sum));
+    lse[row] = static_cast<float>(l);
+    const int64_t label = labels[row];
+    float out = 0.f;
+    if (label != ignore)
+      out = label >= 0 && label < vocab ? static_cast<float>(l - static_cast<double>(target[row])) : NAN;
+    loss[row] = out;
+  }
+}
+
+// gmax = largest finite |dloss| over the rows that count (one block).
+__global__ void __launch_bounds__(1024) rfq_ce_gmax_kernel(const float* dloss, const int64_t* labels, int M, int64_t ignore,
+                                                           float* gmax) {
+  __shared__ float part[32];
+  griddep_launch_dependents();
+  griddep_wait();
+  float m = 0.f;
+  for (int i = threadIdx.x; i < M; i += 1024) {
+    const float g = fabsf(dloss[i]);
+    if (labels[i] != ignore && g <= 3.402823466e38f) m = fmaxf(m, g);
+  }
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    m = part[threadIdx.x];
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (threadIdx.x == 0) *gmax = m;
+  }
+}
+
+// dh = gmax * sum over the splits of the fp32 sums, in order.
+__global__ void __launch_bounds__(256) rfq_ce_hidden_kernel(const float* acc, int splits, int64_t n4, const float* gmax,
+                                                            __nv_bfloat16* dh) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const float g = *gmax;
+  const float4* src = reinterpret_cast<const float4*>(acc);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n4; i += static_cast<int64_t>(gridDim.x) * 256) {
+    float4 f = src[i];
+    for (int s = 1; s < splits; ++s) {
+      const float4 o = src[s * n4 + i];
+      f.x += o.x;
+      f.y += o.y;
+      f.z += o.z;
+      f.w += o.w;
+    }
+    reinterpret_cast<uint2*>(dh)[i] = make_uint2(pack_bf16(f.x * g, f.y * g), pack_bf16(f.z * g, f.w * g));
+  }
+}
+
+template <class Kernel, class... Args>
+cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see griddep_wait()
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int kPair, int kMode>
+cudaError_t launch_mode(const Maps& maps, Params p, int splits, int num_sms, cudaStream_t stream) {
+  using L = Layout<kPair>;
+  auto kernel = rfq_ce_kernel<kPair, kMode>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  p.num_mb = static_cast<int>(ceil_div(p.M, kBM * kPair));
+  p.num_nb = static_cast<int>(ceil_div(p.N, kBN));
+  p.group = 16;
+  p.num_tiles = p.num_mb * p.num_nb * splits;
+  int units = num_sms / kPair;
+  if (units > p.num_tiles) units = p.num_tiles;
+  return launch_pdl(kernel, dim3(units * kPair), dim3(kThreads), L::kSmem, kPair, stream, maps, p);
+}
+
+// A [M] x B [N] product over K; a_ld / b_ld: elements between the rows of the matrix in memory.
+template <int kMode>
+cudaError_t product(EncodeTiledFn encode, const void* a, int64_t a_ld, const void* b, int64_t b_ld, int64_t M, int64_t N,
+                    int64_t K, int splits, Params p, int num_sms, cudaStream_t stream) {
+  constexpr bool kAMn = kMode == kHead;
+  constexpr bool kBMn = kMode == kHidden || kMode == kHead;
+  const bool pair = M > kBM;
+  Maps maps;
+  const bool ok = (kAMn ? encode_bf16_map(encode, &maps.a, a, K, M, a_ld, kBK) : encode_bf16_map(encode, &maps.a, a, M, K, a_ld, kBM)) &&
+                  (kBMn ? encode_bf16_map(encode, &maps.b, b, K, N, b_ld, kBK)
+                        : encode_bf16_map(encode, &maps.b, b, N, K, b_ld, pair ? kBN / 2 : kBN));
+  if (!ok) return cudaErrorInvalidValue;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.num_kt = static_cast<int>(ceil_div(K, kBK));
+  p.kt_per_split = static_cast<int>(ceil_div(p.num_kt, splits));
+  splits = static_cast<int>(ceil_div(p.num_kt, p.kt_per_split));   // a short last piece may fill fewer
+  return pair ? launch_mode<2, kMode>(maps, p, splits, num_sms, stream) : launch_mode<1, kMode>(maps, p, splits, num_sms, stream);
+}
+
+constexpr int64_t kForwardRows = 32768;            // rows of one forward pass (bounds the statistics)
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+constexpr int64_t kMinPiece = 2048;
+constexpr int kPlanSms = 148;                      // the cut does not depend on the device that runs it
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// How the backward pass is cut: vocabulary entries per piece, splits of the dh product, and
+// the offsets of the workspace's parts.
+struct Plan {
+  int64_t piece, pieces, ld_dz;
+  int splits;
+  bool direct;        // dh straight from the product (one piece, one split)
+  size_t off_acc, off_gmax, bytes;
+};
+
+Plan plan_backward(int64_t T, int64_t D, int64_t V, bool want_dh) {
+  Plan q;
+  q.piece = kPieceBytes / 2 / T / kBN * kBN;
+  if (q.piece < kMinPiece) q.piece = kMinPiece;
+  q.pieces = ceil_div(V, q.piece);
+  if (q.pieces == 1) q.piece = V;
+  else q.piece = ceil_div(ceil_div(V, q.pieces), kBN) * kBN;      // even pieces
+  q.pieces = ceil_div(V, q.piece);
+  q.ld_dz = (q.piece + 7) / 8 * 8;
+  // Splits of the dh product's contraction (the piece): the number that leaves the fewest
+  // k-tiles in the longest chain of one CTA (or pair), each tile charged 4 for its epilogue.
+  const int pair = T > kBM ? 2 : 1;
+  const int64_t tiles = ceil_div(T, kBM * pair) * ceil_div(D, kBN), units = kPlanSms / pair;
+  const int64_t kt = ceil_div(q.piece, kBK);
+  int64_t best = INT64_MAX;
+  q.splits = 1;
+  for (int s = 1; s <= 32 && s <= kt; ++s) {
+    const int64_t per = ceil_div(kt, s);
+    if (ceil_div(kt, per) != s) continue;
+    const int64_t cost = ceil_div(tiles * s, units) * (per + 4);
+    if (cost < best) {
+      best = cost;
+      q.splits = s;
+    }
+  }
+  q.direct = q.pieces == 1 && q.splits == 1;
+  size_t at = align256(static_cast<size_t>(T) * q.ld_dz * 2);
+  q.off_acc = at;
+  if (want_dh && !q.direct) at += align256(static_cast<size_t>(q.splits) * T * D * 4);
+  q.off_gmax = at;
+  q.bytes = at + 256;
+  return q;
+}
+
+}  // namespace
+
+size_t ce_forward_workspace(int64_t T, int64_t V) {
+  const int64_t rows = T < kForwardRows ? T : kForwardRows;
+  return align256(static_cast<size_t>(2 * ceil_div(V, kBN)) * rows * sizeof(float2)) + align256(static_cast<size_t>(rows) * 4);
+}
+
+size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh) {
+  return plan_backward(T, D, V, want_dh).bytes;
+}
+
+cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
+                              int64_t ignore, float* loss, float* lse, void* ws, int num_sms, void* encode_tiled,
+                              cudaStream_t stream) {
+  EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
+  const int parts = static_cast<int>(2 * ceil_div(V, kBN));
+  for (int64_t t0 = 0; t0 < T; t0 += kForwardRows) {
+    const int64_t rows = T - t0 < kForwardRows ? T - t0 : kForwardRows;
+    Params p = {};
+    p.labels = labels + t0;
+    p.ignore = ignore;
+    p.vocab = V;
+    p.stats = static_cast<float2*>(ws);
+    p.target = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(parts) * rows * sizeof(float2)));
+    cudaError_t e = product<kLogits>(encode, static_cast<const __nv_bfloat16*>(h) + t0 * D, D, w, D, rows, V, D, 1, p, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(rfq_ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 32))), dim3(32, 32), 0, 1, stream,
+                   static_cast<const float2*>(p.stats), static_cast<const float*>(p.target), p.labels, static_cast<int>(rows),
+                   parts, ignore, V, loss + t0, lse + t0);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labels, const float* lse, const float* dloss,
+                               int64_t T, int64_t D, int64_t V, int64_t ignore, void* dh, void* dw, void* ws, int num_sms,
+                               void* encode_tiled, cudaStream_t stream) {
+  EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
+  const Plan q = plan_backward(T, D, V, dh != nullptr);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
+  float* acc = reinterpret_cast<float*>(base + q.off_acc);
+  float* gmax = reinterpret_cast<float*>(base + q.off_gmax);
+  cudaError_t e = launch_pdl(rfq_ce_gmax_kernel, dim3(1), dim3(1024), 0, 1, stream, dloss, labels, static_cast<int>(T), ignore, gmax);
+  for (int64_t v0 = 0; v0 < V && e == cudaSuccess; v0 += q.piece) {
+    const int64_t n = V - v0 < q.piece ? V - v0 : q.piece;
+    const __nv_bfloat16* wp = static_cast<const __nv_bfloat16*>(w) + v0 * D;
+    Params p = {};
+    p.labels = labels;
+    p.ignore = ignore;
+    p.vocab = V;
+    p.v0 = v0;
+    p.lse = lse;
+    p.dloss = dloss;
+    p.gmax = gmax;
+    p.dz = dz;
+    p.ld_dz = q.ld_dz;
+    e = product<kGrad>(encode, h, D, wp, D, T, n, D, 1, p, num_sms, stream);
+    if (e == cudaSuccess && dh != nullptr) {
+      p.acc = acc;
+      p.accumulate = v0 > 0;
+      p.out = q.direct ? static_cast<__nv_bfloat16*>(dh) : nullptr;
+      e = product<kHidden>(encode, dz, q.ld_dz, wp, D, T, D, n, q.splits, p, num_sms, stream);
+    }
+    if (e == cudaSuccess && dw != nullptr) {
+      p.out = static_cast<__nv_bfloat16*>(dw) + v0 * D;
+      e = product<kHead>(encode, dz, q.ld_dz, h, D, n, D, T, 1, p, num_sms, stream);
+    }
+  }
+  if (e == cudaSuccess && dh != nullptr && !q.direct) {
+    const int64_t n4 = T * D / 4;
+    const int64_t blocks = ceil_div(n4, 256) < 8 * num_sms ? ceil_div(n4, 256) : 8 * num_sms;
+    e = launch_pdl(rfq_ce_hidden_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, stream, static_cast<const float*>(acc),
+                   q.splits, n4, static_cast<const float*>(gmax), static_cast<__nv_bfloat16*>(dh));
+  }
+  return e;
+}
+
+cudaError_t read_and_clear_ce_error(unsigned int* value) {
+  unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_ce_error, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_ce_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace rfq

@@ -58,9 +58,20 @@ cudaError_t launch_gemm_mxfp8(const void* qx_codes, const void* qx_scales, const
 cudaError_t launch_mma_rate_probe(int variant, int iters, unsigned long long* cycles, int max_clusters,
                                   int* clusters_used, cudaStream_t stream);
 
-// Read and clear the device error words (GEMM and quantizer) of the current device.
+// Softmax cross entropy at the output head (rfq_ce.cu).  dh / dw may be nullptr.
+size_t ce_forward_workspace(int64_t T, int64_t V);
+size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh);
+cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
+                              int64_t ignore, float* loss, float* lse, void* ws, int num_sms, void* encode_tiled,
+                              cudaStream_t stream);
+cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labels, const float* lse, const float* dloss,
+                               int64_t T, int64_t D, int64_t V, int64_t ignore, void* dh, void* dw, void* ws, int num_sms,
+                               void* encode_tiled, cudaStream_t stream);
+
+// Read and clear the device error words (GEMM, quantizer, fused layer, output head) of the current device.
 cudaError_t read_and_clear_device_error(unsigned int* value);
 cudaError_t read_and_clear_quant_error(unsigned int* value);
 cudaError_t read_and_clear_fused_error(unsigned int* value);
+cudaError_t read_and_clear_ce_error(unsigned int* value);
 
 }  // namespace rfq

@@ -370,6 +370,27 @@ __device__ __forceinline__ void mma_mxf8_g(uint32_t d_tmem, uint64_t adesc, uint
     mma_mxf8(d_tmem, adesc, bdesc, idesc, sfa_tmem, sfb_tmem, accumulate);
 }
 
+// D[tmem] (+)= A[smem] x B[smem]^T of bf16 operands, fp32 accumulator (kind::f16,
+// K = 16 per instruction).
+template <int kPair>
+__device__ __forceinline__ void mma_bf16_g(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if constexpr (kPair == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrive once on `bar` (same offset) in every CTA of the pair when the tcgen05
 // operations issued so far by this thread have completed.
 template <int kPair>

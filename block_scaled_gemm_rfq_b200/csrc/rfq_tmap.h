@@ -49,4 +49,18 @@ inline bool encode_scales_map(EncodeTiledFn encode, CUtensorMap* map, const void
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D map over a row-major bf16 matrix [rows][cols] with `ld` elements between rows
+// (a multiple of 8); box = 64 elements (128 bytes) x box_rows rows, 128-byte swizzle,
+// zero fill outside.
+inline bool encode_bf16_map(EncodeTiledFn encode, CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
+                            int64_t ld, uint32_t box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {64u, box_rows};
+  cuuint32_t elem_strides[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace rfq

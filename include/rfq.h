@@ -316,6 +316,49 @@ rfq_status_t rfq_gemm_mxfp8(const void* qx_codes, const void* qx_scales,
                             void* y, rfq_out_t y_type, cudaStream_t stream);
 
 /*
+ * Softmax cross entropy at the output head, without the logits (training and scoring; the
+ * paper has no counterpart).  z = h . w^T is the projection of T hidden states to V
+ * vocabulary entries, one label per row:
+ *
+ *     lse[t] = log sum_v exp z[t][v]        loss[t] = lse[t] - z[t][labels[t]]
+ *
+ * and for the gradient dloss[t] of loss[t]
+ *
+ *     dz[t][v] = dloss[t] (exp(z[t][v] - lse[t]) - [v == labels[t]]),  dh = dz . w,  dw = dz^T . h
+ *
+ * No [T][V] array is kept: the logits of a tile live in tensor memory and dz exists for one
+ * piece of the vocabulary at a time, in the workspace.
+ *
+ *   h_bf16   [T][D], w_bf16 [V][D]: bf16, 16-byte aligned; D a multiple of 8, 8..65536;
+ *            0 <= T <= 2^24, 1 <= V <= 2^24
+ *   labels   [T] int64.  A row whose label is ignore_index has loss 0 and gives no gradient
+ *            (its lse is written).  Any other label outside [0, V) is an error of the
+ *            caller's: its loss is NaN, and so are its gradients.
+ *   loss, lse, dloss   [T] fp32.  loss is per row: a mean or sum over the rows is the
+ *            caller's, as dloss (e.g. 1 / counted rows).  Rows of dloss whose label is
+ *            ignore_index are not looked at.
+ *   dh_bf16  [T][D], dw_bf16 [V][D]: bf16, 16-byte aligned, fully overwritten; either may be
+ *            NULL (a frozen head, or scoring).
+ *   workspace   rfq_linear_ce_workspace_bytes(T, D, V, want_dh, want_dw) bytes, 256-byte
+ *            aligned (want_* nonzero for the gradients that rfq_linear_ce_backward will be
+ *            asked for; both zero: the forward pass alone).  Nothing in it is carried from
+ *            one call to the next.
+ * Logits are fp32 sums of exact products; the row maximum and sum are fp32, their last
+ * join fp64.  dz is rounded to bf16 relative to the largest |dloss| (so a constant dloss
+ * costs no rounding) and both gradients are fp32 sums rounded once to bf16.  A row with a
+ * non-finite logit other than -inf has a non-finite loss.  T == 0 launches nothing, except
+ * that dw is then zeroed.  Results do not depend on timing: no atomics.
+ */
+size_t rfq_linear_ce_workspace_bytes(int64_t T, int64_t D, int64_t V, int want_dh, int want_dw);
+rfq_status_t rfq_linear_ce(const void* h_bf16, const void* w_bf16, const int64_t* labels, int64_t T, int64_t D,
+                           int64_t V, int64_t ignore_index, float* loss, float* lse, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, const int64_t* labels, const float* lse,
+                                    const float* dloss, int64_t T, int64_t D, int64_t V, int64_t ignore_index,
+                                    void* dh_bf16, void* dw_bf16, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/*
  * rfq_mma_rate_probe -- measurement support (no counterpart in the paper): the rate
  * at which this GPU's tensor cores retire the MMA instructions rfq_gemm issues,
  * with the operands resident in shared memory (no loads, no epilogue).  It is the
@@ -353,7 +396,8 @@ rfq_status_t rfq_mma_rate_probe(int variant, int64_t iterations, unsigned long l
  * load, 2 free stage, 3 accumulator ready, 4 accumulator free, 5 teardown;
  * 6 a wait of the quantizer for its TMA load; the same codes 1, 2, 3, 5 for
  * the corresponding waits of rfq_linear_fused, and 7 its quantizer warps
- * waiting for a staged tile of X).
+ * waiting for a staged tile of X; 1..5 also for those waits of rfq_linear_ce and its
+ * backward).
  */
 rfq_status_t rfq_check_device_error(cudaStream_t stream, int* detail);
 
