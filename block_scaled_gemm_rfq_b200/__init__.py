@@ -26,6 +26,8 @@ __all__ = [
     "QuantizedTensor", "quantize_mxfp4_alloc", "quantize_weight_alloc", "gemm_alloc", "linear_alloc",
     "EXPORTED_SYMBOLS", "OUT_F32", "OUT_BF16", "mma_rate_probe", "MMA_PROBE_MAX_ITERATIONS",
     "linear_ce_workspace_bytes", "linear_ce", "linear_ce_backward", "linear_ce_alloc", "linear_ce_backward_alloc",
+    "lora_workspace_bytes", "lora", "lora_backward", "lora_alloc", "lora_backward_alloc", "linear_lora_workspace_bytes",
+    "linear_lora", "linear_lora_alloc", "LORA_MAX_RANK", "LORA_MAX_ADAPTERS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +49,7 @@ EXPORTED_SYMBOLS = (
     "rfq_gemm_yt", "rfq_linear_dgrad", "rfq_linear_wgrad_workspace_bytes", "rfq_linear_wgrad",
     "rfq_mxfp8_codes_bytes", "rfq_quantize_mxfp8", "rfq_gemm_mxfp8", "rfq_mma_rate_probe",
     "rfq_linear_ce_workspace_bytes", "rfq_linear_ce", "rfq_linear_ce_backward",
+    "rfq_lora_workspace_bytes", "rfq_lora", "rfq_lora_backward", "rfq_linear_lora_workspace_bytes", "rfq_linear_lora",
 )
 
 # Largest iteration count of the tensor-core rate probe (RFQ_MMA_PROBE_MAX_ITERATIONS).
@@ -54,6 +57,10 @@ MMA_PROBE_MAX_ITERATIONS = 100000
 
 # Size of the library's fixed scratch array (RFQ_STATIC_WORKSPACE_BYTES in include/rfq.h).
 STATIC_WORKSPACE_BYTES = 32 << 20
+
+# Limits of the adapters (RFQ_LORA_MAX_RANK, RFQ_LORA_MAX_ADAPTERS in include/rfq.h).
+LORA_MAX_RANK = 128
+LORA_MAX_ADAPTERS = 4096
 
 # Largest M of the single-kernel linear layer (RFQ_FUSED_MAX_M in include/rfq.h).
 FUSED_MAX_M = 64
@@ -107,6 +114,11 @@ def load_library():
                 "rfq_linear_ce_workspace_bytes": (SZ, [I64, I64, I64, I, I]),
                 "rfq_linear_ce": (I, [P, P, P, I64, I64, I64, I64, P, P, P, SZ, P]),
                 "rfq_linear_ce_backward": (I, [P, P, P, P, P, I64, I64, I64, I64, P, P, P, SZ, P]),
+                "rfq_lora_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I]),
+                "rfq_lora": (I, [P, I64, I64, P, P, P, P, I64, I64, I64, P, P, I, P, P, SZ, P]),
+                "rfq_lora_backward": (I, [P, I64, I64, P, P, P, P, I64, I64, I64, P, P, P, P, I, P, P, I, P, SZ, P]),
+                "rfq_linear_lora_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I]),
+                "rfq_linear_lora": (I, [P, I64, I64, P, P, I64, P, P, P, P, I64, I64, P, I, I, P, P, SZ, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(lib, name)
@@ -368,6 +380,113 @@ def linear_ce_backward(h, w, labels, lse, dloss, dh, dw, workspace, ignore_index
             _ptr(dh), _ptr(dw), workspace.data_ptr(), workspace.numel(), st), "rfq_linear_ce_backward")
 
 
+def lora_workspace_bytes(M: int, K: int, N: int, rank: int, n_adapters: int, backward: bool = False) -> int:
+    """rfq_lora_workspace_bytes: workspace of rfq_lora and, where `backward`, of rfq_lora_backward too."""
+    return int(load_library().rfq_lora_workspace_bytes(M, K, N, rank, n_adapters, int(bool(backward))))
+
+
+def linear_lora_workspace_bytes(M: int, K: int, N: int, rank: int, n_adapters: int, use_residual: bool = True) -> int:
+    """rfq_linear_lora_workspace_bytes: workspace of rfq_linear_lora."""
+    return int(load_library().rfq_linear_lora_workspace_bytes(M, K, N, rank, n_adapters, int(bool(use_residual))))
+
+
+def _lora_shapes(where, x, a, b, scale, ids, M, K):
+    """(n, rank, N) of the adapters, after checking the tensors that every adapter call takes."""
+    import torch
+    n, r, _ = a.shape
+    N = b.shape[1]
+    dev = a.device
+    if x is not None:
+        _need(f"{where}: x", x, (M, K), torch.bfloat16, dev)
+    _need(f"{where}: a", a, (n, r, K), torch.bfloat16, dev)
+    _need(f"{where}: b", b, (n, N, r), torch.bfloat16, dev)
+    _need(f"{where}: scale", scale, (n,), torch.float32, dev)
+    _need(f"{where}: ids", ids, (M,), torch.int32, dev)
+    return n, r, N
+
+
+def _out_type(where, t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return OUT_BF16
+    if t.dtype == torch.float32:
+        return OUT_F32
+    raise RFQError(1, f"{where}: want bfloat16 or float32, got {t.dtype}")
+
+
+def lora(x, a, b, scale, ids, y, workspace, base=None, hidden=None, stream=None):
+    """rfq_lora: y [M, N] = base + the adapters' share of every row; a [n, rank, K], b [n, N, rank] bf16,
+    scale [n] fp32, ids [M] int32 (outside [0, n): no adapter).  base may be None (zeros) or y; hidden
+    [M, rank] fp32 receives what the backward pass needs for b's gradient."""
+    import torch
+    M, K = x.shape
+    dev = x.device
+    n, r, N = _lora_shapes("rfq_lora", x, a, b, scale, ids, M, K)
+    y_type = _out_type("rfq_lora: y", y)
+    _need("rfq_lora: y", y, (M, N), y.dtype, dev)
+    if base is not None:
+        _need("rfq_lora: base", base, (M, N), y.dtype, dev)
+    if hidden is not None:
+        _need("rfq_lora: hidden", hidden, (M, r), torch.float32, dev)
+    _need_workspace("rfq_lora", workspace, dev)
+    with _On(dev, stream) as st:
+        _check(load_library().rfq_lora(x.data_ptr(), M, K, a.data_ptr(), b.data_ptr(), scale.data_ptr(), ids.data_ptr(),
+                                       n, r, N, _ptr(base), y.data_ptr(), y_type, _ptr(hidden), workspace.data_ptr(),
+                                       workspace.numel(), st), "rfq_lora")
+
+
+def lora_backward(x, a, b, scale, ids, dy, hidden, workspace, dx=None, dx_base=None, da=None, db=None, stream=None):
+    """rfq_lora_backward: dx [M, K] = dx_base + the adapters' share, da [n, rank, K], db [n, N, rank]; any of
+    the three may be None (da and db have one dtype).  x may be None without da, hidden without db."""
+    import torch
+    M, N_dy = dy.shape
+    K = a.shape[2]
+    dev = dy.device
+    where = "rfq_lora_backward"
+    n, r, N = _lora_shapes(where, x, a, b, scale, ids, M, K)
+    _need(f"{where}: dy", dy, (M, N), torch.bfloat16, a.device)
+    if hidden is not None:
+        _need(f"{where}: hidden", hidden, (M, r), torch.float32, dev)
+    dx_type = grad_type = OUT_F32
+    if dx is not None:
+        dx_type = _out_type(f"{where}: dx", dx)
+        _need(f"{where}: dx", dx, (M, K), dx.dtype, dev)
+        if dx_base is not None:
+            _need(f"{where}: dx_base", dx_base, (M, K), dx.dtype, dev)
+    for name, t, shape in (("da", da, (n, r, K)), ("db", db, (n, N, r))):
+        if t is not None:
+            grad_type = _out_type(f"{where}: {name}", t)
+            _need(f"{where}: {name}", t, shape, t.dtype if name == "da" or da is None else da.dtype, dev)
+    _need_workspace(where, workspace, dev)
+    with _On(dev, stream) as st:
+        _check(load_library().rfq_lora_backward(
+            _ptr(x), M, K, a.data_ptr(), b.data_ptr(), scale.data_ptr(), ids.data_ptr(), n, r, N, dy.data_ptr(), _ptr(hidden),
+            _ptr(dx_base), _ptr(dx), dx_type, _ptr(da), _ptr(db), grad_type, workspace.data_ptr(), workspace.numel(), st),
+            "rfq_lora_backward")
+
+
+def linear_lora(x, qw_codes, qw_scales, N, a, b, scale, ids, y, workspace, use_residual=True, hidden=None, stream=None):
+    """rfq_linear_lora: rfq_linear of x against the pre-quantized weight, with every row's adapter added (see `lora`)."""
+    import torch
+    M, K = x.shape
+    dev = x.device
+    n, r, Nb = _lora_shapes("rfq_linear_lora", x, a, b, scale, ids, M, K)
+    y_type = _out_type("rfq_linear_lora: y", y)
+    _need("rfq_linear_lora: b", b, (n, N, r), torch.bfloat16, dev)
+    _need("rfq_linear_lora: y", y, (M, N), y.dtype, dev)
+    for name, t, size in (("qw_codes", qw_codes, codes_bytes(N, K)), ("qw_scales", qw_scales, scales_bytes(N, K))):
+        if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != dev or t.numel() < size:
+            raise RFQError(1, f"rfq_linear_lora: {name} is a contiguous uint8 tensor of at least {size} bytes on {dev}")
+    if hidden is not None:
+        _need("rfq_linear_lora: hidden", hidden, (M, r), torch.float32, dev)
+    _need_workspace("rfq_linear_lora", workspace, dev)
+    with _On(dev, stream) as st:
+        _check(load_library().rfq_linear_lora(
+            x.data_ptr(), M, K, qw_codes.data_ptr(), qw_scales.data_ptr(), N, a.data_ptr(), b.data_ptr(), scale.data_ptr(),
+            ids.data_ptr(), n, r, y.data_ptr(), y_type, int(bool(use_residual)), _ptr(hidden), workspace.data_ptr(),
+            workspace.numel(), st), "rfq_linear_lora")
+
+
 def check_device_error(stream=None):
     """Synchronize and report a bounded-wait timeout inside a kernel (raises RFQError)."""
     detail = ctypes.c_int(0)
@@ -536,3 +655,50 @@ def linear_ce_backward_alloc(h, w, labels, lse, dloss, want_dh=True, want_dw=Tru
         ws = _empty_u8(linear_ce_workspace_bytes(T, D, w.shape[0], want_dh, want_dw), h.device)
     linear_ce_backward(h, w, labels, lse, dloss, dh, dw, ws, ignore_index, stream)
     return dh, dw
+
+
+def lora_alloc(x, a, b, scale, ids, base=None, out_dtype=None, want_hidden=False, stream=None):
+    """rfq_lora into a new [M, N] tensor (base's type, else bf16 unless `out_dtype`); with `want_hidden`
+    returns (y, hidden)."""
+    import torch
+    M, K = x.shape
+    n, r, _ = a.shape
+    N = b.shape[1]
+    with _torch_stream(stream, x.device):
+        y = torch.empty((M, N), dtype=base.dtype if base is not None else out_dtype or torch.bfloat16, device=x.device)
+        hidden = torch.empty((M, r), dtype=torch.float32, device=x.device) if want_hidden else None
+        ws = _empty_u8(lora_workspace_bytes(M, K, N, r, n), x.device)
+    lora(x, a, b, scale, ids, y, ws, base, hidden, stream)
+    return (y, hidden) if want_hidden else y
+
+
+def lora_backward_alloc(x, a, b, scale, ids, dy, hidden, dx_base=None, want_dx=True, want_da=True, want_db=True,
+                        dx_dtype=None, grad_dtype=None, stream=None):
+    """rfq_lora_backward into new tensors: (dx, da, db), None in the place of what is not wanted; bf16
+    unless `dx_dtype` (or dx_base's type) and `grad_dtype`."""
+    import torch
+    M = dy.shape[0]
+    n, r, K = a.shape
+    N = b.shape[1]
+    dx_dtype = dx_base.dtype if dx_base is not None else dx_dtype or torch.bfloat16
+    with _torch_stream(stream, dy.device):
+        dx = torch.empty((M, K), dtype=dx_dtype, device=dy.device) if want_dx else None
+        da = torch.empty((n, r, K), dtype=grad_dtype or torch.bfloat16, device=dy.device) if want_da else None
+        db = torch.empty((n, N, r), dtype=grad_dtype or torch.bfloat16, device=dy.device) if want_db else None
+        ws = _empty_u8(lora_workspace_bytes(M, K, N, r, n, backward=True), dy.device)
+    lora_backward(x, a, b, scale, ids, dy, hidden, ws, dx, dx_base if want_dx else None, da, db, stream)
+    return dx, da, db
+
+
+def linear_lora_alloc(x, qw: QuantizedTensor, a, b, scale, ids, out_dtype=None, use_residual=True, want_hidden=False,
+                      stream=None):
+    """rfq_linear_lora into a new [M, qw.rows] tensor (bf16 unless `out_dtype`); with `want_hidden` returns (y, hidden)."""
+    import torch
+    M, K = x.shape
+    n, r, _ = a.shape
+    with _torch_stream(stream, x.device):
+        y = torch.empty((M, qw.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
+        hidden = torch.empty((M, r), dtype=torch.float32, device=x.device) if want_hidden else None
+        ws = _empty_u8(linear_lora_workspace_bytes(M, K, qw.rows, r, n, use_residual), x.device)
+    linear_lora(x, qw.codes, qw.scales, qw.rows, a, b, scale, ids, y, ws, use_residual, hidden, stream)
+    return (y, hidden) if want_hidden else y

@@ -191,6 +191,15 @@ rfq_status_t check_workspace(const void* workspace, size_t bytes, size_t need) {
   return aligned_to(workspace, 256) ? RFQ_OK : RFQ_ERR_MISALIGNED;
 }
 
+// Adapters: ranks 8..128 in steps of 8, up to 4096 adapters, up to 2^24 rows and 2^20 columns.
+bool lora_shape_ok(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n) {
+  constexpr int64_t kMaxRows = int64_t(1) << 24, kMaxCols = int64_t(1) << 20;
+  return M <= kMaxRows && K >= 8 && K <= kMaxCols && (K % 8) == 0 && N >= 8 && N <= kMaxCols && (N % 8) == 0 && rank >= 8 &&
+         rank <= RFQ_LORA_MAX_RANK && (rank % 8) == 0 && n >= 1 && n <= RFQ_LORA_MAX_ADAPTERS;
+}
+
+bool out_type_ok(rfq_out_t t) { return t == RFQ_OUT_F32 || t == RFQ_OUT_BF16; }
+
 }  // namespace
 
 extern "C" {
@@ -405,6 +414,92 @@ rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, cons
   if ((st = current_device(&sms)) != RFQ_OK) return st;
   return from_cuda(rfq::launch_ce_backward(h_bf16, w_bf16, labels, lse, dloss, T, D, V, ignore_index, dh_bf16, dw_bf16,
                                            workspace, sms, g_encode_tiled, stream));
+}
+
+size_t rfq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n_adapters, int backward) {
+  if (M <= 0 || !lora_shape_ok(M, K, N, rank, n_adapters)) return 0;
+  const size_t f = rfq::lora_forward_workspace(M, K, rank, n_adapters);
+  const size_t b = backward ? rfq::lora_backward_workspace(M, K, N, rank, n_adapters) : 0;
+  return f > b ? f : b;
+}
+
+rfq_status_t rfq_lora(const void* x_bf16, int64_t M, int64_t K, const void* a_bf16, const void* b_bf16, const float* scale,
+                      const int32_t* ids, int64_t n_adapters, int64_t rank, int64_t N, const void* base, void* y,
+                      rfq_out_t y_type, float* hidden, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (M < 0 || K < 0 || N < 0 || rank < 0 || n_adapters < 0) return RFQ_ERR_INVALID_ARG;
+  if (!out_type_ok(y_type)) return RFQ_ERR_INVALID_ARG;
+  if (!lora_shape_ok(M, K, N, rank, n_adapters)) return RFQ_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return RFQ_OK;
+  if (!x_bf16 || !a_bf16 || !b_bf16 || !scale || !ids || !y) return RFQ_ERR_INVALID_ARG;
+  if (!aligned16(x_bf16) || !aligned16(a_bf16) || !aligned16(b_bf16) || !aligned_to(scale, 4) || !aligned_to(ids, 4) ||
+      !aligned16(base) || !aligned16(y) || !aligned_to(hidden, 4))
+    return RFQ_ERR_MISALIGNED;
+  rfq_status_t st = check_workspace(workspace, workspace_bytes, rfq::lora_forward_workspace(M, K, rank, n_adapters));
+  if (st != RFQ_OK) return st;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RFQ_OK) return st;
+  return from_cuda(rfq::launch_lora_forward(x_bf16, a_bf16, b_bf16, scale, ids, base, y, y_type == RFQ_OUT_BF16, hidden, M, K, N,
+                                            rank, n_adapters, workspace, stream));
+}
+
+rfq_status_t rfq_lora_backward(const void* x_bf16, int64_t M, int64_t K, const void* a_bf16, const void* b_bf16,
+                               const float* scale, const int32_t* ids, int64_t n_adapters, int64_t rank, int64_t N,
+                               const void* dy_bf16, const float* hidden, const void* dx_base, void* dx, rfq_out_t dx_type,
+                               void* da, void* db, rfq_out_t grad_type, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
+  if (M < 0 || K < 0 || N < 0 || rank < 0 || n_adapters < 0) return RFQ_ERR_INVALID_ARG;
+  if (!out_type_ok(dx_type) || !out_type_ok(grad_type)) return RFQ_ERR_INVALID_ARG;
+  if (!lora_shape_ok(M, K, N, rank, n_adapters)) return RFQ_ERR_UNSUPPORTED_SHAPE;
+  if (!dx && !da && !db) return RFQ_OK;
+  if (!aligned16(dx) || !aligned16(da) || !aligned16(db) || !aligned16(dx_base)) return RFQ_ERR_MISALIGNED;
+  int sms = 0;
+  rfq_status_t st;
+  if (M == 0) {   // no rows: the adapters' gradients are zero
+    if (!da && !db) return RFQ_OK;
+    if ((st = current_device(&sms)) != RFQ_OK) return st;
+    const size_t e = grad_type == RFQ_OUT_BF16 ? 2u : 4u, nr = static_cast<size_t>(n_adapters) * static_cast<size_t>(rank);
+    if (da && (st = from_cuda(cudaMemsetAsync(da, 0, nr * static_cast<size_t>(K) * e, stream))) != RFQ_OK) return st;
+    return db ? from_cuda(cudaMemsetAsync(db, 0, nr * static_cast<size_t>(N) * e, stream)) : RFQ_OK;
+  }
+  if (!a_bf16 || !b_bf16 || !scale || !ids || !dy_bf16 || (da && !x_bf16) || (db && !hidden)) return RFQ_ERR_INVALID_ARG;
+  if (!aligned16(x_bf16) || !aligned16(a_bf16) || !aligned16(b_bf16) || !aligned16(dy_bf16) || !aligned_to(scale, 4) ||
+      !aligned_to(ids, 4) || !aligned_to(hidden, 4))
+    return RFQ_ERR_MISALIGNED;
+  st = check_workspace(workspace, workspace_bytes, rfq::lora_backward_workspace(M, K, N, rank, n_adapters));
+  if (st != RFQ_OK) return st;
+  if ((st = current_device(&sms)) != RFQ_OK) return st;
+  return from_cuda(rfq::launch_lora_backward(x_bf16, a_bf16, b_bf16, scale, ids, dy_bf16, hidden, dx_base, dx,
+                                             dx_type == RFQ_OUT_BF16, da, db, grad_type == RFQ_OUT_BF16, M, K, N, rank,
+                                             n_adapters, workspace, stream));
+}
+
+size_t rfq_linear_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n_adapters, int use_residual) {
+  const size_t adapters = rfq_lora_workspace_bytes(M, K, N, rank, n_adapters, 0);
+  if (adapters == 0 || (K % 32) != 0) return 0;
+  const size_t linear = rfq_linear_workspace_bytes(M, K, use_residual);
+  return adapters > linear ? adapters : linear;
+}
+
+rfq_status_t rfq_linear_lora(const void* x_bf16, int64_t M, int64_t K, const void* qw_codes, const void* qw_scales, int64_t N,
+                             const void* a_bf16, const void* b_bf16, const float* scale, const int32_t* ids,
+                             int64_t n_adapters, int64_t rank, void* y, rfq_out_t y_type, int use_residual, float* hidden,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  // Everything the adapters will ask for is checked before the projection is launched.
+  if (M < 0 || K < 0 || N < 0 || rank < 0 || n_adapters < 0) return RFQ_ERR_INVALID_ARG;
+  if (!out_type_ok(y_type)) return RFQ_ERR_INVALID_ARG;
+  if (!lora_shape_ok(M, K, N, rank, n_adapters) || (K % 32) != 0) return RFQ_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return RFQ_OK;
+  if (!a_bf16 || !b_bf16 || !scale || !ids || !y) return RFQ_ERR_INVALID_ARG;
+  if (!aligned16(a_bf16) || !aligned16(b_bf16) || !aligned_to(scale, 4) || !aligned_to(ids, 4) || !aligned16(y) ||
+      !aligned_to(hidden, 4))
+    return RFQ_ERR_MISALIGNED;
+  rfq_status_t st = check_workspace(workspace, workspace_bytes,
+                                    rfq_linear_lora_workspace_bytes(M, K, N, rank, n_adapters, use_residual));
+  if (st != RFQ_OK) return st;
+  st = rfq_linear(x_bf16, M, K, qw_codes, qw_scales, N, y, y_type, use_residual, workspace, workspace_bytes, stream);
+  if (st != RFQ_OK) return st;
+  return rfq_lora(x_bf16, M, K, a_bf16, b_bf16, scale, ids, n_adapters, rank, N, y, y, y_type, hidden, workspace,
+                  workspace_bytes, stream);
 }
 
 rfq_status_t rfq_mma_rate_probe(int variant, int64_t iterations, unsigned long long* cycles, int64_t cycles_len,

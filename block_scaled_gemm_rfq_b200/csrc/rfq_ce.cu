@@ -53,6 +53,11 @@ constexpr int kThreads = 320;            // warp 0 TMA, warp 1 MMA, warps 2..9 e
 constexpr uint32_t kTmemCols = 512;      // two accumulators of 256 fp32 columns
 constexpr uint32_t kSmemLimit = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
+// The tensor cores add into the fp32 accumulator by truncation, so a long contraction drifts
+// towards zero: 3e-6 of lse at D = 4096 when one accumulator takes all of it.  Where the
+// logits themselves are the result (kLogits) the accumulator therefore takes 1024 elements of
+// the contraction at a time and the epilogue adds those parts with rounding.
+constexpr int kLogitsPart = 16;          // k-tiles
 
 template <int kPair>
 struct Layout {
@@ -262,35 +267,39 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       bool ok = true;
       for (int tile = unit; tile < p.num_tiles && ok; tile += num_units) {
         const Tile t = tile_at(p, tile);
-        if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, &g_ce_error, kErrWaitAccEmpty)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t acc = tmem + buf * kBN;
-        for (int kt = t.kt0; kt < t.kt1; ++kt) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, &g_ce_error, kErrWaitFull)) {
+        const int part = kMode == kLogits ? kLogitsPart : t.kt1 - t.kt0;
+        for (int kp = t.kt0; kp < t.kt1 && ok; kp += part) {
+          if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, &g_ce_error, kErrWaitAccEmpty)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint8_t* sa = smem + stage * L::kStage;
-          const uint64_t da = operand_desc<kAMn>(sa);
-          const uint64_t db = operand_desc<kBMn>(sa + L::kATile);
+          const uint32_t acc = tmem + buf * kBN;
+          const int kp1 = min(kp + part, t.kt1);
+          for (int kt = kp; kt < kp1; ++kt) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, &g_ce_error, kErrWaitFull)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint8_t* sa = smem + stage * L::kStage;
+            const uint64_t da = operand_desc<kAMn>(sa);
+            const uint64_t db = operand_desc<kBMn>(sa + L::kATile);
 #pragma unroll
-          for (uint32_t q = 0; q < kBK / 16; ++q)
-            mma_bf16_g<kPair>(acc, da + q * kDescStep<kAMn>, db + q * kDescStep<kBMn>, idesc,
-                              (kt != t.kt0 || q != 0) ? 1u : 0u);
-          tc_commit_g<kPair>(&empty[stage]);
-          if (++stage == static_cast<uint32_t>(L::kStages)) {
-            stage = 0;
-            phase ^= 1u;
+            for (uint32_t q = 0; q < kBK / 16; ++q)
+              mma_bf16_g<kPair>(acc, da + q * kDescStep<kAMn>, db + q * kDescStep<kBMn>, idesc,
+                                (kt != kp || q != 0) ? 1u : 0u);
+            tc_commit_g<kPair>(&empty[stage]);
+            if (++stage == static_cast<uint32_t>(L::kStages)) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
+          if (!ok) break;
+          tc_commit_g<kPair>(&acc_full[buf]);
+          buf ^= 1u;
+          if (buf == 0) acc_phase ^= 1u;
         }
-        if (!ok) break;
-        tc_commit_g<kPair>(&acc_full[buf]);
-        buf ^= 1u;
-        if (buf == 0) acc_phase ^= 1u;
       }
       if (!ok) {
         // Teardown after an abort: wait for the MMAs already issued.
@@ -312,22 +321,44 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       const Tile t = tile_at(p, tile);
       const int row = (t.mb * kPair + static_cast<int>(rank)) * kBM + quad * 32 + lane;
       const int col0 = t.nb * kBN + half * 128;
-      if (!mbar_wait(&acc_full[buf], acc_phase, abort_flag, &g_ce_error, kErrWaitAccFull, 2 * kWaitLimitNs)) break;
-      tc_fence_after();
-      __syncwarp();   // rows past the end leave the loop body early
       uint32_t v[4][32];
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN + half * 128;
+      auto take = [&](bool first) {
+        if (!mbar_wait(&acc_full[buf], acc_phase, abort_flag, &g_ce_error, kErrWaitAccFull, 2 * kWaitLimitNs)) return false;
+        tc_fence_after();
+        __syncwarp();   // rows past the end leave the loop body early
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN + half * 128;
+        if (first) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_load_32x32b_x32(taddr + 32 * c, v[c]);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kPair == 2) mbar_arrive_remote(map_to_cta(smem_addr(&acc_empty[buf]), 0));
-        else mbar_arrive(&acc_empty[buf]);
-      }
-      buf ^= 1u;
-      if (buf == 0) acc_phase ^= 1u;
+          for (int c = 0; c < 4; ++c) tmem_load_32x32b_x32(taddr + 32 * c, v[c]);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t u[2][8];
+            tmem_load_32x32b_x8(taddr + 16 * c, u[0]);
+            tmem_load_32x32b_x8(taddr + 16 * c + 8, u[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t& w = v[c >> 1][16 * (c & 1) + i];
+              w = __float_as_uint(__uint_as_float(w) + __uint_as_float(u[i >> 3][i & 7]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair == 2) mbar_arrive_remote(map_to_cta(smem_addr(&acc_empty[buf]), 0));
+          else mbar_arrive(&acc_empty[buf]);
+        }
+        buf ^= 1u;
+        if (buf == 0) acc_phase ^= 1u;
+        return true;
+      };
+      bool ok = take(true);
+      if constexpr (kMode == kLogits)
+        for (int kp = t.kt0 + kLogitsPart; kp < t.kt1 && ok; kp += kLogitsPart) ok = take(false);
+      if (!ok) break;
       if (row >= p.M) continue;
 
       if constexpr (kMode == kLogits) {

@@ -68,6 +68,17 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
                                int64_t T, int64_t D, int64_t V, int64_t ignore, void* dh, void* dw, void* ws, int num_sms,
                                void* encode_tiled, cudaStream_t stream);
 
+// Low-rank adapters beside a projection (rfq_lora.cu).  base, hidden, dx, da, db may be nullptr.
+size_t lora_forward_workspace(int64_t M, int64_t K, int64_t r, int64_t n);
+size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n);
+cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* base,
+                                void* y, bool y_bf16, float* hidden, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n,
+                                void* ws, cudaStream_t stream);
+cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* dy,
+                                 const float* hidden, const void* dx_base, void* dx, bool dx_bf16, void* da, void* db,
+                                 bool grad_bf16, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, void* ws,
+                                 cudaStream_t stream);
+
 // Read and clear the device error words (GEMM, quantizer, fused layer, output head) of the current device.
 cudaError_t read_and_clear_device_error(unsigned int* value);
 cudaError_t read_and_clear_quant_error(unsigned int* value);

@@ -359,6 +359,61 @@ rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, cons
                                     cudaStream_t stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection (serving and fine-tuning on
+ * a frozen MXFP4 weight; the paper has no counterpart).  Row m uses adapter a = ids[m]:
+ *
+ *     s[m] = scale[a] A[a] x[m]         y[m] = base[m] + B[a] s[m]
+ *
+ * rfq_lora adds the adapters to a base; rfq_linear_lora is rfq_linear with the adapters
+ * added to its Y.  rfq_lora_backward gives, for dy = dL/dY (the adapters are linear, so the
+ * base's own gradient passes by; rfq_linear_dgrad gives it, into dx_base):
+ *
+ *     ds[m] = scale[a] B[a]^T dy[m]     dx[m] = dx_base[m] + A[a]^T ds[m]
+ *     dA[a] = sum over a's rows of ds[m] x[m]^T      dB[a] = sum of dy[m] s[m]^T
+ *
+ *   x_bf16 [M][K], a_bf16 [n_adapters][rank][K], b_bf16 [n_adapters][N][rank], dy_bf16 [M][N]:
+ *            bf16, 16-byte aligned; K and N multiples of 8 up to 2^20 (rfq_linear_lora: K a
+ *            multiple of 32), M <= 2^24
+ *   rank     8..RFQ_LORA_MAX_RANK, a multiple of 8; n_adapters 1..RFQ_LORA_MAX_ADAPTERS
+ *   scale    [n_adapters] fp32; ids [M] int32, in device memory, read by the kernels: a captured
+ *            graph follows their contents.  A row whose id is outside [0, n_adapters) has no
+ *            adapter: y is its base, dx its dx_base, its hidden is zero.  Rows of one adapter
+ *            need not be neighbours; they are cheapest if they are.
+ *   base     [M][N] in y_type, NULL for zeros, or y itself (then rows without an adapter are
+ *            left as they were).  dx_base [M][K] in dx_type likewise.  Any other overlap of an
+ *            output with an input is not allowed.
+ *   hidden   [M][rank] fp32 or NULL: rfq_lora writes s, which rfq_lora_backward reads for dB
+ *   dx, da, db   any may be NULL.  da [n_adapters][rank][K] and db [n_adapters][N][rank] in
+ *            grad_type, fully overwritten (zeros for an adapter without rows).  x_bf16 may be
+ *            NULL without da, hidden without db.
+ *   workspace   256-byte aligned, rfq_lora_workspace_bytes(...) bytes (backward != 0: enough for
+ *            both passes), rfq_linear_lora_workspace_bytes(...) for rfq_linear_lora.  Nothing in
+ *            it is carried from one call to the next.
+ * All sums are fp32.  s and ds enter the second product in bf16 for a bf16 result (two terms,
+ * 16 bits, in dA and dB) and as three bf16 terms (24 bits) for an fp32 result.  rfq_linear_lora
+ * with a bf16 Y rounds the projection to bf16 before the adapters are added, as any base is.
+ * A row reads its own adapter alone: values that are not finite stay in their row (dx, y) and
+ * adapter (dA, dB).  M == 0 launches nothing, except that da and db are then zeroed.  No
+ * atomics: results repeat bit for bit.
+ */
+#define RFQ_LORA_MAX_RANK 128
+#define RFQ_LORA_MAX_ADAPTERS 4096
+size_t rfq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n_adapters, int backward);
+rfq_status_t rfq_lora(const void* x_bf16, int64_t M, int64_t K, const void* a_bf16, const void* b_bf16, const float* scale,
+                      const int32_t* ids, int64_t n_adapters, int64_t rank, int64_t N, const void* base, void* y,
+                      rfq_out_t y_type, float* hidden, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+rfq_status_t rfq_lora_backward(const void* x_bf16, int64_t M, int64_t K, const void* a_bf16, const void* b_bf16,
+                               const float* scale, const int32_t* ids, int64_t n_adapters, int64_t rank, int64_t N,
+                               const void* dy_bf16, const float* hidden, const void* dx_base, void* dx, rfq_out_t dx_type,
+                               void* da, void* db, rfq_out_t grad_type, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+size_t rfq_linear_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n_adapters, int use_residual);
+rfq_status_t rfq_linear_lora(const void* x_bf16, int64_t M, int64_t K, const void* qw_codes, const void* qw_scales, int64_t N,
+                             const void* a_bf16, const void* b_bf16, const float* scale, const int32_t* ids,
+                             int64_t n_adapters, int64_t rank, void* y, rfq_out_t y_type, int use_residual, float* hidden,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * rfq_mma_rate_probe -- measurement support (no counterpart in the paper): the rate
  * at which this GPU's tensor cores retire the MMA instructions rfq_gemm issues,
  * with the operands resident in shared memory (no loads, no epilogue).  It is the
