@@ -12,6 +12,7 @@ R = X - DQ(QX) requantized by the same MXFP4 rule.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -28,6 +29,7 @@ __all__ = [
     "linear_ce_workspace_bytes", "linear_ce", "linear_ce_backward", "linear_ce_alloc", "linear_ce_backward_alloc",
     "lora_workspace_bytes", "lora", "lora_backward", "lora_alloc", "lora_backward_alloc", "linear_lora_workspace_bytes",
     "linear_lora", "linear_lora_alloc", "LORA_MAX_RANK", "LORA_MAX_ADAPTERS",
+    "grad_clip_workspace_bytes", "grad_norm", "grad_clip", "grad_norm_alloc", "grad_clip_alloc",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -50,6 +52,7 @@ EXPORTED_SYMBOLS = (
     "rfq_mxfp8_codes_bytes", "rfq_quantize_mxfp8", "rfq_gemm_mxfp8", "rfq_mma_rate_probe",
     "rfq_linear_ce_workspace_bytes", "rfq_linear_ce", "rfq_linear_ce_backward",
     "rfq_lora_workspace_bytes", "rfq_lora", "rfq_lora_backward", "rfq_linear_lora_workspace_bytes", "rfq_linear_lora",
+    "rfq_grad_clip_workspace_bytes", "rfq_grad_norm", "rfq_grad_clip",
 )
 
 # Largest iteration count of the tensor-core rate probe (RFQ_MMA_PROBE_MAX_ITERATIONS).
@@ -114,6 +117,9 @@ def load_library():
                 "rfq_linear_ce_workspace_bytes": (SZ, [I64, I64, I64, I, I]),
                 "rfq_linear_ce": (I, [P, P, P, I64, I64, I64, I64, P, P, P, SZ, P]),
                 "rfq_linear_ce_backward": (I, [P, P, P, P, P, I64, I64, I64, I64, P, P, P, SZ, P]),
+                "rfq_grad_clip_workspace_bytes": (SZ, [I64]),
+                "rfq_grad_norm": (I, [P, P, P, I64, P, P, SZ, P]),
+                "rfq_grad_clip": (I, [P, P, P, P, I64, ctypes.c_float, P, P, SZ, P]),
                 "rfq_lora_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I]),
                 "rfq_lora": (I, [P, I64, I64, P, P, P, P, I64, I64, I64, P, P, I, P, P, SZ, P]),
                 "rfq_lora_backward": (I, [P, I64, I64, P, P, P, P, I64, I64, I64, P, P, P, P, I, P, P, I, P, SZ, P]),
@@ -487,6 +493,64 @@ def linear_lora(x, qw_codes, qw_scales, N, a, b, scale, ids, y, workspace, use_r
             workspace.numel(), st), "rfq_linear_lora")
 
 
+def grad_clip_workspace_bytes(count: int) -> int:
+    """rfq_grad_clip_workspace_bytes: workspace of rfq_grad_norm and rfq_grad_clip for a list of `count` tensors."""
+    return int(load_library().rfq_grad_clip_workspace_bytes(count))
+
+
+def _tensor_list(where, tensors, device, like=None):
+    """Host arrays (addresses, element counts, types) of a list of contiguous bf16 / fp32 tensors on one device."""
+    import torch
+    T = torch.Tensor
+    dtypes = [t.dtype for t in tensors]
+    if like is not None and [t.dtype for t in like] != dtypes:
+        raise RFQError(1, f"{where}: an output has the type of its gradient")
+    if any(d is not torch.bfloat16 and d is not torch.float32 for d in dtypes):
+        raise RFQError(1, f"{where}: want bfloat16 or float32 tensors")
+    if not all(map(T.is_contiguous, tensors)) or not set(map(T.get_device, tensors)) <= {device.index}:
+        raise RFQError(1, f"{where}: want contiguous tensors on {device}")
+    numels = array.array("q", map(T.numel, tensors))
+    if like is not None and numels != array.array("q", map(T.numel, like)):
+        raise RFQError(1, f"{where}: an output has the size of its gradient")
+    types = array.array("i", [OUT_BF16 if d is torch.bfloat16 else OUT_F32 for d in dtypes])
+    return array.array("Q", map(T.data_ptr, tensors)), numels, types
+
+
+def _norm_args(where, grads, norm, workspace):
+    import torch
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise RFQError(1, f"{where}: the norm is one float32")
+    _need_workspace(where, workspace, norm.device)
+    return _tensor_list(where, grads, norm.device)
+
+
+def grad_norm(grads, norm, workspace, stream=None):
+    """rfq_grad_norm: norm (one fp32 on the device) = the 2-norm over all elements of a list of bf16 / fp32 tensors."""
+    grads = list(grads)
+    ptrs, numels, types = _norm_args("rfq_grad_norm", grads, norm, workspace)
+    with _On(norm.device, stream) as st:
+        _check(load_library().rfq_grad_norm(ptrs.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0], len(grads),
+                                            norm.data_ptr(), workspace.data_ptr(), workspace.numel(), st), "rfq_grad_norm")
+
+
+def grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None):
+    """rfq_grad_clip: the list scaled by min(1, max_norm / (norm + 1e-6)), in place or into `outs`, and its norm
+    before that (one fp32 on the device)."""
+    grads = list(grads)
+    ptrs, numels, types = _norm_args("rfq_grad_clip", grads, norm, workspace)
+    out_ptrs = None
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != len(grads):
+            raise RFQError(1, "rfq_grad_clip: one output for each gradient")
+        out_ptrs = _tensor_list("rfq_grad_clip: outs", outs, norm.device, like=grads)[0]
+    with _On(norm.device, stream) as st:
+        _check(load_library().rfq_grad_clip(
+            ptrs.buffer_info()[0], None if out_ptrs is None else out_ptrs.buffer_info()[0], numels.buffer_info()[0],
+            types.buffer_info()[0], len(grads), float(max_norm), norm.data_ptr(), workspace.data_ptr(), workspace.numel(), st),
+            "rfq_grad_clip")
+
+
 def check_device_error(stream=None):
     """Synchronize and report a bounded-wait timeout inside a kernel (raises RFQError)."""
     detail = ctypes.c_int(0)
@@ -702,3 +766,27 @@ def linear_lora_alloc(x, qw: QuantizedTensor, a, b, scale, ids, out_dtype=None, 
         ws = _empty_u8(linear_lora_workspace_bytes(M, K, qw.rows, r, n, use_residual), x.device)
     linear_lora(x, qw.codes, qw.scales, qw.rows, a, b, scale, ids, y, ws, use_residual, hidden, stream)
     return (y, hidden) if want_hidden else y
+
+
+def grad_norm_alloc(grads, stream=None):
+    """rfq_grad_norm with a fresh workspace into a new fp32 tensor of one element."""
+    import torch
+    grads = list(grads)
+    device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    with _torch_stream(stream, device):
+        norm = torch.empty(1, dtype=torch.float32, device=device)
+        ws = _empty_u8(grad_clip_workspace_bytes(len(grads)), device)
+    grad_norm(grads, norm, ws, stream)
+    return norm
+
+
+def grad_clip_alloc(grads, max_norm, stream=None):
+    """rfq_grad_clip in place with a fresh workspace; returns the norm before clipping (a new fp32 tensor)."""
+    import torch
+    grads = list(grads)
+    device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    with _torch_stream(stream, device):
+        norm = torch.empty(1, dtype=torch.float32, device=device)
+        ws = _empty_u8(grad_clip_workspace_bytes(len(grads)), device)
+    grad_clip(grads, max_norm, norm, ws, stream=stream)
+    return norm

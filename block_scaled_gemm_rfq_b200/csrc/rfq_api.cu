@@ -200,6 +200,36 @@ bool lora_shape_ok(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n) {
 
 bool out_type_ok(rfq_out_t t) { return t == RFQ_OUT_F32 || t == RFQ_OUT_BF16; }
 
+// A list of gradients: every entry a bf16 or fp32 array on its own alignment, 2^43 elements in all
+// (the kernels number pieces of 8192 elements with 30 bits).
+rfq_status_t check_list(const void* const* in, const void* const* out, const int64_t* numels, const rfq_out_t* types,
+                        int64_t count) {
+  if (count < 0 || count > (int64_t(1) << 24) || (count > 0 && (!in || !numels || !types))) return RFQ_ERR_INVALID_ARG;
+  constexpr int64_t kMost = int64_t(1) << 42;
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (numels[i] < 0 || !out_type_ok(types[i])) return RFQ_ERR_INVALID_ARG;
+    if (numels[i] > kMost || (total += (numels[i] + 8191) / 8192 * 8192) > kMost) return RFQ_ERR_UNSUPPORTED_SHAPE;
+    if (numels[i] == 0) continue;
+    const uintptr_t size = types[i] == RFQ_OUT_F32 ? 4 : 2;
+    if (!in[i] || (out && !out[i])) return RFQ_ERR_INVALID_ARG;
+    if (!aligned_to(in[i], size) || (out && !aligned_to(out[i], size))) return RFQ_ERR_MISALIGNED;
+  }
+  return RFQ_OK;
+}
+
+rfq_status_t clip_impl(const void* const* in, void* const* out, const int64_t* numels, const rfq_out_t* types, int64_t count,
+                       bool scale, float max_norm, float* norm, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  rfq_status_t st = check_list(in, out, numels, types, count);
+  if (st != RFQ_OK) return st;
+  if (!norm) return RFQ_ERR_INVALID_ARG;
+  if (!aligned_to(norm, 4)) return RFQ_ERR_MISALIGNED;
+  if ((st = check_workspace(workspace, workspace_bytes, rfq::clip_workspace(count))) != RFQ_OK) return st;
+  int sms = 0;
+  if ((st = current_device(&sms)) != RFQ_OK) return st;
+  return from_cuda(rfq::launch_clip(in, out, numels, types, count, scale, max_norm, norm, workspace, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -500,6 +530,20 @@ rfq_status_t rfq_linear_lora(const void* x_bf16, int64_t M, int64_t K, const voi
   if (st != RFQ_OK) return st;
   return rfq_lora(x_bf16, M, K, a_bf16, b_bf16, scale, ids, n_adapters, rank, N, y, y, y_type, hidden, workspace,
                   workspace_bytes, stream);
+}
+
+size_t rfq_grad_clip_workspace_bytes(int64_t count) { return count < 0 || count > (int64_t(1) << 24) ? 0 : rfq::clip_workspace(count); }
+
+rfq_status_t rfq_grad_norm(const void* const* grads, const int64_t* numels, const rfq_out_t* types, int64_t count, float* norm,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return clip_impl(grads, nullptr, numels, types, count, false, 0.f, norm, workspace, workspace_bytes, stream);
+}
+
+rfq_status_t rfq_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const rfq_out_t* types,
+                           int64_t count, float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  if (!(max_norm >= 0.f)) return RFQ_ERR_INVALID_ARG;
+  return clip_impl(grads, outs, numels, types, count, true, max_norm, norm, workspace, workspace_bytes, stream);
 }
 
 rfq_status_t rfq_mma_rate_probe(int variant, int64_t iterations, unsigned long long* cycles, int64_t cycles_len,

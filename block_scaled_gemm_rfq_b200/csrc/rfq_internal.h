@@ -6,6 +6,8 @@
 
 #include <cstdint>
 
+#include "rfq.h"
+
 namespace rfq {
 
 // Kernel 1: fused quantizer.  qr_codes == nullptr selects plain MXFP4.
@@ -78,6 +80,12 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
                                  const float* hidden, const void* dx_base, void* dx, bool dx_bf16, void* da, void* db,
                                  bool grad_bf16, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, void* ws,
                                  cudaStream_t stream);
+
+// Global norm of a list of tensors (host arrays) and, where `scale`, the list scaled to it (rfq_clip.cu).
+// out == nullptr scales in place.
+size_t clip_workspace(int64_t count);
+cudaError_t launch_clip(const void* const* in, void* const* out, const int64_t* numels, const rfq_out_t* types, int64_t count,
+                        bool scale, float max_norm, float* norm, void* ws, cudaStream_t stream);
 
 // Read and clear the device error words (GEMM, quantizer, fused layer, output head) of the current device.
 cudaError_t read_and_clear_device_error(unsigned int* value);

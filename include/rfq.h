@@ -414,6 +414,38 @@ rfq_status_t rfq_linear_lora(const void* x_bf16, int64_t M, int64_t K, const voi
                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Global norm of a list of gradients and clipping to a largest norm (training; the paper has
+ * no counterpart).
+ *
+ *     norm = sqrt(sum of x^2 over all elements of all tensors)
+ *     outs[i] = min(1, max_norm / (norm + 1e-6)) * grads[i]
+ *
+ * rfq_grad_norm writes the norm alone.  rfq_grad_clip writes the norm (before clipping) and the
+ * scaled list; outs NULL scales in place, and then nothing is written where the factor is 1.
+ *
+ *   grads, outs   host arrays of `count` device pointers, aligned to their element (16-byte
+ *                 aligned ones are faster); outs[i] may be grads[i].  Any other overlap, and a
+ *                 tensor twice in the list, is not allowed.  A NULL pointer is allowed for an
+ *                 empty tensor alone.
+ *   numels        host array of their element counts; types: host array of their types
+ *                 (RFQ_OUT_F32 or RFQ_OUT_BF16; an output has the type of its input)
+ *   max_norm      >= 0; infinity never scales
+ *   norm          device pointer to one fp32
+ *   workspace     rfq_grad_clip_workspace_bytes(count) bytes, 256-byte aligned
+ * The host arrays are read before the call returns; a captured graph keeps the addresses in them.
+ * 0 <= count <= 2^24, 2^42 elements in all; an empty list has norm 0.  Squares are summed in fp32
+ * over 32 elements and in fp64 from there, so the norm of any finite fp32 or bf16 values is right
+ * unless it exceeds fp32's range itself.  A list with an infinity or a NaN has a norm that is not
+ * finite, and is scaled by 0 or NaN.  No atomics: results repeat bit for bit.
+ */
+size_t rfq_grad_clip_workspace_bytes(int64_t count);
+rfq_status_t rfq_grad_norm(const void* const* grads, const int64_t* numels, const rfq_out_t* types, int64_t count, float* norm,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+rfq_status_t rfq_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const rfq_out_t* types,
+                           int64_t count, float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/*
  * rfq_mma_rate_probe -- measurement support (no counterpart in the paper): the rate
  * at which this GPU's tensor cores retire the MMA instructions rfq_gemm issues,
  * with the operands resident in shared memory (no loads, no epilogue).  It is the
