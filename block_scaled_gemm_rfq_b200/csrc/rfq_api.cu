@@ -469,7 +469,7 @@ rfq_status_t rfq_lora(const void* x_bf16, int64_t M, int64_t K, const void* a_bf
   int sms = 0;
   if ((st = current_device(&sms)) != RFQ_OK) return st;
   return from_cuda(rfq::launch_lora_forward(x_bf16, a_bf16, b_bf16, scale, ids, base, y, y_type == RFQ_OUT_BF16, hidden, M, K, N,
-                                            rank, n_adapters, workspace, stream));
+                                            rank, n_adapters, workspace, sms, g_encode_tiled, stream));
 }
 
 rfq_status_t rfq_lora_backward(const void* x_bf16, int64_t M, int64_t K, const void* a_bf16, const void* b_bf16,
@@ -500,7 +500,7 @@ rfq_status_t rfq_lora_backward(const void* x_bf16, int64_t M, int64_t K, const v
   if ((st = current_device(&sms)) != RFQ_OK) return st;
   return from_cuda(rfq::launch_lora_backward(x_bf16, a_bf16, b_bf16, scale, ids, dy_bf16, hidden, dx_base, dx,
                                              dx_type == RFQ_OUT_BF16, da, db, grad_type == RFQ_OUT_BF16, M, K, N, rank,
-                                             n_adapters, workspace, stream));
+                                             n_adapters, workspace, sms, g_encode_tiled, stream));
 }
 
 size_t rfq_linear_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n_adapters, int use_residual) {
@@ -577,9 +577,12 @@ rfq_status_t rfq_check_device_error(cudaStream_t stream, int* detail) {
   if (rfq::read_and_clear_fused_error(&f) != cudaSuccess) return RFQ_ERR_CUDA;
   unsigned int c = 0;
   if (rfq::read_and_clear_ce_error(&c) != cudaSuccess) return RFQ_ERR_CUDA;
+  unsigned int l = 0;
+  if (rfq::read_and_clear_lora_error(&l) != cudaSuccess) return RFQ_ERR_CUDA;
   if (v == 0) v = q;
   if (v == 0) v = f;
   if (v == 0) v = c;
+  if (v == 0) v = l;
   if (detail) *detail = static_cast<int>(v);
   return v ? RFQ_ERR_TIMEOUT : RFQ_OK;
 }

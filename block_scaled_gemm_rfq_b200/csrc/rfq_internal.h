@@ -75,11 +75,17 @@ size_t lora_forward_workspace(int64_t M, int64_t K, int64_t r, int64_t n);
 size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n);
 cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* base,
                                 void* y, bool y_bf16, float* hidden, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n,
-                                void* ws, cudaStream_t stream);
+                                void* ws, int num_sms, void* encode_tiled, cudaStream_t stream);
 cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* dy,
                                  const float* hidden, const void* dx_base, void* dx, bool dx_bf16, void* da, void* db,
-                                 bool grad_bf16, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, void* ws,
-                                 cudaStream_t stream);
+                                 bool grad_bf16, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, void* ws, int num_sms,
+                                 void* encode_tiled, cudaStream_t stream);
+// Their two products over long batches (rfq_lora_wide.cu): s [M][r] = scale (P src), out = base + Q s,
+// the pool [n][r][C], transposed [n][C][r] (shrink) and the other way round (expand).
+cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool trans, const int* ids, const float* scale, float* s,
+                                    int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream);
+cudaError_t launch_lora_expand_wide(const float* s, const void* pool, bool trans, const int* ids, const void* base, void* out, bool f32,
+                                    int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream);
 
 // Global norm of a list of tensors (host arrays) and, where `scale`, the list scaled to it (rfq_clip.cu).
 // out == nullptr scales in place.
@@ -87,10 +93,11 @@ size_t clip_workspace(int64_t count);
 cudaError_t launch_clip(const void* const* in, void* const* out, const int64_t* numels, const rfq_out_t* types, int64_t count,
                         bool scale, float max_norm, float* norm, void* ws, cudaStream_t stream);
 
-// Read and clear the device error words (GEMM, quantizer, fused layer, output head) of the current device.
+// Read and clear the device error words (GEMM, quantizer, fused layer, output head, adapters) of the current device.
 cudaError_t read_and_clear_device_error(unsigned int* value);
 cudaError_t read_and_clear_quant_error(unsigned int* value);
 cudaError_t read_and_clear_fused_error(unsigned int* value);
 cudaError_t read_and_clear_ce_error(unsigned int* value);
+cudaError_t read_and_clear_lora_error(unsigned int* value);
 
 }  // namespace rfq

@@ -12,20 +12,32 @@
 //     dA_a = sum ds_m x_m^T         dB_a = sum dy_m s_m^T
 //
 // With r far below K and N every product is bound by memory: x and dy are read and y and
-// dx written once per pass over them, at 2 r flops for each of their elements.  So the
-// kernels are built around the wide matrices' rows and use warp-level m16n8k16 MMAs, whose
-// operands may be transposed on the way from shared memory (A and B are each needed in
-// both directions) and whose rows can be gathered:
+// dx written once per pass over them, at 2 r flops for each of their elements:
 //
-//   shrink   s, ds: rows x wide -> rank, the contraction split over CTAs, partial sums fp32
-//   expand   y, dx: rank -> wide, adds the partial sums in order, adds the base
+//   shrink   s, ds: rows x wide -> rank
+//   expand   y, dx: rank -> wide, added to the base
 //   split    s, ds as sums of bf16 terms for the next one
 //   outer    dA, dB: contraction over rows, split into row ranges
 //   reduce   sums the ranges in order and rounds
 //
-// The rows of a 128-row chunk are grouped by adapter inside the CTA that works on them (no
-// host knowledge of the ids, no order asked of them): groups of up to kRows rows share an
-// adapter's weights.  No atomics: a result does not depend on timing.
+// Long batches take the shrink and expand of rfq_lora_wide.cu (tcgen05, 128 neighbouring
+// rows).  Here are those of short batches, where rows have adapters of their own and time goes
+// into reading the adapters' weights, and the adapters' gradients; all on warp-level m16n8k16
+// MMAs.  The rows of a 128-row chunk are grouped by adapter inside the CTA that works on them (no
+// host knowledge of the ids, no order asked of them): groups of up to 16 rows share an
+// adapter's weights.
+//
+// Weights that run along the contraction (A in shrink, B in expand: the forward pass) go from
+// global memory straight into MMA fragments, each used by one warp once: a thread's fragment
+// takes any four contraction elements of its row as long as the other operand takes the
+// same, so it loads neighbouring ones, 8 or 16 bytes at a time.  Weights that run across it (the
+// backward pass) and the gradients' operands go through shared memory with 16-byte
+// asynchronous copies and are transposed on the way out (ldmatrix).  Each thread keeps the
+// addresses of the pieces it copies and steps them along: with the addresses formed anew for
+// each copy the kernels issued 1600 instructions a warp for 8 KiB and ran at 1.9 TB/s; with one
+// bulk copy for each 256-byte row piece they were slower still (about 65 ns a copy and SM).
+//
+// No atomics: a result does not depend on timing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,22 +51,22 @@ namespace rfq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 128;      // rows grouped by one CTA
-constexpr int kStages = 4;
+constexpr int kChunk = 128;                // rows grouped by one CTA
+constexpr int kRows = 16;                  // rows of one group
+constexpr int kMaxStages = 6;
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kStaticSmem = 24 * 1024;     // more than any kernel here has besides its dynamic part
 
 __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-// Row stride in shared memory, in 16-byte units: odd, so that eight rows at one column fall
-// into eight different bank groups (ldmatrix without conflicts).
-__host__ __device__ constexpr int odd_stride(int chunks16) { return chunks16 | 1; }
+// Row stride in shared memory of rows of `bytes` bytes: an odd number of 16-byte units, so that
+// eight rows at one column fall into eight different bank groups (ldmatrix without conflicts).
+__host__ __device__ constexpr int odd_stride(int bytes) { return ((bytes / 16) | 1) * 16; }
+// Rows along which the rank runs (r * 2 bytes) lie back to back in global memory.  Up to 32 bytes,
+// or an odd number of 16-byte units, they are copied as one block as they lie (at most two-way
+// conflicts); longer ones row by row with a padded stride.
+__host__ __device__ constexpr bool rank_block(int r) { return r <= 16 || (r / 8) % 2 == 1; }
+__host__ __device__ constexpr int rank_stride(int r) { return rank_block(r) ? 2 * r : odd_stride(2 * r); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kN>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
-}
 template <bool kTrans>
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   if constexpr (kTrans)
@@ -76,6 +88,25 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[2], uint32_t b) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(b));
+}
+// 16 bytes from global to shared memory; zeros (and no read) where `valid` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most stages - 2 groups of this thread are on their way (stages: 2 to kMaxStages).
+__device__ __forceinline__ void cp_wait_stage(int stages) {
+  switch (stages) {
+    case 2: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+  }
 }
 
 // The rows of one chunk, grouped by adapter: order[] lists them (as offsets in the chunk) by
@@ -101,14 +132,30 @@ __device__ void group_rows(Groups& g, const int* ids, int64_t row0, int64_t M, i
     }
     g.ids[t] = id;
   }
+  // Rows already in order (neighbours of one request, one adapter for all): nothing to sort, and
+  // a run's first row is the last one before t that differs from its predecessor.
   __syncthreads();
-  if (t < count) {
+  const bool sorted = __syncthreads_and(t == 0 || t >= count || g.ids[t - 1] <= id);
+  if (sorted) {
+    if (t < kChunk) {
+      const unsigned bits = __ballot_sync(0xffffffffu, t < count && (t == 0 || g.ids[t - 1] != id));
+      if ((t & 31) == 0) g.start[t >> 5] = static_cast<int>(bits);
+    }
+    __syncthreads();
+    if (t < count) {
+      int w = t >> 5;
+      unsigned bits = static_cast<unsigned>(g.start[w]) & (0xffffffffu >> (31 - (t & 31)));
+      while (bits == 0) bits = static_cast<unsigned>(g.start[--w]);   // row 0 begins a run
+      g.order[t] = t;
+      g.flag[t] = (t - (w * 32 + 31 - __clz(bits))) % kRows == 0;
+    }
+  } else if (t < count) {
     int less = 0, before = 0;
-#pragma unroll 8
-    for (int j = 0; j < count; ++j) {
-      const int v = g.ids[j];
-      less += v < id;
-      before += v == id && j < t;
+#pragma unroll 4
+    for (int j = 0; j < kChunk; j += 4) {   // entries past the last row hold INT_MAX
+      const int4 v = *reinterpret_cast<const int4*>(&g.ids[j]);
+      less += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
+      before += (v.x == id && j < t) + (v.y == id && j + 1 < t) + (v.z == id && j + 2 < t) + (v.w == id && j + 3 < t);
     }
     g.order[less + before] = t;
     g.flag[less + before] = before % kRows == 0;
@@ -132,40 +179,33 @@ __device__ void group_rows(Groups& g, const int* ids, int64_t row0, int64_t M, i
 
 // ---------------------------------------------------------------- shrink
 // part[split][m][j] = sum over the split's k of src[m][k] P_a[j][k], P = A (rows j, k along the
-// row) or, kTrans, B (rows k, j along the row).
+// row; the direct kernel) or B^T (rows k, j along the row).
 struct ShrinkParams {
   const __nv_bfloat16* src;   // [M][C]
-  const __nv_bfloat16* p;     // [n][r][C] or [n][C][r]
+  const __nv_bfloat16* p;     // [n][r][C] (direct) or [n][C][r]
   const int* ids;
   float* part;                // [splits][M][r]
   int64_t M, C, c_split;      // c_split: contraction elements of one split (a multiple of kBK)
   int n, r, zs;               // zs: CTAs that share the items of one chunk
+  int stages;
 };
 
-template <int kRows>
-struct ShrinkTile {
-  static constexpr int kWm = kRows / 16;         // warps along the rows
-  static constexpr int kWk = 8 / kWm;            // warps along a stage's contraction
-  static constexpr int kBK = kWk == 8 ? 128 : 64;
-  static constexpr int kSteps = kBK / 16 / kWk;  // k16 steps of a warp in one stage
-  static constexpr int kXStride = odd_stride(kBK / 8);
-  static constexpr int kXBytes = kRows * kXStride * 16;
-};
-template <int kRows, bool kTrans>
-__host__ __device__ constexpr int shrink_p_stride(int r) {
-  return kTrans ? odd_stride(r / 8) : odd_stride(ShrinkTile<kRows>::kBK / 8);
-}
-template <int kRows, bool kTrans>
-__host__ __device__ constexpr int shrink_p_bytes(int r) {
-  return (kTrans ? ShrinkTile<kRows>::kBK : r) * shrink_p_stride<kRows, kTrans>(r) * 16;
+constexpr int kBK = 128;                         // contraction elements of one stage
+constexpr int kRowStride = odd_stride(kBK * 2);  // of a 256-byte row segment
+__host__ __device__ constexpr int shrink_p_bytes(int r) { return kBK * rank_stride(r); }
+__host__ __device__ constexpr int shrink_red_bytes(int r) {
+  return (8 / (kRows / 16) - 1) * kRows * r * 4;
 }
 
-template <int kRows, bool kTrans, int kJ>   // kJ: 8-column tiles of the rank, at most
+template <int kJ>   // 8-column tiles of the rank, at most
 __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkParams p) {
-  using T = ShrinkTile<kRows>;
+  constexpr int kWm = kRows / 16;               // warps along the rows
+  constexpr int kWk = 8 / kWm;                  // warps along a stage's contraction
+  constexpr int kSteps = kBK / 16 / kWk;        // k16 steps of a warp in one stage
+  constexpr int kXCopies = kRows / 16;          // row pieces of 16 bytes a thread copies per stage
+  constexpr int kPCopies = kJ * 8 * (kBK / 8) / kThreads;   // of the adapter's weights, at most
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Groups g;
-  __shared__ int64_t row_of[kRows];
+  __shared__ __align__(16) Groups g;
   griddep_launch_dependents();
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
@@ -173,49 +213,63 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
   group_rows<kRows>(g, p.ids, row0, p.M, p.n);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wm = warp % T::kWm, wk = warp / T::kWm;
-  const int p_stride = shrink_p_stride<kRows, kTrans>(p.r);
-  const int p_bytes = shrink_p_bytes<kRows, kTrans>(p.r);
-  const int stage_bytes = T::kXBytes + p_bytes;
-  const uint32_t base = smem_addr(smem);
+  const int wm = warp % kWm, wk = warp / kWm;
   const int jt = p.r / 8;
+  const int p_stride = rank_stride(p.r);
+  const int stage_bytes = kRows * kRowStride + shrink_p_bytes(p.r);
+  const uint32_t base = smem_addr(smem);
+  float* red = reinterpret_cast<float*>(smem + p.stages * stage_bytes);   // [kWk - 1][kRows][r]
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * p.c_split;
   const int64_t c1 = min(p.C, c0 + p.c_split);
-  const int iters = static_cast<int>(ceil_div(c1 - c0, T::kBK));
+  const int iters = static_cast<int>(ceil_div(c1 - c0, kBK));
+  const int qx = tid & 15;                      // this thread's 16-byte piece of a 256-byte row segment
 
   for (int item = z; item < g.items; item += p.zs) {
     const int first = g.start[item], rows = g.start[item + 1] - first;
     const int a = g.ids[g.order[first]];
     if (a == INT_MAX) break;   // rows without an adapter come last
-    for (int i = tid; i < kRows; i += kThreads) row_of[i] = i < rows ? row0 + g.order[first + i] : -1;
-    __syncthreads();
+    const __nv_bfloat16* x_at[kXCopies];
+    unsigned x_row = 0;
+#pragma unroll
+    for (int u = 0; u < kXCopies; ++u) {
+      const int m = (tid >> 4) + 16 * u;
+      const bool has = m < rows;
+      x_row |= static_cast<unsigned>(has) << u;
+      x_at[u] = p.src + (row0 + g.order[has ? first + m : first]) * p.C + c0 + 8 * qx;
+    }
     const __nv_bfloat16* pa = p.p + static_cast<int64_t>(a) * p.r * p.C;
-
-    auto load = [&](int it) {
-      if (it < iters) {
-        const uint32_t sx = base + (it % kStages) * stage_bytes, sp = sx + T::kXBytes;
-        const int64_t c = c0 + static_cast<int64_t>(it) * T::kBK;
-        for (int i = tid; i < kRows * (T::kBK / 8); i += kThreads) {
-          const int m = i / (T::kBK / 8), q = i % (T::kBK / 8);
-          const int64_t row = row_of[m];
-          const bool ok = row >= 0 && c + 8 * q < c1;
-          cp_async16(sx + (m * T::kXStride + q) * 16, ok ? p.src + row * p.C + c + 8 * q : p.src, ok);
+    const __nv_bfloat16* p_at[kPCopies];
+    uint32_t p_to[kPCopies];
+    int p_k[kPCopies];         // contraction element of the piece in its stage; kBK where there is none
+#pragma unroll
+    for (int u = 0; u < kPCopies; ++u) {
+      const int i = tid + kThreads * u;
+      const int k = i / jt;
+      p_k[u] = k < kBK ? k : kBK;
+      p_at[u] = pa + c0 * p.r + 8 * static_cast<int64_t>(i);
+      p_to[u] = k * p_stride + (i - k * jt) * 16;
+    }
+    int load_stage = 0, load_left = static_cast<int>(c1 - c0);   // contraction elements not yet asked for
+    auto load = [&]() {
+      if (load_left > 0) {
+        const uint32_t sx = base + load_stage * stage_bytes, sp = sx + kRows * kRowStride;
+#pragma unroll
+        for (int u = 0; u < kXCopies; ++u) {
+          const bool ok = (x_row >> u & 1u) && 8 * qx < load_left;
+          cp_async16(sx + ((tid >> 4) + 16 * u) * kRowStride + 16 * qx, ok ? x_at[u] : p.src, ok);
+          x_at[u] += kBK;
         }
-        if constexpr (kTrans) {
-          for (int i = tid; i < T::kBK * jt; i += kThreads) {
-            const int k = i / jt, q = i - k * jt;
-            const bool ok = c + k < c1;
-            cp_async16(sp + (k * p_stride + q) * 16, ok ? pa + (c + k) * p.r + 8 * q : p.p, ok);
+#pragma unroll
+        for (int u = 0; u < kPCopies; ++u)
+          if (p_k[u] < kBK) {
+            const bool ok = p_k[u] < load_left;
+            cp_async16(sp + p_to[u], ok ? p_at[u] : p.p, ok);
+            p_at[u] += kBK * p.r;
           }
-        } else {
-          for (int i = tid; i < p.r * (T::kBK / 8); i += kThreads) {
-            const int j = i / (T::kBK / 8), q = i % (T::kBK / 8);
-            const bool ok = c + 8 * q < c1;
-            cp_async16(sp + (j * p_stride + q) * 16, ok ? pa + static_cast<int64_t>(j) * p.C + c + 8 * q : p.p, ok);
-          }
-        }
       }
       cp_commit();
+      load_left -= kBK;
+      if (++load_stage == p.stages) load_stage = 0;
     };
 
     float acc[kJ][4];
@@ -223,53 +277,158 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
     for (int j = 0; j < kJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    for (int it = 0; it < kStages - 1; ++it) load(it);
+    for (int it = 0; it < p.stages - 1; ++it) load();
+    int stage = 0;
     for (int it = 0; it < iters; ++it) {
-      cp_wait<kStages - 2>();
+      cp_wait_stage(p.stages);
       __syncthreads();
-      load(it + kStages - 1);
-      const uint32_t sx = base + (it % kStages) * stage_bytes, sp = sx + T::kXBytes;
+      load();
+      const uint32_t sx = base + stage * stage_bytes, sp = sx + kRows * kRowStride;
+      if (wm * 16 < rows) {
 #pragma unroll
-      for (int s = 0; s < T::kSteps; ++s) {
-        const int ks = wk * T::kSteps + s;
-        uint32_t fa[4];
-        ldsm4<false>(fa, sx + ((wm * 16 + (lane & 15)) * T::kXStride + 2 * ks + (lane >> 4)) * 16);
+        for (int s = 0; s < kSteps; ++s) {
+          const int ks = wk * kSteps + s;
+          uint32_t fa[4];
+          ldsm4<false>(fa, sx + (wm * 16 + (lane & 15)) * kRowStride + 32 * ks + (lane >> 4) * 16);
 #pragma unroll
-        for (int j = 0; j < kJ; j += 2) {
-          if (j + 1 < jt) {
-            uint32_t fb[4];
-            if constexpr (kTrans) ldsm4<true>(fb, sp + ((ks * 16 + (lane & 15)) * p_stride + j + (lane >> 4)) * 16);
-            else ldsm4<false>(fb, sp + ((j * 8 + (lane & 7) + ((lane >> 4) << 3)) * p_stride + 2 * ks + ((lane >> 3) & 1)) * 16);
-            mma16816(acc[j], fa, fb[0], fb[1]);
-            if constexpr (kJ > 1) mma16816(acc[j + 1], fa, fb[2], fb[3]);
-          } else if (j < jt) {
-            uint32_t fb[2];
-            if constexpr (kTrans) ldsm2<true>(fb, sp + ((ks * 16 + (lane & 15)) * p_stride + j) * 16);
-            else ldsm2<false>(fb, sp + ((j * 8 + (lane & 7)) * p_stride + 2 * ks + ((lane >> 3) & 1)) * 16);
-            mma16816(acc[j], fa, fb[0], fb[1]);
+          for (int j = 0; j < kJ; j += 2) {
+            if (j + 1 < jt) {
+              uint32_t fb[4];
+              ldsm4<true>(fb, sp + (ks * 16 + (lane & 15)) * p_stride + (j + (lane >> 4)) * 16);
+              mma16816(acc[j], fa, fb[0], fb[1]);
+              mma16816(acc[j + 1], fa, fb[2], fb[3]);
+            } else if (j < jt) {
+              uint32_t fb[2];
+              ldsm2<true>(fb, sp + (ks * 16 + (lane & 15)) * p_stride + j * 16);
+              mma16816(acc[j], fa, fb[0], fb[1]);
+            }
           }
         }
       }
+      if (++stage == p.stages) stage = 0;
     }
-    cp_wait<0>();
+    // Join the warps that shared a row tile, in order; the first of them writes [rows][r].
+    const int ra = wm * 16 + (lane >> 2), rb = ra + 8;
+    if (wk > 0) {
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+        if (j < jt) {
+          float* at = red + ((wk - 1) * kRows + ra) * p.r + j * 8 + 2 * (lane & 3);
+          *reinterpret_cast<float2*>(at) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(at + 8 * p.r) = make_float2(acc[j][2], acc[j][3]);
+        }
+    }
     __syncthreads();
-    // Join the warps that shared a row tile (in order) and write [rows][r].
-    float* red = reinterpret_cast<float*>(smem);   // [kWk][kRows][r]
+    if (wk == 0) {
+      float* out = p.part + static_cast<int64_t>(blockIdx.y) * p.M * p.r;
+      const int64_t row_a = ra < rows ? row0 + g.order[first + ra] : -1, row_b = rb < rows ? row0 + g.order[first + rb] : -1;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+        if (j < jt) {
+          const int col = j * 8 + 2 * (lane & 3);
+          float2 va = make_float2(acc[j][0], acc[j][1]), vb = make_float2(acc[j][2], acc[j][3]);
+#pragma unroll
+          for (int w = 0; w < kWk - 1; ++w) {
+            const float2 ua = *reinterpret_cast<const float2*>(red + (w * kRows + ra) * p.r + col);
+            const float2 ub = *reinterpret_cast<const float2*>(red + (w * kRows + rb) * p.r + col);
+            va.x += ua.x;
+            va.y += ua.y;
+            vb.x += ub.x;
+            vb.y += ub.y;
+          }
+          if (row_a >= 0) *reinterpret_cast<float2*>(out + row_a * p.r + col) = va;
+          if (row_b >= 0) *reinterpret_cast<float2*>(out + row_b * p.r + col) = vb;
+        }
+    }
+    __syncthreads();
+  }
+}
+
+// The forward shrink: P = A, whose rows run along the contraction.  Each warp takes 32 elements of
+// it at a time: lane (g, q) loads elements 8 q .. 8 q + 7 of row g of the adapter (for each
+// eight of the rank) and of the rows g and g + 8 of src; the halves of these 16 bytes are the
+// fragments of two MMAs.
+template <int kJ>   // 8-column tiles of the rank, at most
+__global__ void __launch_bounds__(kThreads) rfq_lora_shrink_direct_kernel(const ShrinkParams p) {
+  __shared__ __align__(16) Groups g;
+  __shared__ float red[4][16][kJ * 8];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
+  const int z = static_cast<int>(blockIdx.x % p.zs);
+  group_rows<kRows>(g, p.ids, row0, p.M, p.n);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int jt = p.r / 8, quad = lane & 3, line = lane >> 2;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * p.c_split;
+  const int64_t c1 = min(p.C, c0 + p.c_split);
+  for (int item = z; item < g.items; item += p.zs) {
+    const int first = g.start[item], rows = g.start[item + 1] - first;
+    const int a = g.ids[g.order[first]];
+    if (a == INT_MAX) break;   // rows without an adapter come last
+    const bool has_a = line < rows, has_b = line + 8 < rows;
+    const int64_t row_a = row0 + g.order[first + (has_a ? line : 0)], row_b = row0 + g.order[first + (has_b ? line + 8 : 0)];
+    const __nv_bfloat16* xa = p.src + row_a * p.C;
+    const __nv_bfloat16* xb = p.src + row_b * p.C;
+    const __nv_bfloat16* pa = p.p + (static_cast<int64_t>(a) * p.r + line) * p.C;
+    float acc[kJ][4];
 #pragma unroll
     for (int j = 0; j < kJ; ++j)
-      if (j < jt) {
-        const int col = j * 8 + 2 * (lane & 3);
-        float* at = red + (static_cast<int64_t>(wk) * kRows + wm * 16 + (lane >> 2)) * p.r + col;
-        *reinterpret_cast<float2*>(at) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(at + 8 * p.r) = make_float2(acc[j][2], acc[j][3]);
-      }
-    __syncthreads();
-    for (int i = tid; i < rows * p.r; i += kThreads) {
-      const int m = i / p.r, j = i - m * p.r;
-      float v = red[i];
 #pragma unroll
-      for (int w = 1; w < T::kWk; ++w) v += red[w * kRows * p.r + i];
-      p.part[(static_cast<int64_t>(blockIdx.y) * p.M + row_of[m]) * p.r + j] = v;
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll 2
+    for (int64_t c = c0 + 32 * warp + 8 * quad; c < c1 + 8 * quad; c += 8 * 32) {
+      const bool ok = c < c1;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 ua = ok && has_a ? *reinterpret_cast<const uint4*>(xa + c) : zero;
+      const uint4 ub = ok && has_b ? *reinterpret_cast<const uint4*>(xb + c) : zero;
+      const uint32_t f0[4] = {ua.x, ub.x, ua.y, ub.y}, f1[4] = {ua.z, ub.z, ua.w, ub.w};
+      uint4 w[kJ];
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) w[j] = ok && j < jt ? *reinterpret_cast<const uint4*>(pa + 8 * j * p.C + c) : zero;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+        if (j < jt) {
+          mma16816(acc[j], f0, w[j].x, w[j].y);
+          mma16816(acc[j], f1, w[j].z, w[j].w);
+        }
+    }
+    // Join the warps, four and four, then the others to the first, which writes [rows][r].
+    auto give = [&](int slot) {
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const int col = j * 8 + 2 * quad;
+        *reinterpret_cast<float2*>(&red[slot][line][col]) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2*>(&red[slot][line + 8][col]) = make_float2(acc[j][2], acc[j][3]);
+      }
+    };
+    auto take = [&](int slot) {
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const int col = j * 8 + 2 * quad;
+        const float2 ua = *reinterpret_cast<const float2*>(&red[slot][line][col]);
+        const float2 ub = *reinterpret_cast<const float2*>(&red[slot][line + 8][col]);
+        acc[j][0] += ua.x;
+        acc[j][1] += ua.y;
+        acc[j][2] += ub.x;
+        acc[j][3] += ub.y;
+      }
+    };
+    if (warp >= 4) give(warp - 4);
+    __syncthreads();
+    if (warp < 4) take(warp);
+    __syncthreads();
+    if (warp > 0 && warp < 4) give(warp);
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < 4; ++w) take(w);
+      float* out = p.part + static_cast<int64_t>(blockIdx.y) * p.M * p.r;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+        if (j < jt) {
+          const int col = j * 8 + 2 * quad;
+          if (has_a) *reinterpret_cast<float2*>(out + row_a * p.r + col) = make_float2(acc[j][0], acc[j][1]);
+          if (has_b) *reinterpret_cast<float2*>(out + row_b * p.r + col) = make_float2(acc[j][2], acc[j][3]);
+        }
     }
     __syncthreads();
   }
@@ -278,6 +437,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
 // s'[m][j] = scale_a * sum of the splits, in order.
 __device__ __forceinline__ float join_parts(const float* part, int splits, int64_t stride, int64_t at, float scale) {
   float v = part[at];
+#pragma unroll 4
   for (int s = 1; s < splits; ++s) v += part[s * stride + at];
   return v * scale;
 }
@@ -292,41 +452,52 @@ __device__ __forceinline__ void split_terms(float v, __nv_bfloat16 (&t)[kT]) {
 }
 
 // ---------------------------------------------------------------- expand
-// out[m][c] = base[m][c] + sum_j s'[m][j] Q_a, Q = B (rows c, j along the row) or, kTrans, A
-// (rows j, c along the row).
+// out[m][c] = base[m][c] + sum_j s'[m][j] Q_a, Q = B (rows c, j along the row; the direct kernel)
+// or A^T (rows j, c along the row).  There a stage holds a [kRows][kBN] tile of the base and the adapter's
+// weights for its columns; the sum is formed in place and copied out from there, in whole row pieces.
 struct ExpandParams {
   const float* part;          // [splits][M][r]
   const float* scale;         // [n]
-  const __nv_bfloat16* q;     // [n][C][r] or [n][r][C]
+  const __nv_bfloat16* q;     // [n][C][r] (direct) or [n][r][C]
   const int* ids;
   const void* base;           // [M][C] or nullptr
   void* out;                  // [M][C]
   float* hidden;              // [M][r] or nullptr
   int64_t M, C;
   int n, r, splits, zs;
+  int tiles;                  // column tiles of one CTA (of 32 columns in the direct kernel)
+  int stages;
 };
 
-constexpr int kExpandCols = 256;
-template <bool kTrans>
-__host__ __device__ constexpr int expand_q_bytes(int r) {
-  const int r16 = (r + 15) / 16 * 16;
-  return kTrans ? r16 * odd_stride(kExpandCols / 8) * 16 : kExpandCols * odd_stride(r16 / 8) * 16;
+// Columns of one tile: 256 bytes of a row.
+template <bool kF32>
+constexpr int kBN = kF32 ? 64 : 128;
+template <bool kF32>
+constexpr int kQStride = odd_stride(kBN<kF32> * 2);
+template <bool kF32>
+__host__ __device__ constexpr int expand_stage_bytes(int r) {
+  return kRows * kRowStride + r * kQStride<kF32>;
 }
-template <int kRows, int kT>
+// The rank-r vector enters the MMA in bf16: one term (2^-8 of the adapter's share, below the
+// rounding of a bf16 output) or, for an fp32 output, three (24 bits).
+template <bool kF32>
+constexpr int kExpandTerms = kF32 ? 3 : 1;
+template <bool kF32>
 __host__ __device__ constexpr int expand_s_bytes(int r) {
-  return kT * kRows * odd_stride((r + 15) / 16 * 2) * 16;
+  return kExpandTerms<kF32> * kRows * odd_stride(2 * r);
 }
 
-template <int kRows, bool kTrans, bool kF32>
+template <bool kF32>
 __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandParams p) {
-  // The rank-r vector enters the MMA in bf16: one term (2^-8 of the adapter's share, below the
-  // rounding of a bf16 output) or, for an fp32 output, three (24 bits).
-  constexpr int kT = kF32 ? 3 : 1;
+  constexpr int kT = kExpandTerms<kF32>;
   constexpr int kWm = kRows / 16, kWn = 8 / kWm;
-  constexpr int kWarpCols = kExpandCols / kWn;
+  constexpr int kCols = kBN<kF32>;
+  constexpr int kWarpCols = kCols / kWn;
+  constexpr int kPairs = kWarpCols >= 16 ? 2 : 1;      // 8-column tiles a warp takes at once
+  constexpr int kSize = kF32 ? 4 : 2;
+  constexpr int kCopies = kRows / 16;                  // row pieces of 16 bytes a thread copies per tile
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Groups g;
-  __shared__ int64_t row_of[kRows];
+  __shared__ __align__(16) Groups g;
   griddep_launch_dependents();
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
@@ -335,186 +506,321 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wm = warp % kWm, wn = warp / kWm;
-  const int r16 = (p.r + 15) / 16 * 16;
-  const int q_stride = kTrans ? odd_stride(kExpandCols / 8) : odd_stride(r16 / 8);
-  const int s_stride = odd_stride(r16 / 8);
-  const uint32_t sq = smem_addr(smem);
-  uint8_t* s_bytes = smem + expand_q_bytes<kTrans>(p.r);
-  const uint32_t ss = smem_addr(s_bytes);
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kExpandCols;
-  const int cols = static_cast<int>(min(static_cast<int64_t>(kExpandCols), p.C - c0));
+  constexpr int q_stride = kQStride<kF32>;
+  const int s_stride = odd_stride(2 * p.r);
+  const int stage_bytes = expand_stage_bytes<kF32>(p.r);
+  uint8_t* s_mem = smem + p.stages * stage_bytes;
+  const uint32_t base = smem_addr(smem), s_base = smem_addr(s_mem);
+  const int64_t begin = static_cast<int64_t>(blockIdx.y) * p.tiles * kCols;
+  const int64_t end = min(p.C, begin + static_cast<int64_t>(p.tiles) * kCols);
+  const int iters = static_cast<int>(ceil_div(end - begin, kCols));
+  const int qx = tid & 15;
+  constexpr int kPiece = 16 / kSize;                   // columns of a 16-byte piece
+  const uint8_t* from = static_cast<const uint8_t*>(p.base);
+  uint8_t* to = static_cast<uint8_t*>(p.out);
 
   for (int item = z; item < g.items; item += p.zs) {
     const int first = g.start[item], rows = g.start[item + 1] - first;
     const int a = g.ids[g.order[first]];
     const bool with = a != INT_MAX;
-    for (int i = tid; i < kRows; i += kThreads) row_of[i] = i < rows ? row0 + g.order[first + i] : -1;
-    __syncthreads();
-    if (with) {
-      if constexpr (kTrans) {
-        const __nv_bfloat16* qa = p.q + static_cast<int64_t>(a) * p.r * p.C;
-        for (int i = tid; i < r16 * (kExpandCols / 8); i += kThreads) {
-          const int j = i / (kExpandCols / 8), c = i % (kExpandCols / 8);
-          const bool ok = j < p.r && 8 * c < cols;
-          cp_async16(sq + (j * q_stride + c) * 16, ok ? qa + j * p.C + c0 + 8 * c : p.q, ok);
-        }
-      } else {
-        const __nv_bfloat16* qa = p.q + (static_cast<int64_t>(a) * p.C + c0) * p.r;
-        const int jc = r16 / 8;
-        for (int i = tid; i < kExpandCols * jc; i += kThreads) {
-          const int c = i / jc, j = i - c * jc;
-          const bool ok = c < cols && 8 * j < p.r;
-          cp_async16(sq + (c * q_stride + j) * 16, ok ? qa + static_cast<int64_t>(c) * p.r + 8 * j : p.q, ok);
+    if (p.hidden != nullptr && blockIdx.y == 0 && !with)
+      for (int i = tid; i < rows * p.r; i += kThreads) p.hidden[(row0 + g.order[first + i / p.r]) * p.r + i % p.r] = 0.f;
+    // Rows without an adapter (they come last) keep what they have where the base is the output itself.
+    if (!with && p.base == p.out) continue;
+    int64_t at[kCopies];        // byte offset of this thread's pieces, in the base and in the output
+    unsigned has = 0;
+#pragma unroll
+    for (int u = 0; u < kCopies; ++u) {
+      const int m = (tid >> 4) + 16 * u;
+      has |= static_cast<unsigned>(m < rows) << u;
+      at[u] = ((row0 + g.order[m < rows ? first + m : first]) * p.C + begin) * kSize + 16 * qx;
+    }
+    const __nv_bfloat16* qa = p.q + (with ? static_cast<int64_t>(a) * p.r * p.C : 0);
+    int load_stage = 0, load_it = 0;
+    auto load = [&]() {
+      if (load_it < iters) {
+        const uint32_t sb = base + load_stage * stage_bytes, sq = sb + kRows * kRowStride;
+        const int left = static_cast<int>(min(static_cast<int64_t>(kCols), end - begin - static_cast<int64_t>(load_it) * kCols));
+        if (from != nullptr)
+#pragma unroll
+          for (int u = 0; u < kCopies; ++u) {
+            const bool ok = (has >> u & 1u) && kPiece * qx < left;
+            cp_async16(sb + ((tid >> 4) + 16 * u) * kRowStride + 16 * qx, ok ? from + at[u] + load_it * 256 : from, ok);
+          }
+        if (with) {
+          const int64_t c = begin + static_cast<int64_t>(load_it) * kCols;
+          constexpr int kQ = kCols / 8;
+          for (int i = tid; i < p.r * kQ; i += kThreads) {
+            const int j = i / kQ, q = i % kQ;
+            const bool ok = 8 * q < left;
+            cp_async16(sq + j * q_stride + 16 * q, ok ? qa + j * p.C + c + 8 * q : p.q, ok);
+          }
         }
       }
       cp_commit();
+      ++load_it;
+      if (++load_stage == p.stages) load_stage = 0;
+    };
+    for (int it = 0; it < p.stages - 1; ++it) load();
+    if (with) {
       const float scale = p.scale[a];
-      for (int i = tid; i < kRows * r16; i += kThreads) {
-        const int m = i / r16, j = i - m * r16;
-        float v = 0.f;
-        if (m < rows && j < p.r) {
-          v = join_parts(p.part, p.splits, p.M * p.r, row_of[m] * p.r + j, scale);
-          if (p.hidden != nullptr && blockIdx.y == 0) p.hidden[row_of[m] * p.r + j] = v;
-        }
+      for (int i = tid; i < rows * p.r; i += kThreads) {
+        const int m = i / p.r, j = i - m * p.r;
+        const int64_t sat = (row0 + g.order[first + m]) * p.r + j;
+        const float v = join_parts(p.part, p.splits, p.M * p.r, sat, scale);
+        if (p.hidden != nullptr && blockIdx.y == 0) p.hidden[sat] = v;
         __nv_bfloat16 t[kT];
         split_terms<kT>(v, t);
 #pragma unroll
-        for (int e = 0; e < kT; ++e)
-          *reinterpret_cast<__nv_bfloat16*>(s_bytes + ((e * kRows + m) * s_stride * 16) + 2 * j) = t[e];
+        for (int e = 0; e < kT; ++e) *reinterpret_cast<__nv_bfloat16*>(s_mem + (e * kRows + m) * s_stride + 2 * j) = t[e];
       }
-      cp_wait<0>();
-    } else if (p.hidden != nullptr && blockIdx.y == 0) {
-      for (int i = tid; i < rows * p.r; i += kThreads) p.hidden[row_of[i / p.r] * p.r + i % p.r] = 0.f;
     }
-    __syncthreads();
-    if (with || p.base != p.out) {
-      // Each thread ends up with 8 neighbouring columns of two rows (16 bytes of bf16): it holds
-      // two columns of each of four 8-column tiles, and the four lanes of a quad exchange them.
-      const int quad = lane & 3;
-      const int64_t row_a = row_of[wm * 16 + (lane >> 2)], row_b = row_of[wm * 16 + 8 + (lane >> 2)];
-      // Before the loop over column groups: whether this thread has rows at all.
-#pragma unroll 2
-      for (int gcol = wn * kWarpCols; gcol < (wn + 1) * kWarpCols; gcol += 32) {
-        if (gcol >= cols) break;
-        const int col = gcol + 8 * quad;
-        const bool col_ok = col < cols;
-        float base_a[8], base_b[8];
-        auto load_base = [&](float (&f)[8], int64_t row) {
+    int stage = 0;
+    for (int it = 0; it < iters; ++it) {
+      cp_wait_stage(p.stages);
+      __syncthreads();
+      load();
+      uint8_t* sb = smem + stage * stage_bytes;
+      const uint32_t sq = base + stage * stage_bytes + kRows * kRowStride;
+      const int left = static_cast<int>(min(static_cast<int64_t>(kCols), end - begin - static_cast<int64_t>(it) * kCols));
+      if (wm * 16 < rows && (with || from == nullptr)) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = 0.f;
-          if (p.base == nullptr || row < 0 || !col_ok) return;
-          const int64_t at = row * p.C + c0 + col;
+        for (int col = wn * kWarpCols; col < (wn + 1) * kWarpCols; col += 8 * kPairs) {
+          if (col >= left) break;
+          float acc[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+          if (with) {
+            int ks = 0;
+            for (; ks < p.r / 16; ++ks) {
+              uint32_t fb[4];
+              if constexpr (kPairs == 2) {
+                ldsm4<true>(fb, sq + (ks * 16 + (lane & 15)) * q_stride + col * 2 + (lane >> 4) * 16);
+              } else {
+                uint32_t f2[2];
+                ldsm2<true>(f2, sq + (ks * 16 + (lane & 15)) * q_stride + col * 2);
+                fb[0] = f2[0];
+                fb[1] = f2[1];
+              }
+#pragma unroll
+              for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
+                uint32_t fa[4];
+                ldsm4<false>(fa, s_base + (e * kRows + wm * 16 + (lane & 15)) * s_stride + 32 * ks + (lane >> 4) * 16);
+                mma16816(acc[0], fa, fb[0], fb[1]);
+                if constexpr (kPairs == 2) mma16816(acc[1], fa, fb[2], fb[3]);
+              }
+            }
+            if (p.r & 8) {   // the last eight of the rank
+              uint32_t fb[2];
+              // With one 8-column tile both halves of the load read it.
+              ldsm2<true>(fb, sq + (ks * 16 + (lane & 7)) * q_stride + col * 2 + (kPairs == 2 ? (lane >> 3) & 1 : 0) * 16);
+#pragma unroll
+              for (int e = kT - 1; e >= 0; --e) {
+                uint32_t fa[2];
+                ldsm2<false>(fa, s_base + (e * kRows + wm * 16 + (lane & 15)) * s_stride + 32 * ks);
+                mma1688(acc[0], fa, fb[0]);
+                if constexpr (kPairs == 2) mma1688(acc[1], fa, fb[1]);
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint8_t* o = sb + (wm * 16 + 8 * h + (lane >> 2)) * kRowStride + (col + 8 * i + 2 * (lane & 3)) * kSize;
+              float x = acc[i][2 * h], y = acc[i][2 * h + 1];
+              if constexpr (kF32) {
+                if (from != nullptr) {
+                  const float2 b = *reinterpret_cast<const float2*>(o);
+                  x += b.x;
+                  y += b.y;
+                }
+                *reinterpret_cast<float2*>(o) = make_float2(x, y);
+              } else {
+                if (from != nullptr) {
+                  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o));
+                  x += b.x;
+                  y += b.y;
+                }
+                *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(x, y);
+              }
+            }
+        }
+      }
+      __syncthreads();
+      if (kPiece * qx < left)
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u)
+          if (has >> u & 1u)
+            *reinterpret_cast<uint4*>(to + at[u] + it * 256) = *reinterpret_cast<const uint4*>(sb + ((tid >> 4) + 16 * u) * kRowStride + 16 * qx);
+      if (++stage == p.stages) stage = 0;
+    }
+    __syncthreads();   // the next group's copies and s' go where this one's were
+  }
+}
+
+// The forward expand: Q = B, whose rows run along the rank.  A warp takes 32 columns at a time as
+// four 8-column tiles whose columns are interleaved, so that lane (g, q) ends up with columns
+// 8 q .. 8 q + 7 of the rows g and g + 8: 16 bytes of bf16.
+template <bool kF32>
+__global__ void __launch_bounds__(kThreads) rfq_lora_expand_direct_kernel(const ExpandParams p) {
+  constexpr int kT = kExpandTerms<kF32>;
+  __shared__ __align__(16) Groups g;
+  __shared__ __align__(16) __nv_bfloat16 sm[kT][kRows][RFQ_LORA_MAX_RANK + 8];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
+  const int z = static_cast<int>(blockIdx.x % p.zs);
+  group_rows<kRows>(g, p.ids, row0, p.M, p.n);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3, line = lane >> 2;
+  const int64_t begin = static_cast<int64_t>(blockIdx.y) * p.tiles * 32;
+  const int64_t end = min(p.C, begin + static_cast<int64_t>(p.tiles) * 32);
+  for (int item = z; item < g.items; item += p.zs) {
+    const int first = g.start[item], rows = g.start[item + 1] - first;
+    const int a = g.ids[g.order[first]];
+    const bool with = a != INT_MAX;
+    if (p.hidden != nullptr && blockIdx.y == 0 && !with)
+      for (int i = tid; i < rows * p.r; i += kThreads) p.hidden[(row0 + g.order[first + i / p.r]) * p.r + i % p.r] = 0.f;
+    // Rows without an adapter (they come last) keep what they have where the base is the output itself.
+    if (!with && p.base == p.out) continue;
+    if (with) {
+      const float scale = p.scale[a];
+      for (int i = tid; i < rows * p.r; i += kThreads) {
+        const int m = i / p.r, j = i - m * p.r;
+        const int64_t at = (row0 + g.order[first + m]) * p.r + j;
+        const float v = join_parts(p.part, p.splits, p.M * p.r, at, scale);
+        if (p.hidden != nullptr && blockIdx.y == 0) p.hidden[at] = v;
+        __nv_bfloat16 t[kT];
+        split_terms<kT>(v, t);
+#pragma unroll
+        for (int e = 0; e < kT; ++e) sm[e][m][j] = t[e];
+      }
+      __syncthreads();
+    }
+    const bool has[2] = {line < rows, line + 8 < rows};
+    const int64_t row[2] = {row0 + g.order[first + (has[0] ? line : 0)], row0 + g.order[first + (has[1] ? line + 8 : 0)]};
+    // Column of this lane's fragment row in tile i: 8 (g / 2) + 2 i + (g & 1).
+    const __nv_bfloat16* qa = with ? p.q + (static_cast<int64_t>(a) * p.C + 8 * (line >> 1) + (line & 1)) * p.r : p.q;
+    for (int64_t c = begin + 32 * warp; c < end; c += 8 * 32) {
+      const int64_t col = c + 8 * quad;
+      float f[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[h][e] = 0.f;
+        if (p.base != nullptr && has[h] && col < p.C) {
           if constexpr (kF32) {
-            const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p.base) + at);
-            const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.base) + at + 4);
-            f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
-            f[4] = w.x; f[5] = w.y; f[6] = w.z; f[7] = w.w;
+            const float* b = static_cast<const float*>(p.base) + row[h] * p.C + col;
+            const float4 u = *reinterpret_cast<const float4*>(b), w = *reinterpret_cast<const float4*>(b + 4);
+            f[h][0] = u.x; f[h][1] = u.y; f[h][2] = u.z; f[h][3] = u.w;
+            f[h][4] = w.x; f[h][5] = w.y; f[h][6] = w.z; f[h][7] = w.w;
           } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.base) + at);
+            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.base) + row[h] * p.C + col);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              f[2 * e] = __uint_as_float(w[e] << 16);
-              f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+              f[h][2 * e] = __uint_as_float(w[e] << 16);
+              f[h][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
             }
-          }
-        };
-        load_base(base_a, row_a);
-        load_base(base_b, row_b);
-        if (with) {
-          float acc[4][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-          for (int ks = 0; ks < r16 / 16; ++ks) {
-            uint32_t fb[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c = gcol + 16 * h;
-              if constexpr (kTrans) ldsm4<true>(fb[h], sq + ((ks * 16 + (lane & 15)) * q_stride + c / 8 + (lane >> 4)) * 16);
-              else ldsm4<false>(fb[h], sq + ((c + (lane & 7) + ((lane >> 4) << 3)) * q_stride + 2 * ks + ((lane >> 3) & 1)) * 16);
-            }
-#pragma unroll
-            for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
-              uint32_t fa[4];
-              ldsm4<false>(fa, ss + ((e * kRows + wm * 16 + (lane & 15)) * s_stride + 2 * ks + (lane >> 4)) * 16);
-              mma16816(acc[0], fa, fb[0][0], fb[0][1]);
-              mma16816(acc[1], fa, fb[0][2], fb[0][3]);
-              mma16816(acc[2], fa, fb[1][0], fb[1][1]);
-              mma16816(acc[3], fa, fb[1][2], fb[1][3]);
-            }
-          }
-          // 4 x 4 exchange inside each quad: lane q gives tile i to lane i and gets tile q from all.
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // In step d lane q sends the pair of tile q ^ d and receives that of its own tile from lane q ^ d.
-            const int from = quad ^ i;
-            float send[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              send[e] = from == 0 ? acc[0][e] : from == 1 ? acc[1][e] : from == 2 ? acc[2][e] : acc[3][e];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) send[e] = __shfl_xor_sync(0xffffffffu, send[e], i);
-            // `from` is also the lane it came from: columns 2 * from, 2 * from + 1 of the tile.
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (from == k) {
-                base_a[2 * k] += send[0];
-                base_a[2 * k + 1] += send[1];
-                base_b[2 * k] += send[2];
-                base_b[2 * k + 1] += send[3];
-              }
           }
         }
-        auto store = [&](const float (&f)[8], int64_t row) {
-          if (row < 0 || !col_ok) return;
-          const int64_t at = row * p.C + c0 + col;
+      }
+      if (with) {
+        float acc[4][4];
+        bool ok[4];
+        const __nv_bfloat16* q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+          ok[i] = c + 8 * (line >> 1) + 2 * i + (line & 1) < p.C;
+          q[i] = qa + (c + 2 * i) * p.r;
+        }
+        int k = 0;
+#pragma unroll 2
+        for (; k + 16 <= p.r; k += 16) {
+          uint2 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = ok[i] ? *reinterpret_cast<const uint2*>(q[i] + k + 4 * quad) : make_uint2(0u, 0u);
+#pragma unroll
+          for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
+            const uint2 sa = *reinterpret_cast<const uint2*>(&sm[e][line][k + 4 * quad]);
+            const uint2 sb = *reinterpret_cast<const uint2*>(&sm[e][line + 8][k + 4 * quad]);
+            const uint32_t fa[4] = {sa.x, sb.x, sa.y, sb.y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma16816(acc[i], fa, w[i].x, w[i].y);
+          }
+        }
+        if (k < p.r) {   // the last eight of the rank
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = ok[i] ? *reinterpret_cast<const uint32_t*>(q[i] + k + 2 * quad) : 0u;
+#pragma unroll
+          for (int e = kT - 1; e >= 0; --e) {
+            const uint32_t fa[2] = {*reinterpret_cast<const uint32_t*>(&sm[e][line][k + 2 * quad]),
+                                    *reinterpret_cast<const uint32_t*>(&sm[e][line + 8][k + 2 * quad])};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma1688(acc[i], fa, w[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[0][2 * i] += acc[i][0];
+          f[0][2 * i + 1] += acc[i][1];
+          f[1][2 * i] += acc[i][2];
+          f[1][2 * i + 1] += acc[i][3];
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (has[h] && col < p.C) {
           if constexpr (kF32) {
-            float* o = static_cast<float*>(p.out) + at;
-            *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4*>(o + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            float* o = static_cast<float*>(p.out) + row[h] * p.C + col;
+            *reinterpret_cast<float4*>(o) = make_float4(f[h][0], f[h][1], f[h][2], f[h][3]);
+            *reinterpret_cast<float4*>(o + 4) = make_float4(f[h][4], f[h][5], f[h][6], f[h][7]);
           } else {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-              w[e] = *reinterpret_cast<uint32_t*>(&b);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(f[h][2 * e], f[h][2 * e + 1]);
+              w[e] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row[h] * p.C + col) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        };
-        store(base_a, row_a);
-        store(base_b, row_b);
-      }
+        }
     }
-    __syncthreads();
+    __syncthreads();   // the next group's s' goes where this one's was
   }
 }
 
 // ---------------------------------------------------------------- split
-// The rank-r vectors as bf16 terms [term][M][r]: ds' from its partial sums, s' as saved by the
-// forward pass.  Rows without an adapter are never read by what follows.
+// The rank-r vectors as bf16 terms [M][term][r]: ds' from its partial sums (scale nullptr: they are
+// scaled already), s' as saved by the forward pass.  Rows without an adapter are never read by what follows.
 template <int kT>
-__global__ void __launch_bounds__(kThreads) rfq_lora_split_kernel(const float* part, const float* scale, const int* ids, int n, int64_t M,
-                                                                  int r, int splits, __nv_bfloat16* ds, const float* hidden,
-                                                                  __nv_bfloat16* s) {
+__global__ void __launch_bounds__(kThreads) rfq_lora_split_kernel(const float* part, const float* scale, const int* ids, int n,
+                                                                       int64_t M, int r, int splits, __nv_bfloat16* ds,
+                                                                       const float* hidden, __nv_bfloat16* s) {
   griddep_launch_dependents();
   griddep_wait();
   const int64_t total = M * r;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int a = ids[i / r];
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t m = i / r;
+    const int a = ids[m];
     if (a < 0 || a >= n) continue;
+    const int64_t at = m * kT * r + (i - m * r);
     __nv_bfloat16 t[kT];
     if (ds != nullptr) {
-      split_terms<kT>(join_parts(part, splits, total, i, scale[a]), t);
+      split_terms<kT>(join_parts(part, splits, total, i, scale != nullptr ? scale[a] : 1.f), t);
 #pragma unroll
-      for (int e = 0; e < kT; ++e) ds[e * total + i] = t[e];
+      for (int e = 0; e < kT; ++e) ds[at + e * r] = t[e];
     }
     if (s != nullptr) {
       split_terms<kT>(hidden[i], t);
 #pragma unroll
-      for (int e = 0; e < kT; ++e) s[e * total + i] = t[e];
+      for (int e = 0; e < kT; ++e) s[at + e * r] = t[e];
     }
   }
 }
@@ -523,12 +829,12 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_split_kernel(const float* p
 // part[range][a][j][c] = sum over the range's rows of adapter a of v[m][j] w[m][c], for the two
 // pairs (v, w) = (ds', x) and (s', dy).
 constexpr int kOuterCols = 128;
-constexpr int kOuterRows = 32;        // rows of one stage
+constexpr int kOuterRows = 64;        // rows of one stage
 constexpr int kMaxRange = 4096;       // rows of one range
 constexpr int kMaxAdapters = 4096;
 
 struct OuterSide {
-  const __nv_bfloat16* v;     // [term][M][r]
+  const __nv_bfloat16* v;     // [M][term][r]
   const __nv_bfloat16* w;     // [M][C]
   float* part;                // [ranges][n][r][C]
   int64_t C;
@@ -540,11 +846,17 @@ struct OuterParams {
   int* present;               // [ranges][n]
   int64_t M;
   int n, r, range;            // range: rows of one range
+  int stages;
 };
 
+constexpr int kWStride = odd_stride(kOuterCols * 2);
+template <int kT>
+__host__ __device__ constexpr int outer_v_stride(int r) {
+  return odd_stride(kT * r * 2);
+}
 template <int kT>
 __host__ __device__ constexpr int outer_stage_bytes(int r) {
-  return kOuterRows * odd_stride(kOuterCols / 8) * 16 + kT * kOuterRows * odd_stride((r + 15) / 16 * 2) * 16;
+  return kOuterRows * (kWStride + outer_v_stride<kT>(r));
 }
 
 template <int kJ16, int kT>   // kJ16: 16-row tiles of the rank, at most
@@ -558,20 +870,20 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
   griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int tile = static_cast<int>(blockIdx.x);
-  const int which = tile >= p.side[0].tiles;
-  if (which) tile -= p.side[0].tiles;
-  const OuterSide s = which ? p.side[1] : p.side[0];
+  const bool second = tile >= p.side[0].tiles;
+  if (second) tile -= p.side[0].tiles;
+  const OuterSide s = second ? p.side[1] : p.side[0];
   const int range = static_cast<int>(blockIdx.y);
   const int64_t row0 = static_cast<int64_t>(range) * p.range;
   const int count = static_cast<int>(min(static_cast<int64_t>(p.range), p.M - row0));
   const int64_t c0 = static_cast<int64_t>(tile) * kOuterCols;
-  const int r16 = (p.r + 15) / 16 * 16;
-  const int j16 = r16 / 16;
-  constexpr int kWStride = odd_stride(kOuterCols / 8);
-  const int v_stride = odd_stride(r16 / 8);
-  constexpr int kWBytes = kOuterRows * kWStride * 16;
+  const int v_stride = outer_v_stride<kT>(p.r);
+  const int v_pieces = kT * p.r / 8;            // 16-byte pieces of a row of v
   const int stage_bytes = outer_stage_bytes<kT>(p.r);
   const uint32_t base = smem_addr(smem);
+  const int j16 = (p.r + 15) / 16;
+  const int qx = tid & 15;
+  const bool qx_ok = c0 + 8 * qx < s.C;
 
   for (int i = tid; i < p.n; i += kThreads) here[i] = 0;
   __syncthreads();
@@ -582,13 +894,13 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
     if (ok) here[id] = 1;
   }
   __syncthreads();
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0 && blockIdx.z == 0)
     for (int i = tid; i < p.n; i += kThreads) p.present[static_cast<int64_t>(range) * p.n + i] = here[i];
 
-  for (int a = 0; a < p.n; ++a) {
+  const int per = static_cast<int>(ceil_div(count, kThreads));
+  for (int a = static_cast<int>(blockIdx.z); a < p.n; a += gridDim.z) {
     if (!here[a]) continue;
     // The rows of this adapter, in order.
-    const int per = static_cast<int>(ceil_div(count, kThreads));
     int mine = 0;
     for (int i = tid * per; i < min(count, (tid + 1) * per); ++i) mine += rid[i] == a;
     int before = mine;
@@ -597,6 +909,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
       const int o = __shfl_up_sync(0xffffffffu, before, d);
       if (lane >= d) before += o;
     }
+    __syncthreads();   // the adapter before this one is done with list, warp_count and the stages
     if (lane == 31) warp_count[warp] = before;
     __syncthreads();
     int total = 0, offset = before - mine;
@@ -609,25 +922,25 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
     __syncthreads();
 
     const int iters = (total + kOuterRows - 1) / kOuterRows;
-    auto load = [&](int it) {
-      if (it < iters) {
-        const uint32_t sw = base + (it % kStages) * stage_bytes, sv = sw + kWBytes;
-        for (int i = tid; i < kOuterRows * (kOuterCols / 8); i += kThreads) {
-          const int m = i / (kOuterCols / 8), q = i % (kOuterCols / 8);
-          const int at = it * kOuterRows + m;
-          const bool ok = at < total && c0 + 8 * q < s.C;
-          cp_async16(sw + (m * kWStride + q) * 16, ok ? s.w + (row0 + list[at]) * s.C + c0 + 8 * q : s.w, ok);
+    int load_stage = 0, load_at = 0;
+    auto load = [&]() {
+      if (load_at < total) {
+        const uint32_t sw = base + load_stage * stage_bytes, sv = sw + kOuterRows * kWStride;
+#pragma unroll
+        for (int u = 0; u < kOuterRows / 16; ++u) {   // rows past the last: zeros
+          const int m = (tid >> 4) + 16 * u;
+          const bool ok = load_at + m < total && qx_ok;
+          cp_async16(sw + m * kWStride + 16 * qx, ok ? s.w + (row0 + list[load_at + m]) * s.C + c0 + 8 * qx : s.w, ok);
         }
-        const int jc = r16 / 8;
-        for (int i = tid; i < kT * kOuterRows * jc; i += kThreads) {
-          const int em = i / jc, j = i - em * jc;
-          const int e = em / kOuterRows, m = em - e * kOuterRows;
-          const int at = it * kOuterRows + m;
-          const bool ok = at < total && 8 * j < p.r;
-          cp_async16(sv + (em * v_stride + j) * 16, ok ? s.v + (e * p.M + row0 + list[at]) * p.r + 8 * j : s.v, ok);
+        for (int i = tid; i < kOuterRows * v_pieces; i += kThreads) {
+          const int m = i / v_pieces, q = i - m * v_pieces;
+          const bool ok = load_at + m < total;
+          cp_async16(sv + m * v_stride + 16 * q, ok ? s.v + (row0 + list[load_at + m]) * kT * p.r + 8 * q : s.v, ok);
         }
       }
       cp_commit();
+      load_at += kOuterRows;
+      if (++load_stage == p.stages) load_stage = 0;
     };
     float acc[kJ16][2][4];
 #pragma unroll
@@ -636,30 +949,33 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][h][e] = 0.f;
-    for (int it = 0; it < kStages - 1; ++it) load(it);
+    for (int it = 0; it < p.stages - 1; ++it) load();
+    int stage = 0;
     for (int it = 0; it < iters; ++it) {
-      cp_wait<kStages - 2>();
+      cp_wait_stage(p.stages);
       __syncthreads();
-      load(it + kStages - 1);
-      const uint32_t sw = base + (it % kStages) * stage_bytes, sv = sw + kWBytes;
+      load();
+      const uint32_t sw = base + stage * stage_bytes, sv = sw + kOuterRows * kWStride;
 #pragma unroll
       for (int ks = 0; ks < kOuterRows / 16; ++ks) {
         uint32_t fb[4];   // w: rows along the contraction; tiles of columns 16 * warp, + 8
-        ldsm4<true>(fb, sw + ((ks * 16 + (lane & 15)) * kWStride + 2 * warp + (lane >> 4)) * 16);
+        ldsm4<true>(fb, sw + (ks * 16 + (lane & 15)) * kWStride + 32 * warp + (lane >> 4) * 16);
 #pragma unroll
         for (int j = 0; j < kJ16; ++j)
           if (j < j16) {
 #pragma unroll
             for (int e = kT - 1; e >= 0; --e) {
-              uint32_t fa[4];   // v^T: 16 of the rank x 16 rows
-              ldsm4<true>(fa, sv + ((e * kOuterRows + ks * 16 + (lane & 7) + ((lane >> 4) << 3)) * v_stride + 2 * j + ((lane >> 3) & 1)) * 16);
+              // v^T: 16 of the rank x 16 rows.  Where the rank ends after 8, the other 8 are whatever
+              // lies behind (inside the stages): their results are not kept.
+              uint32_t fa[4];
+              ldsm4<true>(fa, sv + (ks * 16 + (lane & 7) + ((lane >> 4) << 3)) * v_stride + 2 * e * p.r + 32 * j + ((lane >> 3) & 1) * 16);
               mma16816(acc[j][0], fa, fb[0], fb[1]);
               mma16816(acc[j][1], fa, fb[2], fb[3]);
             }
           }
       }
+      if (++stage == p.stages) stage = 0;
     }
-    cp_wait<0>();
     float* out = s.part + (static_cast<int64_t>(range) * p.n + a) * p.r * s.C;
 #pragma unroll
     for (int j = 0; j < kJ16; ++j)
@@ -672,7 +988,6 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
           if (jb < p.r) *reinterpret_cast<float2*>(out + jb * s.C + c) = make_float2(acc[j][h][2], acc[j][h][3]);
         }
       }
-    __syncthreads();
   }
 }
 
@@ -739,7 +1054,7 @@ constexpr int kPlanSms = 148;   // the cut does not depend on the device that ru
 
 template <class Kernel, class Params>
 cudaError_t launch(Kernel kernel, const Params& p, dim3 grid, size_t smem, cudaStream_t stream) {
-  if (smem > 24 * 1024) {   // with the static part (at most 21 KiB) it may pass the default limit of 48 KiB
+  if (smem > kStaticSmem) {   // with the static part it may pass the default limit of 48 KiB
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
@@ -757,40 +1072,41 @@ cudaError_t launch(Kernel kernel, const Params& p, dim3 grid, size_t smem, cudaS
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Rows of one group: 16 where an adapter has few rows of a batch, else 64.
-int group_size(int64_t M, int64_t n) { return M <= 32 * n || M <= 64 ? 16 : 64; }
+// Stages of a ring: four if two CTAs then share an SM, else as many as fit one (2 to 6).
+int ring_stages(int stage_bytes, int other_bytes) {
+  const int half = (kSmemLimit / 2 - kStaticSmem / 4 - other_bytes) / stage_bytes;
+  if (half >= 3) return half < 4 ? half : 4;
+  const int whole = (kSmemLimit - kStaticSmem - other_bytes) / stage_bytes;
+  return whole < kMaxStages ? whole : kMaxStages;
+}
 
-// Splits of the shrink product's contraction: enough CTAs for four per SM, at least two stages each.
-int shrink_splits(int64_t M, int64_t C, int64_t n, int64_t* c_split, int* zs) {
-  const int rows = group_size(M, n), bk = rows == 16 ? 128 : 64;
+// Whether a batch goes by chunks of 128 neighbouring rows (rfq_lora_wide.cu) or by groups of up to 16
+// rows of one adapter: the latter up to 64 rows, and where an adapter has no more than 32 rows on
+// average, since a chunk is passed over once for each adapter in it.
+bool wide(int64_t M, int64_t n) { return M > 64 && M > 32 * n; }
+
+// CTAs that share the groups of one chunk.
+int64_t chunk_ctas(int64_t M, int64_t most) {
   const int64_t chunks = ceil_div(M, kChunk);
-  // CTAs per chunk: as many as it can have groups, while the chunks alone do not fill the device.
-  int64_t z = ceil_div(M < kChunk ? M : kChunk, rows == 16 ? 1 : rows);
-  while (z > 1 && chunks * z > 2 * kPlanSms) z = (z + 1) / 2;
-  const int64_t most = ceil_div(C, 2 * bk);
-  int64_t s = ceil_div(4 * kPlanSms, chunks * (z < 16 ? z : 16));
+  int64_t z = M <= 32 ? M : ceil_div(M < kChunk ? M : kChunk, 2);
+  while (z > 1 && chunks * z > most) z = (z + 1) / 2;
+  return z;
+}
+
+// Splits of the shrink product's contraction: four CTAs per SM over all, 256 elements each at least.
+int shrink_splits(int64_t M, int64_t C, int64_t* c_split, int* zs) {
+  const int64_t chunks = ceil_div(M, kChunk), z = chunk_ctas(M, 2 * kPlanSms);
+  const int64_t most = ceil_div(C, 256);
+  int64_t s = 4 * kPlanSms / (chunks * z);
   if (s > most) s = most;
   if (s > 32) s = 32;
   if (s < 1) s = 1;
-  *c_split = ceil_div(ceil_div(C, s), bk) * bk;
+  *c_split = ceil_div(ceil_div(C, s), 256) * 256;
   *zs = static_cast<int>(z);
   return static_cast<int>(ceil_div(C, *c_split));
 }
 
-template <int kRows, bool kTrans>
-cudaError_t shrink_rank(const ShrinkParams& p, dim3 grid, cudaStream_t stream) {
-  using T = ShrinkTile<kRows>;
-  size_t smem = static_cast<size_t>(kStages) * (T::kXBytes + shrink_p_bytes<kRows, kTrans>(p.r));
-  const size_t red = static_cast<size_t>(T::kWk) * kRows * p.r * 4;
-  if (red > smem) smem = red;
-  if (p.r <= 16) return launch(rfq_lora_shrink_kernel<kRows, kTrans, 2>, p, grid, smem, stream);
-  if (p.r <= 32) return launch(rfq_lora_shrink_kernel<kRows, kTrans, 4>, p, grid, smem, stream);
-  if (p.r <= 64) return launch(rfq_lora_shrink_kernel<kRows, kTrans, 8>, p, grid, smem, stream);
-  return launch(rfq_lora_shrink_kernel<kRows, kTrans, 16>, p, grid, smem, stream);
-}
-
-template <bool kTrans>
-cudaError_t shrink(const void* src, const void* w, const int* ids, float* part, int64_t M, int64_t C, int64_t n, int64_t r,
+cudaError_t shrink(const void* src, const void* w, bool trans, const int* ids, float* part, int64_t M, int64_t C, int64_t n, int64_t r,
                    int* splits, cudaStream_t stream) {
   ShrinkParams p = {};
   p.src = static_cast<const __nv_bfloat16*>(src);
@@ -801,21 +1117,44 @@ cudaError_t shrink(const void* src, const void* w, const int* ids, float* part, 
   p.C = C;
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
-  *splits = shrink_splits(M, C, n, &p.c_split, &p.zs);
+  *splits = shrink_splits(M, C, &p.c_split, &p.zs);
   const dim3 grid(static_cast<unsigned>(ceil_div(M, kChunk) * p.zs), static_cast<unsigned>(*splits));
-  return group_size(M, n) == 16 ? shrink_rank<16, kTrans>(p, grid, stream) : shrink_rank<64, kTrans>(p, grid, stream);
+  if (!trans) {
+    if (r <= 16) return launch(rfq_lora_shrink_direct_kernel<2>, p, grid, 0, stream);
+    if (r <= 32) return launch(rfq_lora_shrink_direct_kernel<4>, p, grid, 0, stream);
+    if (r <= 64) return launch(rfq_lora_shrink_direct_kernel<8>, p, grid, 0, stream);
+    return launch(rfq_lora_shrink_direct_kernel<16>, p, grid, 0, stream);
+  }
+  const int stage = kRows * kRowStride + shrink_p_bytes(p.r), red = shrink_red_bytes(p.r);
+  p.stages = ring_stages(stage, red);
+  const size_t smem = static_cast<size_t>(p.stages) * stage + red;
+  if (r <= 16) return launch(rfq_lora_shrink_kernel<2>, p, grid, smem, stream);
+  if (r <= 32) return launch(rfq_lora_shrink_kernel<4>, p, grid, smem, stream);
+  if (r <= 64) return launch(rfq_lora_shrink_kernel<8>, p, grid, smem, stream);
+  return launch(rfq_lora_shrink_kernel<16>, p, grid, smem, stream);
 }
 
-template <int kRows, bool kTrans>
-cudaError_t expand_rows(const ExpandParams& p, bool f32, dim3 grid, cudaStream_t stream) {
-  const size_t q = expand_q_bytes<kTrans>(p.r);
-  return f32 ? launch(rfq_lora_expand_kernel<kRows, kTrans, true>, p, grid, q + expand_s_bytes<kRows, 3>(p.r), stream)
-             : launch(rfq_lora_expand_kernel<kRows, kTrans, false>, p, grid, q + expand_s_bytes<kRows, 1>(p.r), stream);
+template <bool kF32>
+cudaError_t expand_typed(ExpandParams p, bool trans, cudaStream_t stream) {
+  const int64_t chunks = ceil_div(p.M, kChunk), z = chunk_ctas(p.M, 2 * kPlanSms);
+  p.zs = static_cast<int>(z);
+  // Column tiles of a CTA: eight CTAs per SM over all for the direct kernel (a tile a warp at least),
+  // two for the other.
+  const int64_t tiles = ceil_div(p.C, trans ? kBN<kF32> : 32);
+  int64_t parts = (trans ? 2 : 8) * kPlanSms / (chunks * z);
+  if (!trans && parts > ceil_div(tiles, 8)) parts = ceil_div(tiles, 8);
+  if (parts > tiles) parts = tiles;
+  if (parts < 1) parts = 1;
+  p.tiles = static_cast<int>(ceil_div(tiles, parts));
+  const dim3 grid(static_cast<unsigned>(chunks * z), static_cast<unsigned>(ceil_div(tiles, p.tiles)));
+  if (!trans) return launch(rfq_lora_expand_direct_kernel<kF32>, p, grid, 0, stream);
+  const int stage = expand_stage_bytes<kF32>(p.r), other = expand_s_bytes<kF32>(p.r);
+  p.stages = ring_stages(stage, other);
+  return launch(rfq_lora_expand_kernel<kF32>, p, grid, static_cast<size_t>(p.stages) * stage + other, stream);
 }
 
-template <bool kTrans>
-cudaError_t expand(const float* part, int splits, const float* scale, const void* w, const int* ids, const void* base, void* out,
-                   bool f32, float* hidden, int64_t M, int64_t C, int64_t n, int64_t r, cudaStream_t stream) {
+cudaError_t expand(const float* part, int splits, const float* scale, const void* w, bool trans, const int* ids, const void* base,
+                   void* out, bool f32, float* hidden, int64_t M, int64_t C, int64_t n, int64_t r, cudaStream_t stream) {
   ExpandParams p = {};
   p.part = part;
   p.scale = scale;
@@ -829,18 +1168,14 @@ cudaError_t expand(const float* part, int splits, const float* scale, const void
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
   p.splits = splits;
-  const int rows = group_size(M, n);
-  const int64_t chunks = ceil_div(M, kChunk), tiles = ceil_div(C, kExpandCols);
-  int64_t z = ceil_div(M < kChunk ? M : kChunk, rows == 16 ? 1 : rows);
-  while (z > 1 && chunks * z * tiles > 4 * kPlanSms) z = (z + 1) / 2;
-  p.zs = static_cast<int>(z);
-  const dim3 grid(static_cast<unsigned>(chunks * z), static_cast<unsigned>(tiles));
-  return rows == 16 ? expand_rows<16, kTrans>(p, f32, grid, stream) : expand_rows<64, kTrans>(p, f32, grid, stream);
+  return f32 ? expand_typed<true>(p, trans, stream) : expand_typed<false>(p, trans, stream);
 }
 
 template <int kT>
-cudaError_t outer_rank(const OuterParams& p, dim3 grid, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(kStages) * outer_stage_bytes<kT>(p.r);
+cudaError_t outer_rank(OuterParams p, dim3 grid, cudaStream_t stream) {
+  const int stage = outer_stage_bytes<kT>(p.r);
+  p.stages = ring_stages(stage, kStaticSmem);
+  const size_t smem = static_cast<size_t>(p.stages) * stage + 64;   // the last row's fragments may reach past its end
   if (p.r <= 16) return launch(rfq_lora_outer_kernel<1, kT>, p, grid, smem, stream);
   if (p.r <= 32) return launch(rfq_lora_outer_kernel<2, kT>, p, grid, smem, stream);
   if (p.r <= 64) return launch(rfq_lora_outer_kernel<4, kT>, p, grid, smem, stream);
@@ -849,9 +1184,9 @@ cudaError_t outer_rank(const OuterParams& p, dim3 grid, cudaStream_t stream) {
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Rows of one range of the outer products: about four CTAs per SM over all column tiles.
+// Rows of one range of the outer products: one wave of two CTAs per SM over all column tiles.
 int outer_range(int64_t M, int64_t tiles) {
-  const int64_t want = ceil_div(4 * kPlanSms, tiles);
+  const int64_t want = ceil_div(2 * kPlanSms, tiles);
   int64_t rows = ceil_div(ceil_div(M, want), kOuterRows) * kOuterRows;
   if (rows < 256) rows = 256;
   if (rows > kMaxRange) rows = kMaxRange;
@@ -867,7 +1202,7 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
   BackwardPlan b;
   int64_t cs;
   int z;
-  const int splits = shrink_splits(M, N, n, &cs, &z);
+  const int splits = wide(M, n) ? 1 : shrink_splits(M, N, &cs, &z);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -891,7 +1226,7 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
 size_t lora_forward_workspace(int64_t M, int64_t K, int64_t r, int64_t n) {
   int64_t cs;
   int z;
-  return align256(static_cast<size_t>(shrink_splits(M, K, n, &cs, &z)) * M * r * 4);
+  return align256(static_cast<size_t>(wide(M, n) ? 1 : shrink_splits(M, K, &cs, &z)) * M * r * 4);
 }
 
 size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
@@ -900,33 +1235,44 @@ size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64
 
 cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* base,
                                 void* y, bool y_bf16, float* hidden, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n,
-                                void* ws, cudaStream_t stream) {
+                                void* ws, int num_sms, void* encode_tiled, cudaStream_t stream) {
   float* part = static_cast<float*>(ws);
   int splits = 1;
-  cudaError_t e = shrink<false>(x, a, ids, part, M, K, n, r, &splits, stream);
+  cudaError_t e;
+  if (wide(M, n)) {
+    float* s = hidden != nullptr ? hidden : part;
+    e = launch_lora_shrink_wide(x, a, false, ids, scale, s, M, K, n, r, num_sms, encode_tiled, stream);
+    if (e != cudaSuccess) return e;
+    return launch_lora_expand_wide(s, b, false, ids, base, y, !y_bf16, M, N, n, r, num_sms, encode_tiled, stream);
+  }
+  e = shrink(x, a, false, ids, part, M, K, n, r, &splits, stream);
   if (e != cudaSuccess) return e;
-  return expand<false>(part, splits, scale, b, ids, base, y, !y_bf16, hidden, M, N, n, r, stream);
+  return expand(part, splits, scale, b, false, ids, base, y, !y_bf16, hidden, M, N, n, r, stream);
 }
 
 cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* dy,
                                  const float* hidden, const void* dx_base, void* dx, bool dx_bf16, void* da, void* db,
-                                 bool grad_bf16, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, void* ws,
-                                 cudaStream_t stream) {
+                                 bool grad_bf16, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, void* ws, int num_sms,
+                                 void* encode_tiled, cudaStream_t stream) {
   const BackwardPlan pl = plan_backward(M, K, N, r, n);
   uint8_t* base = static_cast<uint8_t*>(ws);
   float* part = reinterpret_cast<float*>(base + pl.part);
   __nv_bfloat16* ds = reinterpret_cast<__nv_bfloat16*>(base + pl.ds);
   __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(base + pl.s);
+  const bool by_chunks = wide(M, n);
   int splits = 1;
   cudaError_t e = cudaSuccess;
   if (dx != nullptr || da != nullptr) {
-    e = shrink<true>(dy, b, ids, part, M, N, n, r, &splits, stream);
+    e = by_chunks ? launch_lora_shrink_wide(dy, b, true, ids, scale, part, M, N, n, r, num_sms, encode_tiled, stream)
+                  : shrink(dy, b, true, ids, part, M, N, n, r, &splits, stream);
     if (e != cudaSuccess) return e;
   }
   if (dx != nullptr) {
-    e = expand<true>(part, splits, scale, a, ids, dx_base, dx, !dx_bf16, nullptr, M, K, n, r, stream);
+    e = by_chunks ? launch_lora_expand_wide(part, a, true, ids, dx_base, dx, !dx_bf16, M, K, n, r, num_sms, encode_tiled, stream)
+                  : expand(part, splits, scale, a, true, ids, dx_base, dx, !dx_bf16, nullptr, M, K, n, r, stream);
     if (e != cudaSuccess) return e;
   }
+  const float* part_scale = by_chunks ? nullptr : scale;
   if (da == nullptr && db == nullptr) return e;
   {
     const int64_t blocks = ceil_div(M * r, kThreads);
@@ -942,9 +1288,9 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
     __nv_bfloat16* ds_out = da != nullptr ? ds : nullptr;
     __nv_bfloat16* s_out = db != nullptr ? s : nullptr;
     const float* cpart = part;
-    e = grad_bf16 ? cudaLaunchKernelEx(&cfg, rfq_lora_split_kernel<2>, cpart, scale, ids, static_cast<int>(n), M, static_cast<int>(r),
+    e = grad_bf16 ? cudaLaunchKernelEx(&cfg, rfq_lora_split_kernel<2>, cpart, part_scale, ids, static_cast<int>(n), M, static_cast<int>(r),
                                        splits, ds_out, hidden, s_out)
-                  : cudaLaunchKernelEx(&cfg, rfq_lora_split_kernel<3>, cpart, scale, ids, static_cast<int>(n), M, static_cast<int>(r),
+                  : cudaLaunchKernelEx(&cfg, rfq_lora_split_kernel<3>, cpart, part_scale, ids, static_cast<int>(n), M, static_cast<int>(r),
                                        splits, ds_out, hidden, s_out);
     if (e != cudaSuccess) return e;
   }
@@ -965,7 +1311,12 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   o.n = static_cast<int>(n);
   o.r = static_cast<int>(r);
   o.range = pl.range;
-  const dim3 grid(static_cast<unsigned>(o.side[0].tiles + o.side[1].tiles), static_cast<unsigned>(pl.ranges));
+  // Few CTAs and several adapters (short batches): the adapters are shared out too.
+  const int64_t ctas = static_cast<int64_t>(o.side[0].tiles + o.side[1].tiles) * pl.ranges;
+  int64_t zs = 2 * kPlanSms / ctas;
+  if (zs > n) zs = n;
+  if (zs < 1) zs = 1;
+  const dim3 grid(static_cast<unsigned>(o.side[0].tiles + o.side[1].tiles), static_cast<unsigned>(pl.ranges), static_cast<unsigned>(zs));
   e = grad_bf16 ? outer_rank<2>(o, grid, stream) : outer_rank<3>(o, grid, stream);
   if (e != cudaSuccess) return e;
   ReduceParams q = {};

@@ -1,0 +1,790 @@
+// rfq_lora_wide.cu -- the adapters' two products over long batches, on tcgen05.
+//
+//   shrink   s[m] = scale_a P_a src[m]      rows x wide -> rank
+//   expand   out[m] = base[m] + Q_a s[m]    rank -> wide
+//
+// (rfq_lora.cu has the operator; P, Q = A, B going forward and B^T, A^T going back.)  Both are
+// bound by memory: 2 r flops for each element of src, or of base and out, with r <= 128.  What
+// the tensor cores buy here is instructions: with warp-level MMAs a [64 x 128] tile of expand
+// took 7400 warp instructions and ran at 0.7 TB/s; one thread's tcgen05.mma replaces the
+// fragment loads and MMAs of a whole tile, and the epilogue's thread owns a row.
+//
+// One CTA works on a chunk of 128 neighbouring rows.  A product is formed for all 128 rows once
+// for each adapter that the chunk holds, and each row keeps the result of its own: rows of an
+// MMA do not mix, so no row is gathered and nothing leaks between rows.  Chunks of one
+// adapter, the rule in prompts and training, cost one pass.  (Short batches, where rows
+// have adapters of their own, take the kernels of rfq_lora.cu.)
+//
+// shrink: the contraction is split over a cluster of up to 8 CTAs, whose partial sums are added
+// through distributed shared memory in the order of the ranks.  The accumulator takes 1024
+// elements of the contraction at a time (the tensor cores add by truncation) and the epilogue
+// adds those parts with rounding.
+// expand: base tiles come in by TMA, are added to in shared memory and leave from there by TMA.
+//
+// Roles: warp 0 TMA producer, warp 1 MMA issuer, the others epilogue.  Every wait on an mbarrier
+// is bounded (rfq_ptx.cuh); after one that ran out the epilogue runs through its loops without
+// waiting, so that no warp is left alone at a barrier.  No TMA multicast.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "rfq_internal.h"
+#include "rfq_ptx.cuh"
+#include "rfq_tmap.h"
+
+namespace rfq {
+
+__device__ unsigned int g_lora_error = 0;
+
+namespace {
+
+constexpr int kChunk = 128;
+constexpr uint32_t kBox = kChunk * 128;    // 128 rows of 128 bytes
+constexpr uint32_t kSmemLimit = 232448;
+constexpr int kMaxStages = 8;
+constexpr int kPartTiles = 16;             // k-tiles of 64 per accumulation
+
+// Shared-memory operand descriptors, 128-byte swizzle (K-major: 8-row groups 1024 bytes apart;
+// M/N-major: chunks of 64 elements `lead` bytes apart, 8 contraction rows 1024 bytes apart).
+__device__ __forceinline__ uint64_t k_major_desc(uint32_t addr) {
+  return ((addr >> 4) & 0x3FFFull) | (1ull << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t mn_major_desc(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3FFFull) | (static_cast<uint64_t>(lead >> 4) << 16) | ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16, bf16 operands, fp32 accumulator, M = 128.
+__device__ __forceinline__ uint32_t idesc(uint32_t n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(b_mn) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// The adapters of a chunk in the order of their first rows; a warp's lanes hold the 128 ids.
+struct Walk {
+  int id[4];
+  unsigned left;   // bit i: row lane + 32 i not yet taken
+  __device__ __forceinline__ void load(const int* ids, int64_t row0, int64_t M, int n) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = row0 + lane + 32 * i;
+      const int v = row < M ? ids[row] : -1;
+      id[i] = v >= 0 && v < n ? v : -1;
+    }
+    restart();
+  }
+  __device__ __forceinline__ void restart() {
+    left = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) left |= static_cast<unsigned>(id[i] >= 0) << i;
+  }
+  // The next adapter, or -1.  All lanes of the warp call it together.
+  __device__ __forceinline__ int next() {
+    int a = -1;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      const unsigned m = __ballot_sync(0xffffffffu, left >> i & 1u);
+      const int v = __shfl_sync(0xffffffffu, id[i], m ? __ffs(m) - 1 : 0);
+      if (m) a = v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (id[i] == a) left &= ~(1u << i);
+    return a;
+  }
+};
+
+struct Cursor {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == static_cast<uint32_t>(stages)) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// A producer thread's record of what it has asked for, to wait for at the end.
+struct Filled {
+  uint32_t mask = 0, last = 0;
+  __device__ __forceinline__ void add(const Cursor& c) {
+    mask |= 1u << c.stage;
+    last = (last & ~(1u << c.stage)) | (c.phase << c.stage);
+  }
+  __device__ __forceinline__ void drain(uint64_t* full, int stages) {
+    for (int s = 0; s < stages; ++s)
+      if (mask & (1u << s)) {
+        int never = 0;
+        mbar_wait(&full[s], (last >> s) & 1u, &never, &g_lora_error, kErrWaitDrain);
+      }
+  }
+};
+
+// ---------------------------------------------------------------- shrink
+struct ShrinkMaps {
+  CUtensorMap src, p;
+};
+struct ShrinkParams {
+  const int* ids;
+  const float* scale;
+  float* s;            // [M][r]
+  int64_t M;
+  int n, r, kt, kt_per_rank, cluster, stages;
+};
+
+constexpr int kShrinkThreads = 192;   // TMA, MMA, four epilogue warps
+
+__host__ __device__ constexpr uint32_t shrink_p_bytes(bool trans, int r) {
+  const uint32_t r16 = (r + 15) / 16 * 16;
+  return trans ? (r > 64 ? 2u : 1u) * 64u * 128u : r16 * 128u;
+}
+__host__ __device__ constexpr uint32_t shrink_sum_bytes(int r) { return kChunk * (r + 4) * 4; }
+
+template <bool kTrans>
+__global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(const __grid_constant__ ShrinkMaps maps,
+                                                                              const ShrinkParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t r16 = (p.r + 15) / 16 * 16;
+  const uint32_t stage_bytes = kBox + shrink_p_bytes(kTrans, p.r);
+  const uint32_t acc_cols = r16 <= 32 ? 32 : r16 <= 64 ? 64 : 128;
+  float* sums = reinterpret_cast<float*>(smem + p.stages * stage_bytes);   // [128][r + 4]
+  volatile int* abort_flag = &abort_word;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);
+    }
+    mbar_init(&drained, 1);
+    abort_word = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.src);
+    prefetch_tmap(&maps.p);
+  }
+  if (warp == 1) {
+    tmem_alloc_g<1>(&tmem_slot, 2 * acc_cols);
+    tmem_relinquish_g<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  const uint32_t rank = cluster_cta_rank();
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.cluster) * kChunk;
+  const int kt0 = static_cast<int>(rank) * p.kt_per_rank;
+  const int kt1 = min(p.kt, kt0 + p.kt_per_rank);
+  Walk walk;
+  walk.load(p.ids, row0, p.M, p.n);
+
+  if (warp == 0) {
+    Cursor c;
+    Filled filled;
+    bool ok = true;
+    for (int a = walk.next(); a >= 0 && ok; a = walk.next()) {
+      if (lane == 0) {
+        for (int kt = kt0; kt < kt1; ++kt) {
+          ok = mbar_wait(&empty[c.stage], c.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
+          if (!ok) break;
+          uint8_t* sx = smem + c.stage * stage_bytes;
+          mbar_arrive_expect_tx(&full[c.stage], stage_bytes);
+          tma_load_2d(sx, &maps.src, &full[c.stage], kt * 64, static_cast<int>(row0));
+          if constexpr (kTrans) {
+            tma_load_3d(sx + kBox, &maps.p, &full[c.stage], 0, kt * 64, a);
+            if (p.r > 64) tma_load_3d(sx + kBox + 64 * 128, &maps.p, &full[c.stage], 64, kt * 64, a);
+          } else {
+            tma_load_3d(sx + kBox, &maps.p, &full[c.stage], kt * 64, 0, a);
+          }
+          filled.add(c);
+          c.next(p.stages);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) filled.drain(full, p.stages);
+    __syncwarp();
+  } else if (warp == 1) {
+    Cursor c, acc;
+    bool ok = true;
+    const uint32_t id = idesc(r16, kTrans);
+    for (int a = walk.next(); a >= 0 && ok; a = walk.next()) {
+      if (lane == 0) {
+        for (int kp = kt0; kp < kt1 && ok; kp += kPartTiles) {
+          ok = mbar_wait(&acc_empty[acc.stage], acc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitAccEmpty);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + acc.stage * acc_cols;
+          for (int kt = kp; kt < min(kp + kPartTiles, kt1); ++kt) {
+            ok = mbar_wait(&full[c.stage], c.phase, abort_flag, &g_lora_error, kErrWaitFull);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sx = smem_addr(smem) + c.stage * stage_bytes, sp = sx + kBox;
+            const uint64_t da = k_major_desc(sx);
+            const uint64_t db = kTrans ? mn_major_desc(sp, 64 * 128) : k_major_desc(sp);
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q)
+              mma_bf16_g<1>(d, da + 2 * q, db + (kTrans ? 128 : 2) * q, id, (kt != kp || q != 0) ? 1u : 0u);
+            tc_commit(&empty[c.stage]);
+            c.next(p.stages);
+          }
+          if (!ok) break;
+          tc_commit(&acc_full[acc.stage]);
+          acc.next(2);
+        }
+        if (!ok) {   // teardown after an abort: wait for the MMAs already issued
+          tc_commit(&drained);
+          int never = 0;
+          mbar_wait(&drained, 0, &never, &g_lora_error, kErrWaitDrain);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    __syncwarp();
+  } else {
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const int mine = walk.id[0] * (quad == 0) + walk.id[1] * (quad == 1) + walk.id[2] * (quad == 2) + walk.id[3] * (quad == 3);
+    float* out = sums + row * (p.r + 4);
+    Cursor acc;
+    for (int a = walk.next(); a >= 0; a = walk.next()) {
+      for (int kp = kt0; kp < kt1; kp += kPartTiles) {
+        mbar_wait(&acc_full[acc.stage], acc.phase, abort_flag, &g_lora_error, kErrWaitAccFull, 2 * kWaitLimitNs);
+        tc_fence_after();
+        __syncwarp();
+        const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc.stage * acc_cols;
+        for (int j = 0; j < p.r; j += 8) {
+          uint32_t v[8];
+          tmem_load_32x32b_x8(at + j, v);
+          tmem_wait_ld();
+          if (mine == a) {
+            float4* o = reinterpret_cast<float4*>(out + j);
+            float4 x = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
+            float4 y = make_float4(__uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]), __uint_as_float(v[7]));
+            if (kp != kt0) {
+              const float4 u = o[0], w = o[1];
+              x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
+              y.x += w.x; y.y += w.y; y.z += w.z; y.w += w.w;
+            }
+            o[0] = x;
+            o[1] = y;
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[acc.stage]);
+        acc.next(2);
+      }
+    }
+  }
+
+  // Each rank adds the cluster's sums for its share of the rows, in the order of the ranks.
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_g<1>(tmem, 2 * acc_cols);
+  }
+  const int rows = kChunk / p.cluster, r4 = p.r / 4;
+  const uint32_t sums_addr = smem_addr(sums);
+  for (int i = threadIdx.x; i < rows * r4; i += kShrinkThreads) {
+    const int m = static_cast<int>(rank) * rows + i / r4, j = i % r4 * 4;
+    const int64_t row = row0 + m;
+    if (row >= p.M) continue;
+    const int a = p.ids[row];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a >= 0 && a < p.n) {
+      const uint32_t at = sums_addr + (m * (p.r + 4) + j) * 4;
+      for (int k = 0; k < p.cluster; ++k) {
+        const float4 u = ld_shared_cluster_f32x4(map_to_cta(at, k));
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+      }
+      const float w = p.scale[a];
+      v.x *= w; v.y *= w; v.z *= w; v.w *= w;
+    }
+    *reinterpret_cast<float4*>(p.s + row * p.r + j) = v;
+  }
+  cluster_sync();   // the others may still be reading this CTA's sums
+}
+
+// ---------------------------------------------------------------- expand
+struct ExpandMaps {
+  CUtensorMap q, base, out;
+};
+struct ExpandParams {
+  const int* ids;
+  const float* s;       // [M][r]
+  int64_t M;
+  int C;
+  int n, r;
+  int has_base, in_place;
+  int tiles, unit_tiles, col_units;   // column tiles in all, of one unit; units along the columns
+  int64_t units;
+  int base_stages, q_stages;
+};
+
+constexpr int kExpandThreads = 320;    // TMA, MMA, eight epilogue warps
+// Columns of a tile: 256 bytes of a row, two boxes of 128 bytes.
+template <bool kF32>
+constexpr int kCols = kF32 ? 64 : 128;
+// s enters the MMA as one bf16 term (2^-8 of the adapter's share, below the rounding of a bf16
+// output) or, for an fp32 output, as three (24 bits).
+template <bool kF32>
+constexpr int kTerms = kF32 ? 3 : 1;
+
+template <bool kTrans, bool kF32>
+__host__ __device__ constexpr uint32_t expand_q_bytes(int r) {
+  const uint32_t r16 = (r + 15) / 16 * 16;
+  return kTrans ? kCols<kF32> / 64 * r16 * 128u : (r > 64 ? 2u : 1u) * kCols<kF32> * 128u;
+}
+template <bool kF32>
+__host__ __device__ constexpr uint32_t expand_s_bytes(int r) {
+  return (r > 64 ? 2u : 1u) * kTerms<kF32> * kBox;
+}
+
+template <bool kTrans, bool kF32>
+__global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel(const __grid_constant__ ExpandMaps maps,
+                                                                                 const ExpandParams p) {
+  constexpr int kT = kTerms<kF32>;
+  constexpr int kN = kCols<kF32>;
+  constexpr int kBoxCols = kN / 2;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t b_full[kMaxStages], b_empty[kMaxStages], q_full[kMaxStages], q_empty[kMaxStages], acc_full[2], acc_empty[2],
+      s_full, drained;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t r16 = (p.r + 15) / 16 * 16;
+  const uint32_t q_bytes = expand_q_bytes<kTrans, kF32>(p.r);
+  uint8_t* s_mem = smem;                                           // [r / 64][term][128 rows x 128 bytes]
+  uint8_t* b_mem = s_mem + expand_s_bytes<kF32>(p.r);              // base tiles: two boxes each
+  uint8_t* q_mem = b_mem + p.base_stages * 2 * kBox;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&b_full[s], 1);
+      mbar_init(&b_empty[s], 1);
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);
+    }
+    mbar_init(&s_full, 8);
+    mbar_init(&drained, 1);
+    abort_word = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.base);
+    prefetch_tmap(&maps.out);
+  }
+  if (warp == 1) {
+    tmem_alloc_g<1>(&tmem_slot, 256);
+    tmem_relinquish_g<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // A unit is a chunk of rows and a run of column tiles.  Where a chunk has no adapter and the
+  // base is the output, there is nothing to do; every role finds that out for itself.
+  Walk walk;
+  if (warp == 0) {
+    Cursor bc, qc;
+    Filled b_filled, q_filled;
+    bool ok = true;
+    for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
+      const int64_t row0 = unit / p.col_units * kChunk;
+      const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
+      walk.load(p.ids, row0, p.M, p.n);
+      if (p.in_place && !__any_sync(0xffffffffu, walk.left != 0)) continue;
+      for (int t = t0; t < t1 && ok; ++t) {
+        const int col = t * kN;
+        if (p.has_base && lane == 0) {
+          ok = mbar_wait(&b_empty[bc.stage], bc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
+          if (ok) {
+            uint8_t* sb = b_mem + bc.stage * 2 * kBox;
+            mbar_arrive_expect_tx(&b_full[bc.stage], 2 * kBox);
+            tma_load_2d(sb, &maps.base, &b_full[bc.stage], col, static_cast<int>(row0));
+            tma_load_2d(sb + kBox, &maps.base, &b_full[bc.stage], col + kBoxCols, static_cast<int>(row0));
+            b_filled.add(bc);
+            bc.next(p.base_stages);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        walk.restart();
+        for (int a = walk.next(); a >= 0 && ok; a = walk.next()) {
+          if (lane == 0) {
+            ok = mbar_wait(&q_empty[qc.stage], qc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
+            if (ok) {
+              uint8_t* sq = q_mem + qc.stage * q_bytes;
+              mbar_arrive_expect_tx(&q_full[qc.stage], q_bytes);
+              if constexpr (kTrans) {
+#pragma unroll
+                for (int c = 0; c < kN / 64; ++c) tma_load_3d(sq + c * r16 * 128, &maps.q, &q_full[qc.stage], col + 64 * c, 0, a);
+              } else {
+                tma_load_3d(sq, &maps.q, &q_full[qc.stage], 0, col, a);
+                if (p.r > 64) tma_load_3d(sq + kN * 128, &maps.q, &q_full[qc.stage], 64, col, a);
+              }
+              q_filled.add(qc);
+              qc.next(p.q_stages);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+      }
+    }
+    if (lane == 0) {
+      b_filled.drain(b_full, p.base_stages);
+      q_filled.drain(q_full, p.q_stages);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    Cursor qc, acc;
+    uint32_t s_phase = 0;
+    bool ok = true;
+    const uint32_t id = idesc(kN, kTrans);
+    for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
+      const int64_t row0 = unit / p.col_units * kChunk;
+      const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
+      walk.load(p.ids, row0, p.M, p.n);
+      if (!__any_sync(0xffffffffu, walk.left != 0)) continue;
+      if (lane == 0) {
+        ok = mbar_wait(&s_full, s_phase, abort_flag, &g_lora_error, kErrWaitFull);
+        tc_fence_after();
+      }
+      s_phase ^= 1u;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      for (int t = t0; t < t1 && ok; ++t) {
+        walk.restart();
+        for (int a = walk.next(); a >= 0 && ok; a = walk.next()) {
+          if (lane == 0) {
+            ok = mbar_wait(&acc_empty[acc.stage], acc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitAccEmpty) &&
+                 mbar_wait(&q_full[qc.stage], qc.phase, abort_flag, &g_lora_error, kErrWaitFull);
+            if (ok) {
+              tc_fence_after();
+              const uint32_t d = tmem + acc.stage * 128;
+              const uint32_t sq = smem_addr(q_mem) + qc.stage * q_bytes, sa = smem_addr(s_mem);
+              uint32_t more = 0;
+              for (uint32_t k = 0; k < r16 / 16; ++k) {
+                const uint64_t db = kTrans ? mn_major_desc(sq, r16 * 128) + 128 * k : k_major_desc(sq + (k >> 2) * kN * 128) + 2 * (k & 3);
+#pragma unroll
+                for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
+                  mma_bf16_g<1>(d, k_major_desc(sa + ((k >> 2) * kT + e) * kBox) + 2 * (k & 3), db, id, more);
+                  more = 1;
+                }
+              }
+              tc_commit(&q_empty[qc.stage]);
+              tc_commit(&acc_full[acc.stage]);
+            }
+            qc.next(p.q_stages);
+            acc.next(2);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+      }
+      if (!ok && lane == 0) {   // teardown after an abort: wait for the MMAs already issued
+        tc_commit(&drained);
+        int never = 0;
+        mbar_wait(&drained, 0, &never, &g_lora_error, kErrWaitDrain);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int row = quad * 32 + lane;
+    Cursor bc, acc;
+    int release = -1;   // the stage whose tile may still be on its way out
+    for (int64_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
+      const int64_t row0 = unit / p.col_units * kChunk;
+      const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
+      walk.load(p.ids, row0, p.M, p.n);
+      const bool any = __any_sync(0xffffffffu, walk.left != 0);
+      if (!any && p.in_place) continue;
+      const int mine = quad == 0 ? walk.id[0] : quad == 1 ? walk.id[1] : quad == 2 ? walk.id[2] : walk.id[3];
+      if (any) {
+        // s of this chunk in the operand's layout.  The MMAs that read the one before have ended:
+        // their accumulators have been taken.
+        const float* src = p.s + (row0 + row) * p.r;
+        for (int c = half; c < static_cast<int>(r16 / 8); c += 2) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = 0.f;
+          if (mine >= 0 && 8 * c < p.r) {
+            const float4 x = *reinterpret_cast<const float4*>(src + 8 * c), y = *reinterpret_cast<const float4*>(src + 8 * c + 4);
+            f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+            f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+          }
+          uint8_t* to = s_mem + (c >> 3) * kT * kBox + row * 128 + ((c & 7) ^ (row & 7)) * 16;
+#pragma unroll
+          for (int e = 0; e < kT; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * h], f[2 * h + 1]);
+              w[h] = *reinterpret_cast<const uint32_t*>(&b);
+              f[2 * h] -= __uint_as_float(w[h] << 16);
+              f[2 * h + 1] -= __uint_as_float(w[h] & 0xffff0000u);
+            }
+            *reinterpret_cast<uint4*>(to + e * kBox) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_full);
+      }
+      for (int t = t0; t < t1; ++t) {
+        if (p.has_base) mbar_wait(&b_full[bc.stage], bc.phase, abort_flag, &g_lora_error, kErrWaitFull, 2 * kWaitLimitNs);
+        uint8_t* sb = b_mem + bc.stage * 2 * kBox;
+        uint8_t* line = sb + half * kBox + row * 128;
+        if (!p.has_base) {
+          // The stage is free once its last tile has left (one thread waits, all learn of it at the barrier).
+          if (threadIdx.x == 64 && release >= 0) bulk_wait_read_all();
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          if (mine < 0)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        walk.restart();
+        for (int a = walk.next(); a >= 0; a = walk.next()) {
+          mbar_wait(&acc_full[acc.stage], acc.phase, abort_flag, &g_lora_error, kErrWaitAccFull, 2 * kWaitLimitNs);
+          tc_fence_after();
+          __syncwarp();
+          const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc.stage * 128 + half * kBoxCols;
+#pragma unroll
+          for (int g = 0; g < kBoxCols / 32; ++g) {
+            uint32_t v[32];
+            tmem_load_32x32b_x32(at + 32 * g, v);
+            tmem_wait_ld();
+            if (mine == a) {
+              if constexpr (kF32) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  float4* o = reinterpret_cast<float4*>(line + (c ^ (row & 7)) * 16);
+                  float4 f = make_float4(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]), __uint_as_float(v[4 * c + 2]),
+                                         __uint_as_float(v[4 * c + 3]));
+                  if (p.has_base) {
+                    const float4 b = *o;
+                    f.x += b.x; f.y += b.y; f.z += b.z; f.w += b.w;
+                  }
+                  *o = f;
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  uint4* o = reinterpret_cast<uint4*>(line + ((4 * g + c) ^ (row & 7)) * 16);
+                  uint32_t w[4] = {0u, 0u, 0u, 0u};
+                  if (p.has_base) {
+                    const uint4 b = *o;
+                    w[0] = b.x; w[1] = b.y; w[2] = b.z; w[3] = b.w;
+                  }
+#pragma unroll
+                  for (int h = 0; h < 4; ++h) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(w[h] << 16) + __uint_as_float(v[8 * c + 2 * h]),
+                                                                   __uint_as_float(w[h] & 0xffff0000u) + __uint_as_float(v[8 * c + 2 * h + 1]));
+                    w[h] = *reinterpret_cast<const uint32_t*>(&b);
+                  }
+                  *o = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+            }
+            __syncwarp();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[acc.stage]);
+          acc.next(2);
+        }
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x == 64) {
+          if (*abort_flag == 0) {
+            const int col = t * kN;
+            tma_store_2d(&maps.out, sb, col, static_cast<int>(row0));
+            if (col + kBoxCols < p.C) tma_store_2d(&maps.out, sb + kBox, col + kBoxCols, static_cast<int>(row0));
+          }
+          bulk_commit_group();
+          if (p.has_base) {
+            bulk_wait_read_but_one();
+            if (release >= 0) mbar_arrive(&b_empty[release]);
+          }
+        }
+        release = static_cast<int>(bc.stage);
+        bc.next(p.base_stages);
+      }
+    }
+    if (threadIdx.x == 64) bulk_wait_all();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_g<1>(tmem, 256);
+  }
+}
+
+// ---------------------------------------------------------------- host
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// [n][rows][cols] bf16, box 64 columns x box_rows rows of one matrix.
+bool encode_pool_map(EncodeTiledFn encode, CUtensorMap* map, const void* base, int64_t n, int64_t rows, int64_t cols, uint32_t box_rows) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * static_cast<cuuint64_t>(rows) * 2};
+  cuuint32_t box[3] = {64u, box_rows, 1u};
+  cuuint32_t one[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_f32_map(EncodeTiledFn encode, CUtensorMap* map, const void* base, int64_t rows, int64_t cols) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 4};
+  cuuint32_t box[2] = {32u, kChunk};
+  cuuint32_t one[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class Kernel, class Maps, class Params>
+cudaError_t launch(Kernel kernel, const Maps& maps, const Params& p, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see griddep_wait()
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kernel, maps, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool kTrans, bool kF32>
+cudaError_t expand_typed(const ExpandMaps& maps, ExpandParams p, int num_sms, cudaStream_t stream) {
+  const uint32_t q = expand_q_bytes<kTrans, kF32>(p.r), s = expand_s_bytes<kF32>(p.r);
+  const uint32_t room = kSmemLimit - 4096 - s;   // 4 KiB: alignment and the static part
+  p.q_stages = 2;
+  p.base_stages = 2;
+  while (p.base_stages < 4 && (p.base_stages + 1) * 2 * kBox + p.q_stages * q <= room) ++p.base_stages;
+  while (p.q_stages < 4 && p.base_stages * 2 * kBox + (p.q_stages + 1) * q <= room) ++p.q_stages;
+  const size_t smem = 1024 + s + p.base_stages * 2 * kBox + p.q_stages * q;
+  const int64_t grid = p.units < num_sms ? p.units : num_sms;
+  return launch(rfq_lora_expand_wide_kernel<kTrans, kF32>, maps, p, grid, kExpandThreads, smem, 1, stream);
+}
+
+}  // namespace
+
+// s [M][r] = scale (P src), P the pool [n][r][C] or (trans) [n][C][r].
+cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool trans, const int* ids, const float* scale, float* s,
+                                    int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream) {
+  EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
+  ShrinkMaps maps;
+  const uint32_t r16 = static_cast<uint32_t>((r + 15) / 16 * 16);
+  if (!encode_bf16_map(encode, &maps.src, src, M, C, C, kChunk) ||
+      !(trans ? encode_pool_map(encode, &maps.p, pool, n, C, r, 64) : encode_pool_map(encode, &maps.p, pool, n, r, C, r16)))
+    return cudaErrorInvalidValue;
+  ShrinkParams p = {};
+  p.ids = ids;
+  p.scale = scale;
+  p.s = s;
+  p.M = M;
+  p.n = static_cast<int>(n);
+  p.r = static_cast<int>(r);
+  p.kt = static_cast<int>(ceil_div(C, 64));
+  // A cluster of up to 8 along the contraction while two CTAs per SM are not reached, no rank empty.
+  const int64_t chunks = ceil_div(M, kChunk);
+  p.cluster = 1;
+  while (p.cluster < 8 && chunks * p.cluster * 2 <= 2 * num_sms) {
+    const int next = p.cluster * 2, per = static_cast<int>(ceil_div(p.kt, next));
+    if (per < 2 || (next - 1) * per >= p.kt) break;
+    p.cluster = next;
+  }
+  p.kt_per_rank = static_cast<int>(ceil_div(p.kt, p.cluster));
+  const uint32_t stage = kBox + shrink_p_bytes(trans, p.r), sums = shrink_sum_bytes(p.r);
+  // As many stages as leave room for two CTAs per SM, at least three.
+  p.stages = static_cast<int>((kSmemLimit / 2 - 2048 - sums) / stage);
+  if (sums + 2048 > kSmemLimit / 2 || p.stages < 3) p.stages = 3;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * stage + sums;
+  return trans ? launch(rfq_lora_shrink_wide_kernel<true>, maps, p, chunks * p.cluster, kShrinkThreads, smem, p.cluster, stream)
+               : launch(rfq_lora_shrink_wide_kernel<false>, maps, p, chunks * p.cluster, kShrinkThreads, smem, p.cluster, stream);
+}
+
+// out [M][C] = base + Q s, Q the pool [n][C][r] or (trans) [n][r][C].
+cudaError_t launch_lora_expand_wide(const float* s, const void* pool, bool trans, const int* ids, const void* base, void* out, bool f32,
+                                    int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream) {
+  EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
+  ExpandMaps maps;
+  const uint32_t r16 = static_cast<uint32_t>((r + 15) / 16 * 16);
+  const int cols = f32 ? kCols<true> : kCols<false>;
+  auto wide_map = [&](CUtensorMap* map, const void* at) {
+    return f32 ? encode_f32_map(encode, map, at, M, C) : encode_bf16_map(encode, map, at, M, C, C, kChunk);
+  };
+  if (!wide_map(&maps.out, out) || !wide_map(&maps.base, base != nullptr ? base : out) ||
+      !(trans ? encode_pool_map(encode, &maps.q, pool, n, r, C, r16) : encode_pool_map(encode, &maps.q, pool, n, C, r, cols)))
+    return cudaErrorInvalidValue;
+  ExpandParams p = {};
+  p.ids = ids;
+  p.s = s;
+  p.M = M;
+  p.C = static_cast<int>(C);
+  p.n = static_cast<int>(n);
+  p.r = static_cast<int>(r);
+  p.has_base = base != nullptr;
+  p.in_place = base == out;
+  p.tiles = static_cast<int>(ceil_div(C, cols));
+  // Column tiles of one unit: the length (4 to 16 tiles) that leaves the fewest tiles to the CTA
+  // with the most, each unit charged one more for the change of rows.
+  const int64_t chunks = ceil_div(M, kChunk);
+  int64_t best = INT64_MAX;
+  p.unit_tiles = p.tiles;
+  for (int len = 4; len <= 16; ++len) {
+    const int64_t units = chunks * ceil_div(p.tiles, len), cost = ceil_div(units, num_sms) * (len + 1);
+    if (cost < best) {
+      best = cost;
+      p.unit_tiles = len;
+    }
+  }
+  p.col_units = static_cast<int>(ceil_div(p.tiles, p.unit_tiles));
+  p.units = chunks * p.col_units;
+  if (trans) return f32 ? expand_typed<true, true>(maps, p, num_sms, stream) : expand_typed<true, false>(maps, p, num_sms, stream);
+  return f32 ? expand_typed<false, true>(maps, p, num_sms, stream) : expand_typed<false, false>(maps, p, num_sms, stream);
+}
+
+cudaError_t read_and_clear_lora_error(unsigned int* value) {
+  unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_lora_error, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_lora_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace rfq

@@ -483,8 +483,8 @@ rfq_status_t rfq_mma_rate_probe(int variant, int64_t iterations, unsigned long l
  * load, 2 free stage, 3 accumulator ready, 4 accumulator free, 5 teardown;
  * 6 a wait of the quantizer for its TMA load; the same codes 1, 2, 3, 5 for
  * the corresponding waits of rfq_linear_fused, and 7 its quantizer warps
- * waiting for a staged tile of X; 1..5 also for those waits of rfq_linear_ce and its
- * backward).
+ * waiting for a staged tile of X; 1..5 also for those waits of rfq_linear_ce, of
+ * rfq_lora and of their backward passes).
  */
 rfq_status_t rfq_check_device_error(cudaStream_t stream, int* detail);
 
