@@ -80,12 +80,15 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
                                  const float* hidden, const void* dx_base, void* dx, bool dx_bf16, void* da, void* db,
                                  bool grad_bf16, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, void* ws, int num_sms,
                                  void* encode_tiled, cudaStream_t stream);
-// Their two products over long batches (rfq_lora_wide.cu): s [M][r] = scale (P src), out = base + Q s,
-// the pool [n][r][C], transposed [n][C][r] (shrink) and the other way round (expand).
+// Their two products over long batches (rfq_lora_wide.cu).  shrink: s [M][r] fp32 (or nullptr) = scale
+// (P src) and s as bf16 terms [M][num_terms][r], the pool [n][r][C] or, transposed, [n][C][r].  expand:
+// out = base + Q s from the terms, the pool [n][C][r] or, transposed, [n][r][C].
 cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool trans, const int* ids, const float* scale, float* s,
-                                    int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream);
-cudaError_t launch_lora_expand_wide(const float* s, const void* pool, bool trans, const int* ids, const void* base, void* out, bool f32,
-                                    int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream);
+                                    void* terms, int num_terms, int64_t M, int64_t C, int64_t n, int64_t r, int num_sms,
+                                    void* encode_tiled, cudaStream_t stream);
+cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const void* pool, bool trans, const int* ids,
+                                    const void* base, void* out, bool f32, int64_t M, int64_t C, int64_t n, int64_t r,
+                                    int num_sms, void* encode_tiled, cudaStream_t stream);
 
 // Global norm of a list of tensors (host arrays) and, where `scale`, the list scaled to it (rfq_clip.cu).
 // out == nullptr scales in place.

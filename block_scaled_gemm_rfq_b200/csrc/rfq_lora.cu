@@ -51,7 +51,7 @@ namespace rfq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 128;                // rows grouped by one CTA
+constexpr int kChunk = 256;                // rows grouped by one CTA
 constexpr int kRows = 16;                  // rows of one group
 constexpr int kMaxStages = 6;
 constexpr int kSmemLimit = 227 * 1024;
@@ -115,39 +115,36 @@ __device__ __forceinline__ void cp_wait_stage(int stages) {
 struct Groups {
   int ids[kChunk];
   int order[kChunk];
-  int flag[kChunk];
   int start[kChunk + 1];
   int items;
+  int flag[kChunk];            // of the grouping alone
 };
+constexpr int kTable = 3 * kChunk + 2;   // words of a Groups that the next kernel reads back
 
-template <int kRows>
 __device__ void group_rows(Groups& g, const int* ids, int64_t row0, int64_t M, int n) {
+  static_assert(kThreads == kChunk, "a thread for each row");
   const int t = threadIdx.x;
   const int count = static_cast<int>(M - row0 < kChunk ? M - row0 : kChunk);
   int id = INT_MAX;
-  if (t < kChunk) {
-    if (t < count) {
-      const int v = ids[row0 + t];
-      if (v >= 0 && v < n) id = v;
-    }
-    g.ids[t] = id;
+  if (t < count) {
+    const int v = ids[row0 + t];
+    if (v >= 0 && v < n) id = v;
   }
+  g.ids[t] = id;
   // Rows already in order (neighbours of one request, one adapter for all): nothing to sort, and
   // a run's first row is the last one before t that differs from its predecessor.
   __syncthreads();
   const bool sorted = __syncthreads_and(t == 0 || t >= count || g.ids[t - 1] <= id);
   if (sorted) {
-    if (t < kChunk) {
-      const unsigned bits = __ballot_sync(0xffffffffu, t < count && (t == 0 || g.ids[t - 1] != id));
-      if ((t & 31) == 0) g.start[t >> 5] = static_cast<int>(bits);
-    }
+    const unsigned bits = __ballot_sync(0xffffffffu, t < count && (t == 0 || g.ids[t - 1] != id));
+    if ((t & 31) == 0) g.start[t >> 5] = static_cast<int>(bits);
     __syncthreads();
     if (t < count) {
       int w = t >> 5;
-      unsigned bits = static_cast<unsigned>(g.start[w]) & (0xffffffffu >> (31 - (t & 31)));
-      while (bits == 0) bits = static_cast<unsigned>(g.start[--w]);   // row 0 begins a run
+      unsigned run = static_cast<unsigned>(g.start[w]) & (0xffffffffu >> (31 - (t & 31)));
+      while (run == 0) run = static_cast<unsigned>(g.start[--w]);   // row 0 begins a run
       g.order[t] = t;
-      g.flag[t] = (t - (w * 32 + 31 - __clz(bits))) % kRows == 0;
+      g.flag[t] = (t - (w * 32 + 31 - __clz(run))) % kRows == 0;
     }
   } else if (t < count) {
     int less = 0, before = 0;
@@ -177,6 +174,15 @@ __device__ void group_rows(Groups& g, const int* ids, int64_t row0, int64_t M, i
   __syncthreads();
 }
 
+// The grouping is done by shrink; the first CTA of each chunk leaves it for expand.
+__device__ __forceinline__ void leave_groups(const Groups& g, int* table) {
+  for (int i = threadIdx.x; i < kTable; i += kThreads) table[i] = reinterpret_cast<const int*>(&g)[i];
+}
+__device__ __forceinline__ void take_groups(Groups& g, const int* table) {
+  for (int i = threadIdx.x; i < kTable; i += kThreads) reinterpret_cast<int*>(&g)[i] = table[i];
+  __syncthreads();
+}
+
 // ---------------------------------------------------------------- shrink
 // part[split][m][j] = sum over the split's k of src[m][k] P_a[j][k], P = A (rows j, k along the
 // row; the direct kernel) or B^T (rows k, j along the row).
@@ -186,6 +192,7 @@ struct ShrinkParams {
   const int* ids;
   float* part;                // [splits][M][r]
   int64_t M, C, c_split;      // c_split: contraction elements of one split (a multiple of kBK)
+  int* table;                 // [chunks][kTable]
   int n, r, zs;               // zs: CTAs that share the items of one chunk
   int stages;
 };
@@ -210,7 +217,8 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
   const int z = static_cast<int>(blockIdx.x % p.zs);
-  group_rows<kRows>(g, p.ids, row0, p.M, p.n);
+  group_rows(g, p.ids, row0, p.M, p.n);
+  if (z == 0 && blockIdx.y == 0) leave_groups(g, p.table + (blockIdx.x / p.zs) * kTable);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wm = warp % kWm, wk = warp / kWm;
@@ -356,7 +364,8 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_direct_kernel(const 
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
   const int z = static_cast<int>(blockIdx.x % p.zs);
-  group_rows<kRows>(g, p.ids, row0, p.M, p.n);
+  group_rows(g, p.ids, row0, p.M, p.n);
+  if (z == 0 && blockIdx.y == 0) leave_groups(g, p.table + (blockIdx.x / p.zs) * kTable);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int jt = p.r / 8, quad = lane & 3, line = lane >> 2;
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * p.c_split;
@@ -459,7 +468,7 @@ struct ExpandParams {
   const float* part;          // [splits][M][r]
   const float* scale;         // [n]
   const __nv_bfloat16* q;     // [n][C][r] (direct) or [n][r][C]
-  const int* ids;
+  const int* table;           // [chunks][kTable], from shrink
   const void* base;           // [M][C] or nullptr
   void* out;                  // [M][C]
   float* hidden;              // [M][r] or nullptr
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
   const int z = static_cast<int>(blockIdx.x % p.zs);
-  group_rows<kRows>(g, p.ids, row0, p.M, p.n);
+  take_groups(g, p.table + (blockIdx.x / p.zs) * kTable);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wm = warp % kWm, wn = warp / kWm;
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_direct_kernel(const 
   griddep_wait();
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
   const int z = static_cast<int>(blockIdx.x % p.zs);
-  group_rows<kRows>(g, p.ids, row0, p.M, p.n);
+  take_groups(g, p.table + (blockIdx.x / p.zs) * kTable);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3, line = lane >> 2;
   const int64_t begin = static_cast<int64_t>(blockIdx.y) * p.tiles * 32;
   const int64_t end = min(p.C, begin + static_cast<int64_t>(p.tiles) * 32);
@@ -796,31 +805,39 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_direct_kernel(const 
 }
 
 // ---------------------------------------------------------------- split
-// The rank-r vectors as bf16 terms [M][term][r]: ds' from its partial sums (scale nullptr: they are
-// scaled already), s' as saved by the forward pass.  Rows without an adapter are never read by what follows.
+// The rank-r vectors as bf16 terms [M][term][r]: ds' from its partial sums (after the shrink of short
+// batches; that of long ones leaves terms), s' as saved by the forward pass.  Rows without an adapter are never read by what follows.
+struct SplitParams {
+  const float* part;          // [splits][M][r]
+  const float* scale;
+  const int* ids;
+  const float* hidden;        // [M][r]
+  __nv_bfloat16* ds;          // [M][term][r] or nullptr
+  __nv_bfloat16* s;           // [M][term][r] or nullptr
+  int64_t M;
+  int n, r, splits;
+};
+
 template <int kT>
-__global__ void __launch_bounds__(kThreads) rfq_lora_split_kernel(const float* part, const float* scale, const int* ids, int n,
-                                                                       int64_t M, int r, int splits, __nv_bfloat16* ds,
-                                                                       const float* hidden, __nv_bfloat16* s) {
+__global__ void __launch_bounds__(kThreads) rfq_lora_split_kernel(const SplitParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t total = M * r;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t m = i / r;
-    const int a = ids[m];
-    if (a < 0 || a >= n) continue;
-    const int64_t at = m * kT * r + (i - m * r);
+  const int64_t total = p.M * p.r;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t m = i / p.r;
+    const int a = p.ids[m];
+    if (a < 0 || a >= p.n) continue;
+    const int64_t at = m * kT * p.r + (i - m * p.r);
     __nv_bfloat16 t[kT];
-    if (ds != nullptr) {
-      split_terms<kT>(join_parts(part, splits, total, i, scale != nullptr ? scale[a] : 1.f), t);
+    if (p.ds != nullptr) {
+      split_terms<kT>(join_parts(p.part, p.splits, total, i, p.scale[a]), t);
 #pragma unroll
-      for (int e = 0; e < kT; ++e) ds[at + e * r] = t[e];
+      for (int e = 0; e < kT; ++e) p.ds[at + e * p.r] = t[e];
     }
-    if (s != nullptr) {
-      split_terms<kT>(hidden[i], t);
+    if (p.s != nullptr) {
+      split_terms<kT>(p.hidden[i], t);
 #pragma unroll
-      for (int e = 0; e < kT; ++e) s[at + e * r] = t[e];
+      for (int e = 0; e < kT; ++e) p.s[at + e * p.r] = t[e];
     }
   }
 }
@@ -834,7 +851,8 @@ constexpr int kMaxRange = 4096;       // rows of one range
 constexpr int kMaxAdapters = 4096;
 
 struct OuterSide {
-  const __nv_bfloat16* v;     // [M][term][r]
+  const __nv_bfloat16* v;     // [M][ld]: terms of r each, kT or more
+  int ld;
   const __nv_bfloat16* w;     // [M][C]
   float* part;                // [ranges][n][r][C]
   int64_t C;
@@ -884,6 +902,17 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
   const int j16 = (p.r + 15) / 16;
   const int qx = tid & 15;
   const bool qx_ok = c0 + 8 * qx < s.C;
+  // This thread's 16-byte pieces of a stage's v: row, element in v, place in the stage.
+  constexpr int kVCopies = (kOuterRows * kT * kJ16 * 2 + kThreads - 1) / kThreads;
+  int v_m[kVCopies], v_from[kVCopies];
+  uint32_t v_to[kVCopies];
+#pragma unroll
+  for (int u = 0; u < kVCopies; ++u) {
+    const int i = tid + kThreads * u, m = i / v_pieces, q = i - m * v_pieces;
+    v_m[u] = m < kOuterRows ? m : kOuterRows;
+    v_from[u] = m * s.ld + 8 * q;
+    v_to[u] = m * v_stride + 16 * q;
+  }
 
   for (int i = tid; i < p.n; i += kThreads) here[i] = 0;
   __syncthreads();
@@ -922,6 +951,11 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
     __syncthreads();
 
     const int iters = (total + kOuterRows - 1) / kOuterRows;
+    // Rows that are neighbours (one request, one adapter for all) are stepped through; others are looked
+    // up in the list for each copy.
+    const bool run = list[total - 1] - list[0] == total - 1;
+    const __nv_bfloat16* w_at = s.w + (row0 + list[0] + (tid >> 4)) * s.C + c0 + 8 * qx;
+    const __nv_bfloat16* v_at = s.v + (row0 + list[0]) * s.ld;
     int load_stage = 0, load_at = 0;
     auto load = [&]() {
       if (load_at < total) {
@@ -930,25 +964,38 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
         for (int u = 0; u < kOuterRows / 16; ++u) {   // rows past the last: zeros
           const int m = (tid >> 4) + 16 * u;
           const bool ok = load_at + m < total && qx_ok;
-          cp_async16(sw + m * kWStride + 16 * qx, ok ? s.w + (row0 + list[load_at + m]) * s.C + c0 + 8 * qx : s.w, ok);
+          const __nv_bfloat16* from = w_at + 16 * u * s.C;
+          if (!run && ok) from = s.w + (row0 + list[load_at + m]) * s.C + c0 + 8 * qx;
+          cp_async16(sw + m * kWStride + 16 * qx, ok ? from : s.w, ok);
         }
-        for (int i = tid; i < kOuterRows * v_pieces; i += kThreads) {
-          const int m = i / v_pieces, q = i - m * v_pieces;
-          const bool ok = load_at + m < total;
-          cp_async16(sv + m * v_stride + 16 * q, ok ? s.v + (row0 + list[load_at + m]) * kT * p.r + 8 * q : s.v, ok);
-        }
+        w_at += kOuterRows * s.C;
+#pragma unroll
+        for (int u = 0; u < kVCopies; ++u)
+          if (v_m[u] < kOuterRows) {
+            const bool ok = load_at + v_m[u] < total;
+            const __nv_bfloat16* from = v_at + v_from[u];
+            if (!run && ok) from = s.v + (row0 + list[load_at + v_m[u]]) * s.ld + v_from[u] - v_m[u] * s.ld;
+            cp_async16(sv + v_to[u], ok ? from : s.v, ok);
+          }
+        v_at += kOuterRows * s.ld;
       }
       cp_commit();
       load_at += kOuterRows;
       if (++load_stage == p.stages) load_stage = 0;
     };
-    float acc[kJ16][2][4];
+    // fp32 results: the MMAs add by truncation, so each stage's 64 rows are summed on their own and
+    // added to the rest with rounding.
+    constexpr bool kFlush = kT == 3;
+    float acc[kJ16][2][4], sum[kFlush ? kJ16 : 1][2][4];
 #pragma unroll
     for (int j = 0; j < kJ16; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][h][e] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+          acc[j][h][e] = 0.f;
+          if constexpr (kFlush) sum[j][h][e] = 0.f;
+        }
     for (int it = 0; it < p.stages - 1; ++it) load();
     int stage = 0;
     for (int it = 0; it < iters; ++it) {
@@ -974,7 +1021,26 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
             }
           }
       }
+      if constexpr (kFlush) {
+#pragma unroll
+        for (int j = 0; j < kJ16; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sum[j][h][e] += acc[j][h][e];
+              acc[j][h][e] = 0.f;
+            }
+      }
       if (++stage == p.stages) stage = 0;
+    }
+    if constexpr (kFlush) {
+#pragma unroll
+      for (int j = 0; j < kJ16; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][h][e] = sum[j][h][e];
     }
     float* out = s.part + (static_cast<int64_t>(range) * p.n + a) * p.r * s.C;
 #pragma unroll
@@ -1085,17 +1151,18 @@ int ring_stages(int stage_bytes, int other_bytes) {
 // average, since a chunk is passed over once for each adapter in it.
 bool wide(int64_t M, int64_t n) { return M > 64 && M > 32 * n; }
 
-// CTAs that share the groups of one chunk.
-int64_t chunk_ctas(int64_t M, int64_t most) {
-  const int64_t chunks = ceil_div(M, kChunk);
-  int64_t z = M <= 32 ? M : ceil_div(M < kChunk ? M : kChunk, 2);
+// CTAs that share the groups of one chunk: one for each there can be, up to `most` over all chunks.
+int64_t chunk_ctas(int64_t M, int64_t n, int64_t most) {
+  const int64_t chunks = ceil_div(M, kChunk), rows = M < kChunk ? M : kChunk;
+  int64_t z = n + 1 + rows / kRows;   // every adapter, the rows without one, and groups that are full
+  if (z > rows) z = rows;
   while (z > 1 && chunks * z > most) z = (z + 1) / 2;
   return z;
 }
 
 // Splits of the shrink product's contraction: four CTAs per SM over all, 256 elements each at least.
-int shrink_splits(int64_t M, int64_t C, int64_t* c_split, int* zs) {
-  const int64_t chunks = ceil_div(M, kChunk), z = chunk_ctas(M, 2 * kPlanSms);
+int shrink_splits(int64_t M, int64_t C, int64_t n, int64_t* c_split, int* zs) {
+  const int64_t chunks = ceil_div(M, kChunk), z = chunk_ctas(M, n, 2 * kPlanSms);
   const int64_t most = ceil_div(C, 256);
   int64_t s = 4 * kPlanSms / (chunks * z);
   if (s > most) s = most;
@@ -1106,18 +1173,19 @@ int shrink_splits(int64_t M, int64_t C, int64_t* c_split, int* zs) {
   return static_cast<int>(ceil_div(C, *c_split));
 }
 
-cudaError_t shrink(const void* src, const void* w, bool trans, const int* ids, float* part, int64_t M, int64_t C, int64_t n, int64_t r,
+cudaError_t shrink(const void* src, const void* w, bool trans, const int* ids, int* table, float* part, int64_t M, int64_t C, int64_t n, int64_t r,
                    int* splits, cudaStream_t stream) {
   ShrinkParams p = {};
   p.src = static_cast<const __nv_bfloat16*>(src);
   p.p = static_cast<const __nv_bfloat16*>(w);
   p.ids = ids;
+  p.table = table;
   p.part = part;
   p.M = M;
   p.C = C;
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
-  *splits = shrink_splits(M, C, &p.c_split, &p.zs);
+  *splits = shrink_splits(M, C, n, &p.c_split, &p.zs);
   const dim3 grid(static_cast<unsigned>(ceil_div(M, kChunk) * p.zs), static_cast<unsigned>(*splits));
   if (!trans) {
     if (r <= 16) return launch(rfq_lora_shrink_direct_kernel<2>, p, grid, 0, stream);
@@ -1136,12 +1204,12 @@ cudaError_t shrink(const void* src, const void* w, bool trans, const int* ids, f
 
 template <bool kF32>
 cudaError_t expand_typed(ExpandParams p, bool trans, cudaStream_t stream) {
-  const int64_t chunks = ceil_div(p.M, kChunk), z = chunk_ctas(p.M, 2 * kPlanSms);
+  const int64_t chunks = ceil_div(p.M, kChunk), z = chunk_ctas(p.M, p.n, 2 * kPlanSms);
   p.zs = static_cast<int>(z);
-  // Column tiles of a CTA: eight CTAs per SM over all for the direct kernel (a tile a warp at least),
-  // two for the other.
+  // Column tiles of a CTA: one wave of CTAs, three per SM for the direct kernel (and a tile a warp at
+  // least), two for the other.
   const int64_t tiles = ceil_div(p.C, trans ? kBN<kF32> : 32);
-  int64_t parts = (trans ? 2 : 8) * kPlanSms / (chunks * z);
+  int64_t parts = (trans ? 2 : 3) * kPlanSms / (chunks * z);
   if (!trans && parts > ceil_div(tiles, 8)) parts = ceil_div(tiles, 8);
   if (parts > tiles) parts = tiles;
   if (parts < 1) parts = 1;
@@ -1153,13 +1221,13 @@ cudaError_t expand_typed(ExpandParams p, bool trans, cudaStream_t stream) {
   return launch(rfq_lora_expand_kernel<kF32>, p, grid, static_cast<size_t>(p.stages) * stage + other, stream);
 }
 
-cudaError_t expand(const float* part, int splits, const float* scale, const void* w, bool trans, const int* ids, const void* base,
+cudaError_t expand(const float* part, int splits, const float* scale, const void* w, bool trans, const int* table, const void* base,
                    void* out, bool f32, float* hidden, int64_t M, int64_t C, int64_t n, int64_t r, cudaStream_t stream) {
   ExpandParams p = {};
   p.part = part;
   p.scale = scale;
   p.q = static_cast<const __nv_bfloat16*>(w);
-  p.ids = ids;
+  p.table = table;
   p.base = base;
   p.out = out;
   p.hidden = hidden;
@@ -1186,7 +1254,7 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Rows of one range of the outer products: one wave of two CTAs per SM over all column tiles.
 int outer_range(int64_t M, int64_t tiles) {
-  const int64_t want = ceil_div(2 * kPlanSms, tiles);
+  const int64_t want = tiles < 2 * kPlanSms ? 2 * kPlanSms / tiles : 1;
   int64_t rows = ceil_div(ceil_div(M, want), kOuterRows) * kOuterRows;
   if (rows < 256) rows = 256;
   if (rows > kMaxRange) rows = kMaxRange;
@@ -1194,15 +1262,14 @@ int outer_range(int64_t M, int64_t tiles) {
 }
 
 struct BackwardPlan {
-  size_t part, ds, s, part_a, part_b, present, bytes;
+  size_t table, part, ds, s, part_a, part_b, present, bytes;
   int range, ranges;
 };
-// fp32 outputs take three terms, bf16 ones two; the workspace is sized for three.
+// fp32 results take three terms, bf16 ones two; the workspace is sized for three.
 BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
   BackwardPlan b;
   int64_t cs;
   int z;
-  const int splits = wide(M, n) ? 1 : shrink_splits(M, N, &cs, &z);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -1211,7 +1278,9 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
   };
   b.range = outer_range(M, ceil_div(K, kOuterCols) + ceil_div(N, kOuterCols));
   b.ranges = static_cast<int>(ceil_div(M, b.range));
-  b.part = take(static_cast<size_t>(splits) * M * r * 4);
+  const bool chunks = wide(M, n);
+  b.table = take(chunks ? 0 : static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4);
+  b.part = take(chunks ? 0 : static_cast<size_t>(shrink_splits(M, N, n, &cs, &z)) * M * r * 4);
   b.ds = take(static_cast<size_t>(3) * M * r * 2);
   b.s = take(static_cast<size_t>(3) * M * r * 2);
   b.part_a = take(static_cast<size_t>(b.ranges) * n * r * K * 4);
@@ -1224,9 +1293,11 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
 }  // namespace
 
 size_t lora_forward_workspace(int64_t M, int64_t K, int64_t r, int64_t n) {
+  if (wide(M, n)) return align256(static_cast<size_t>(3) * M * r * 2);
   int64_t cs;
   int z;
-  return align256(static_cast<size_t>(wide(M, n) ? 1 : shrink_splits(M, K, &cs, &z)) * M * r * 4);
+  return align256(static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4) +
+         align256(static_cast<size_t>(shrink_splits(M, K, n, &cs, &z)) * M * r * 4);
 }
 
 size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
@@ -1236,18 +1307,19 @@ size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64
 cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* base,
                                 void* y, bool y_bf16, float* hidden, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n,
                                 void* ws, int num_sms, void* encode_tiled, cudaStream_t stream) {
-  float* part = static_cast<float*>(ws);
-  int splits = 1;
   cudaError_t e;
   if (wide(M, n)) {
-    float* s = hidden != nullptr ? hidden : part;
-    e = launch_lora_shrink_wide(x, a, false, ids, scale, s, M, K, n, r, num_sms, encode_tiled, stream);
+    const int terms = y_bf16 ? 1 : 3;
+    e = launch_lora_shrink_wide(x, a, false, ids, scale, hidden, ws, terms, M, K, n, r, num_sms, encode_tiled, stream);
     if (e != cudaSuccess) return e;
-    return launch_lora_expand_wide(s, b, false, ids, base, y, !y_bf16, M, N, n, r, num_sms, encode_tiled, stream);
+    return launch_lora_expand_wide(ws, terms, b, false, ids, base, y, !y_bf16, M, N, n, r, num_sms, encode_tiled, stream);
   }
-  e = shrink(x, a, false, ids, part, M, K, n, r, &splits, stream);
+  int* table = static_cast<int*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4));
+  int splits = 1;
+  e = shrink(x, a, false, ids, table, part, M, K, n, r, &splits, stream);
   if (e != cudaSuccess) return e;
-  return expand(part, splits, scale, b, false, ids, base, y, !y_bf16, hidden, M, N, n, r, stream);
+  return expand(part, splits, scale, b, false, table, base, y, !y_bf16, hidden, M, N, n, r, stream);
 }
 
 cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* dy,
@@ -1257,50 +1329,52 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   const BackwardPlan pl = plan_backward(M, K, N, r, n);
   uint8_t* base = static_cast<uint8_t*>(ws);
   float* part = reinterpret_cast<float*>(base + pl.part);
+  int* table = reinterpret_cast<int*>(base + pl.table);
   __nv_bfloat16* ds = reinterpret_cast<__nv_bfloat16*>(base + pl.ds);
   __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(base + pl.s);
-  const bool by_chunks = wide(M, n);
+  const bool chunks = wide(M, n);
+  const int terms = grad_bf16 ? 2 : 3;
+  // Terms of ds' as shrink leaves them: what the adapters' gradients or an fp32 dx need.
+  const int ds_terms = dx != nullptr && !dx_bf16 ? 3 : terms;
   int splits = 1;
   cudaError_t e = cudaSuccess;
   if (dx != nullptr || da != nullptr) {
-    e = by_chunks ? launch_lora_shrink_wide(dy, b, true, ids, scale, part, M, N, n, r, num_sms, encode_tiled, stream)
-                  : shrink(dy, b, true, ids, part, M, N, n, r, &splits, stream);
+    e = chunks ? launch_lora_shrink_wide(dy, b, true, ids, scale, nullptr, ds, ds_terms, M, N, n, r, num_sms, encode_tiled, stream)
+               : shrink(dy, b, true, ids, table, part, M, N, n, r, &splits, stream);
     if (e != cudaSuccess) return e;
   }
   if (dx != nullptr) {
-    e = by_chunks ? launch_lora_expand_wide(part, a, true, ids, dx_base, dx, !dx_bf16, M, K, n, r, num_sms, encode_tiled, stream)
-                  : expand(part, splits, scale, a, true, ids, dx_base, dx, !dx_bf16, nullptr, M, K, n, r, stream);
+    e = chunks ? launch_lora_expand_wide(ds, ds_terms, a, true, ids, dx_base, dx, !dx_bf16, M, K, n, r, num_sms, encode_tiled, stream)
+               : expand(part, splits, scale, a, true, table, dx_base, dx, !dx_bf16, nullptr, M, K, n, r, stream);
     if (e != cudaSuccess) return e;
   }
-  const float* part_scale = by_chunks ? nullptr : scale;
   if (da == nullptr && db == nullptr) return e;
-  {
+  SplitParams sp = {};
+  sp.part = part;
+  sp.scale = scale;
+  sp.ids = ids;
+  sp.hidden = hidden;
+  sp.M = M;
+  sp.n = static_cast<int>(n);
+  sp.r = static_cast<int>(r);
+  sp.splits = splits;
+  sp.ds = da != nullptr && !chunks ? ds : nullptr;
+  sp.s = db != nullptr ? s : nullptr;
+  if (sp.ds != nullptr || sp.s != nullptr) {
     const int64_t blocks = ceil_div(M * r, kThreads);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks < 8 * kPlanSms ? blocks : 8 * kPlanSms));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    __nv_bfloat16* ds_out = da != nullptr ? ds : nullptr;
-    __nv_bfloat16* s_out = db != nullptr ? s : nullptr;
-    const float* cpart = part;
-    e = grad_bf16 ? cudaLaunchKernelEx(&cfg, rfq_lora_split_kernel<2>, cpart, part_scale, ids, static_cast<int>(n), M, static_cast<int>(r),
-                                       splits, ds_out, hidden, s_out)
-                  : cudaLaunchKernelEx(&cfg, rfq_lora_split_kernel<3>, cpart, part_scale, ids, static_cast<int>(n), M, static_cast<int>(r),
-                                       splits, ds_out, hidden, s_out);
+    const dim3 sgrid(static_cast<unsigned>(blocks < 8 * kPlanSms ? blocks : 8 * kPlanSms));
+    e = grad_bf16 ? launch(rfq_lora_split_kernel<2>, sp, sgrid, 0, stream) : launch(rfq_lora_split_kernel<3>, sp, sgrid, 0, stream);
     if (e != cudaSuccess) return e;
   }
   OuterParams o = {};
   o.side[0].v = ds;
+  o.side[0].ld = static_cast<int>((chunks ? ds_terms : terms) * r);
   o.side[0].w = static_cast<const __nv_bfloat16*>(x);
   o.side[0].part = reinterpret_cast<float*>(base + pl.part_a);
   o.side[0].C = K;
   o.side[0].tiles = da != nullptr ? static_cast<int>(ceil_div(K, kOuterCols)) : 0;
   o.side[1].v = s;
+  o.side[1].ld = static_cast<int>(terms * r);
   o.side[1].w = static_cast<const __nv_bfloat16*>(dy);
   o.side[1].part = reinterpret_cast<float*>(base + pl.part_b);
   o.side[1].C = N;

@@ -19,6 +19,8 @@
 // through distributed shared memory in the order of the ranks.  The accumulator takes 1024
 // elements of the contraction at a time (the tensor cores add by truncation) and the epilogue
 // adds those parts with rounding.
+// shrink leaves s as bf16 terms (one for a bf16 output; three, 24 bits, for an fp32 one), which are
+// expand's operand as they are.
 // expand: base tiles come in by TMA, are added to in shared memory and leave from there by TMA.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, the others epilogue.  Every wait on an mbarrier
@@ -127,7 +129,9 @@ struct ShrinkMaps {
 struct ShrinkParams {
   const int* ids;
   const float* scale;
-  float* s;            // [M][r]
+  float* s;                // [M][r] or nullptr
+  __nv_bfloat16* terms;    // [M][num_terms][r]: s as a sum of bf16 terms
+  int num_terms;
   int64_t M;
   int n, r, kt, kt_per_rank, cluster, stages;
 };
@@ -315,25 +319,34 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
       const float w = p.scale[a];
       v.x *= w; v.y *= w; v.z *= w; v.w *= w;
     }
-    *reinterpret_cast<float4*>(p.s + row * p.r + j) = v;
+    if (p.s != nullptr) *reinterpret_cast<float4*>(p.s + row * p.r + j) = v;
+    __nv_bfloat16* t = p.terms + row * p.num_terms * p.r + j;
+    for (int e = 0; e < p.num_terms; ++e) {   // 8 bits each
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      *reinterpret_cast<uint2*>(t + e * p.r) = w;
+      v.x -= __uint_as_float(w.x << 16);
+      v.y -= __uint_as_float(w.x & 0xffff0000u);
+      v.z -= __uint_as_float(w.y << 16);
+      v.w -= __uint_as_float(w.y & 0xffff0000u);
+    }
   }
   cluster_sync();   // the others may still be reading this CTA's sums
 }
 
 // ---------------------------------------------------------------- expand
 struct ExpandMaps {
-  CUtensorMap q, base, out;
+  CUtensorMap s, q, base, out;
 };
 struct ExpandParams {
   const int* ids;
-  const float* s;       // [M][r]
   int64_t M;
   int C;
   int n, r;
   int has_base, in_place;
   int tiles, unit_tiles, col_units;   // column tiles in all, of one unit; units along the columns
   int64_t units;
-  int base_stages, q_stages;
+  int s_stages, base_stages, q_stages;
 };
 
 constexpr int kExpandThreads = 320;    // TMA, MMA, eight epilogue warps
@@ -363,7 +376,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
   constexpr int kBoxCols = kN / 2;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t b_full[kMaxStages], b_empty[kMaxStages], q_full[kMaxStages], q_empty[kMaxStages], acc_full[2], acc_empty[2],
-      s_full, drained;
+      s_full[2], s_empty[2], drained;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -371,8 +384,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t r16 = (p.r + 15) / 16 * 16;
   const uint32_t q_bytes = expand_q_bytes<kTrans, kF32>(p.r);
+  const uint32_t s_bytes = expand_s_bytes<kF32>(p.r);
   uint8_t* s_mem = smem;                                           // [r / 64][term][128 rows x 128 bytes]
-  uint8_t* b_mem = s_mem + expand_s_bytes<kF32>(p.r);              // base tiles: two boxes each
+  uint8_t* b_mem = s_mem + p.s_stages * s_bytes;                   // base tiles: two boxes each
   uint8_t* q_mem = b_mem + p.base_stages * 2 * kBox;
 
   if (threadIdx.x == 0) {
@@ -386,10 +400,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 8);
     }
-    mbar_init(&s_full, 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_empty[b], 1);
+    }
     mbar_init(&drained, 1);
     abort_word = 0;
     fence_mbar_init();
+    prefetch_tmap(&maps.s);
     prefetch_tmap(&maps.q);
     prefetch_tmap(&maps.base);
     prefetch_tmap(&maps.out);
@@ -409,14 +427,28 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
   // base is the output, there is nothing to do; every role finds that out for itself.
   Walk walk;
   if (warp == 0) {
-    Cursor bc, qc;
-    Filled b_filled, q_filled;
+    Cursor sc, bc, qc;
+    Filled s_filled, b_filled, q_filled;
     bool ok = true;
     for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
       const int64_t row0 = unit / p.col_units * kChunk;
       const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
       walk.load(p.ids, row0, p.M, p.n);
-      if (p.in_place && !__any_sync(0xffffffffu, walk.left != 0)) continue;
+      const bool any = __any_sync(0xffffffffu, walk.left != 0);
+      if (!any && p.in_place) continue;
+      if (any && lane == 0) {
+        ok = mbar_wait(&s_empty[sc.stage], sc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
+        if (ok) {
+          uint8_t* ss = s_mem + sc.stage * s_bytes;
+          mbar_arrive_expect_tx(&s_full[sc.stage], s_bytes);
+          for (int k = 0; k < p.r; k += 64)
+            for (int e = 0; e < kT; ++e)
+              tma_load_3d(ss + ((k >> 6) * kT + e) * kBox, &maps.s, &s_full[sc.stage], k, e, static_cast<int>(row0));
+          s_filled.add(sc);
+          sc.next(p.s_stages);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
       for (int t = t0; t < t1 && ok; ++t) {
         const int col = t * kN;
         if (p.has_base && lane == 0) {
@@ -454,13 +486,15 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
       }
     }
     if (lane == 0) {
+      s_filled.drain(s_full, p.s_stages);
       b_filled.drain(b_full, p.base_stages);
       q_filled.drain(q_full, p.q_stages);
     }
     __syncwarp();
   } else if (warp == 1) {
-    Cursor qc, acc;
-    uint32_t s_phase = 0;
+    Cursor sc, qc, acc;
+    int last = -1;
+    uint32_t last_phase = 0;
     bool ok = true;
     const uint32_t id = idesc(kN, kTrans);
     for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
@@ -469,10 +503,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
       walk.load(p.ids, row0, p.M, p.n);
       if (!__any_sync(0xffffffffu, walk.left != 0)) continue;
       if (lane == 0) {
-        ok = mbar_wait(&s_full, s_phase, abort_flag, &g_lora_error, kErrWaitFull);
+        ok = mbar_wait(&s_full[sc.stage], sc.phase, abort_flag, &g_lora_error, kErrWaitFull);
         tc_fence_after();
       }
-      s_phase ^= 1u;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       for (int t = t0; t < t1 && ok; ++t) {
         walk.restart();
@@ -483,7 +516,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
             if (ok) {
               tc_fence_after();
               const uint32_t d = tmem + acc.stage * 128;
-              const uint32_t sq = smem_addr(q_mem) + qc.stage * q_bytes, sa = smem_addr(s_mem);
+              const uint32_t sq = smem_addr(q_mem) + qc.stage * q_bytes, sa = smem_addr(s_mem) + sc.stage * s_bytes;
               uint32_t more = 0;
               for (uint32_t k = 0; k < r16 / 16; ++k) {
                 const uint64_t db = kTrans ? mn_major_desc(sq, r16 * 128) + 128 * k : k_major_desc(sq + (k >> 2) * kN * 128) + 2 * (k & 3);
@@ -502,11 +535,23 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
       }
-      if (!ok && lane == 0) {   // teardown after an abort: wait for the MMAs already issued
-        tc_commit(&drained);
-        int never = 0;
-        mbar_wait(&drained, 0, &never, &g_lora_error, kErrWaitDrain);
+      if (lane == 0) {
+        if (ok) {
+          tc_commit(&s_empty[sc.stage]);   // with the last MMA of the unit
+          last = static_cast<int>(sc.stage);
+          last_phase = sc.phase;
+        } else {                           // teardown after an abort: wait for the MMAs already issued
+          tc_commit(&drained);
+          int never = 0;
+          mbar_wait(&drained, 0, &never, &g_lora_error, kErrWaitDrain);
+        }
       }
+      sc.next(p.s_stages);
+    }
+    // The last commit arrives on a barrier of this CTA: it has done so before the CTA leaves.
+    if (lane == 0 && ok && last >= 0) {
+      int never = 0;
+      mbar_wait(&s_empty[last], last_phase, &never, &g_lora_error, kErrWaitDrain);
     }
     __syncwarp();
   } else {
@@ -521,37 +566,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
       const bool any = __any_sync(0xffffffffu, walk.left != 0);
       if (!any && p.in_place) continue;
       const int mine = quad == 0 ? walk.id[0] : quad == 1 ? walk.id[1] : quad == 2 ? walk.id[2] : walk.id[3];
-      if (any) {
-        // s of this chunk in the operand's layout.  The MMAs that read the one before have ended:
-        // their accumulators have been taken.
-        const float* src = p.s + (row0 + row) * p.r;
-        for (int c = half; c < static_cast<int>(r16 / 8); c += 2) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = 0.f;
-          if (mine >= 0 && 8 * c < p.r) {
-            const float4 x = *reinterpret_cast<const float4*>(src + 8 * c), y = *reinterpret_cast<const float4*>(src + 8 * c + 4);
-            f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-            f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-          }
-          uint8_t* to = s_mem + (c >> 3) * kT * kBox + row * 128 + ((c & 7) ^ (row & 7)) * 16;
-#pragma unroll
-          for (int e = 0; e < kT; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * h], f[2 * h + 1]);
-              w[h] = *reinterpret_cast<const uint32_t*>(&b);
-              f[2 * h] -= __uint_as_float(w[h] << 16);
-              f[2 * h + 1] -= __uint_as_float(w[h] & 0xffff0000u);
-            }
-            *reinterpret_cast<uint4*>(to + e * kBox) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_full);
-      }
       for (int t = t0; t < t1; ++t) {
         if (p.has_base) mbar_wait(&b_full[bc.stage], bc.phase, abort_flag, &g_lora_error, kErrWaitFull, 2 * kWaitLimitNs);
         uint8_t* sb = b_mem + bc.stage * 2 * kBox;
@@ -691,21 +705,26 @@ cudaError_t launch(Kernel kernel, const Maps& maps, const Params& p, int64_t gri
 template <bool kTrans, bool kF32>
 cudaError_t expand_typed(const ExpandMaps& maps, ExpandParams p, int num_sms, cudaStream_t stream) {
   const uint32_t q = expand_q_bytes<kTrans, kF32>(p.r), s = expand_s_bytes<kF32>(p.r);
-  const uint32_t room = kSmemLimit - 4096 - s;   // 4 KiB: alignment and the static part
+  uint32_t room = kSmemLimit - 4096 - s;   // 4 KiB: alignment and the static part
+  p.s_stages = 1;
+  if (room >= s + 3 * 2 * kBox + 2 * q) {
+    p.s_stages = 2;
+    room -= s;
+  }
   p.q_stages = 2;
   p.base_stages = 2;
   while (p.base_stages < 4 && (p.base_stages + 1) * 2 * kBox + p.q_stages * q <= room) ++p.base_stages;
   while (p.q_stages < 4 && p.base_stages * 2 * kBox + (p.q_stages + 1) * q <= room) ++p.q_stages;
-  const size_t smem = 1024 + s + p.base_stages * 2 * kBox + p.q_stages * q;
+  const size_t smem = 1024 + p.s_stages * s + p.base_stages * 2 * kBox + p.q_stages * q;
   const int64_t grid = p.units < num_sms ? p.units : num_sms;
   return launch(rfq_lora_expand_wide_kernel<kTrans, kF32>, maps, p, grid, kExpandThreads, smem, 1, stream);
 }
 
 }  // namespace
 
-// s [M][r] = scale (P src), P the pool [n][r][C] or (trans) [n][C][r].
+// s [M][r] (or nullptr) = scale (P src), P the pool [n][r][C] or (trans) [n][C][r]; terms [M][num_terms][r].
 cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool trans, const int* ids, const float* scale, float* s,
-                                    int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream) {
+                                    void* terms, int num_terms, int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
   ShrinkMaps maps;
   const uint32_t r16 = static_cast<uint32_t>((r + 15) / 16 * 16);
@@ -716,6 +735,8 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
   p.ids = ids;
   p.scale = scale;
   p.s = s;
+  p.terms = static_cast<__nv_bfloat16*>(terms);
+  p.num_terms = num_terms;
   p.M = M;
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
@@ -739,8 +760,9 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
                : launch(rfq_lora_shrink_wide_kernel<false>, maps, p, chunks * p.cluster, kShrinkThreads, smem, p.cluster, stream);
 }
 
-// out [M][C] = base + Q s, Q the pool [n][C][r] or (trans) [n][r][C].
-cudaError_t launch_lora_expand_wide(const float* s, const void* pool, bool trans, const int* ids, const void* base, void* out, bool f32,
+// out [M][C] = base + Q s, s from its terms (all of num_terms lie there; the output's type says how many
+// are taken), Q the pool [n][C][r] or (trans) [n][r][C].
+cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const void* pool, bool trans, const int* ids, const void* base, void* out, bool f32,
                                     int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
   ExpandMaps maps;
@@ -749,12 +771,21 @@ cudaError_t launch_lora_expand_wide(const float* s, const void* pool, bool trans
   auto wide_map = [&](CUtensorMap* map, const void* at) {
     return f32 ? encode_f32_map(encode, map, at, M, C) : encode_bf16_map(encode, map, at, M, C, C, kChunk);
   };
-  if (!wide_map(&maps.out, out) || !wide_map(&maps.base, base != nullptr ? base : out) ||
+  // [M][term][r] as (r, term, M): a box is one term of 128 rows, zeros behind r.
+  auto s_map = [&](CUtensorMap* map) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(r), static_cast<cuuint64_t>(num_terms), static_cast<cuuint64_t>(M)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(r) * 2, static_cast<cuuint64_t>(r) * 2 * num_terms};
+    cuuint32_t box[3] = {64u, 1u, kChunk};
+    cuuint32_t one[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(terms), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!s_map(&maps.s) || !wide_map(&maps.out, out) || !wide_map(&maps.base, base != nullptr ? base : out) ||
       !(trans ? encode_pool_map(encode, &maps.q, pool, n, r, C, r16) : encode_pool_map(encode, &maps.q, pool, n, C, r, cols)))
     return cudaErrorInvalidValue;
   ExpandParams p = {};
   p.ids = ids;
-  p.s = s;
   p.M = M;
   p.C = static_cast<int>(C);
   p.n = static_cast<int>(n);
@@ -763,12 +794,12 @@ cudaError_t launch_lora_expand_wide(const float* s, const void* pool, bool trans
   p.in_place = base == out;
   p.tiles = static_cast<int>(ceil_div(C, cols));
   // Column tiles of one unit: the length (4 to 16 tiles) that leaves the fewest tiles to the CTA
-  // with the most, each unit charged one more for the change of rows.
+  // with the most, each unit charged a quarter of one more for the change of rows.
   const int64_t chunks = ceil_div(M, kChunk);
   int64_t best = INT64_MAX;
   p.unit_tiles = p.tiles;
   for (int len = 4; len <= 16; ++len) {
-    const int64_t units = chunks * ceil_div(p.tiles, len), cost = ceil_div(units, num_sms) * (len + 1);
+    const int64_t units = chunks * ceil_div(p.tiles, len), cost = ceil_div(units, num_sms) * (4 * len + 1);
     if (cost < best) {
       best = cost;
       p.unit_tiles = len;
