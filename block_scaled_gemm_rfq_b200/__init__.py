@@ -152,32 +152,23 @@ def _stream(stream):
 
 def _need(where, t, shape, dtype, device):
     """Refuse a tensor that is not what the C call will read: its type, shape, packing or device."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise RFQError(1, f"{where}: want a contiguous {dtype} tensor {shape} on {device}, got {t.dtype} "
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise RFQError(1, f"{where}: want a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
                           f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-class _On:
-    """The launch's device and stream: the tensors' device is made current for the call, and without
-    a stream the current stream of that device is taken."""
-
-    __slots__ = ("guard", "stream")
-
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise RFQError(1, f"tensors on {device}: a CUDA device is needed")
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.stream = stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(where, device, stream, fn, *args):
+    """fn(*args, stream) on `device`: made current for the call where it is not, and without a stream the
+    current stream of that device is taken."""
+    import torch
+    if device.type != "cuda":
+        raise RFQError(1, f"{where}: tensors on {device}: a CUDA device is needed")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _check(fn(*args, _stream(stream)), where)
+    # the raw handle: current_stream() builds a Stream object, 3 us a call
+    st = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+    return _check(fn(*args, st), where)
 
 
 def _need_workspace(where, ws, device):
@@ -357,10 +348,8 @@ def linear_ce(h, w, labels, loss, lse, workspace, ignore_index=-100, stream=None
     _need("rfq_linear_ce: loss", loss, (T,), torch.float32, dev)
     _need("rfq_linear_ce: lse", lse, (T,), torch.float32, dev)
     _need_workspace("rfq_linear_ce", workspace, dev)
-    with _On(dev, stream) as st:
-        _check(load_library().rfq_linear_ce(h.data_ptr(), w.data_ptr(), labels.data_ptr(), T, D, V, ignore_index,
-                                            loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                            st), "rfq_linear_ce")
+    _call("rfq_linear_ce", dev, stream, load_library().rfq_linear_ce, h.data_ptr(), w.data_ptr(), labels.data_ptr(),
+              T, D, V, ignore_index, loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def linear_ce_backward(h, w, labels, lse, dloss, dh, dw, workspace, ignore_index=-100, stream=None):
@@ -380,10 +369,9 @@ def linear_ce_backward(h, w, labels, lse, dloss, dh, dw, workspace, ignore_index
     if dw is not None:
         _need("rfq_linear_ce_backward: dw", dw, (V, D), torch.bfloat16, dev)
     _need_workspace("rfq_linear_ce_backward", workspace, dev)
-    with _On(dev, stream) as st:
-        _check(load_library().rfq_linear_ce_backward(
-            h.data_ptr(), w.data_ptr(), labels.data_ptr(), lse.data_ptr(), dloss.data_ptr(), T, D, V, ignore_index,
-            _ptr(dh), _ptr(dw), workspace.data_ptr(), workspace.numel(), st), "rfq_linear_ce_backward")
+    _call("rfq_linear_ce_backward", dev, stream, load_library().rfq_linear_ce_backward, h.data_ptr(), w.data_ptr(),
+              labels.data_ptr(), lse.data_ptr(), dloss.data_ptr(), T, D, V, ignore_index, _ptr(dh), _ptr(dw),
+              workspace.data_ptr(), workspace.numel())
 
 
 def lora_workspace_bytes(M: int, K: int, N: int, rank: int, n_adapters: int, backward: bool = False) -> int:
@@ -435,10 +423,9 @@ def lora(x, a, b, scale, ids, y, workspace, base=None, hidden=None, stream=None)
     if hidden is not None:
         _need("rfq_lora: hidden", hidden, (M, r), torch.float32, dev)
     _need_workspace("rfq_lora", workspace, dev)
-    with _On(dev, stream) as st:
-        _check(load_library().rfq_lora(x.data_ptr(), M, K, a.data_ptr(), b.data_ptr(), scale.data_ptr(), ids.data_ptr(),
-                                       n, r, N, _ptr(base), y.data_ptr(), y_type, _ptr(hidden), workspace.data_ptr(),
-                                       workspace.numel(), st), "rfq_lora")
+    _call("rfq_lora", dev, stream, load_library().rfq_lora, x.data_ptr(), M, K, a.data_ptr(), b.data_ptr(),
+              scale.data_ptr(), ids.data_ptr(), n, r, N, _ptr(base), y.data_ptr(), y_type, _ptr(hidden),
+              workspace.data_ptr(), workspace.numel())
 
 
 def lora_backward(x, a, b, scale, ids, dy, hidden, workspace, dx=None, dx_base=None, da=None, db=None, stream=None):
@@ -464,11 +451,9 @@ def lora_backward(x, a, b, scale, ids, dy, hidden, workspace, dx=None, dx_base=N
             grad_type = _out_type(f"{where}: {name}", t)
             _need(f"{where}: {name}", t, shape, t.dtype if name == "da" or da is None else da.dtype, dev)
     _need_workspace(where, workspace, dev)
-    with _On(dev, stream) as st:
-        _check(load_library().rfq_lora_backward(
-            _ptr(x), M, K, a.data_ptr(), b.data_ptr(), scale.data_ptr(), ids.data_ptr(), n, r, N, dy.data_ptr(), _ptr(hidden),
-            _ptr(dx_base), _ptr(dx), dx_type, _ptr(da), _ptr(db), grad_type, workspace.data_ptr(), workspace.numel(), st),
-            "rfq_lora_backward")
+    _call("rfq_lora_backward", dev, stream, load_library().rfq_lora_backward, _ptr(x), M, K, a.data_ptr(),
+              b.data_ptr(), scale.data_ptr(), ids.data_ptr(), n, r, N, dy.data_ptr(), _ptr(hidden), _ptr(dx_base),
+              _ptr(dx), dx_type, _ptr(da), _ptr(db), grad_type, workspace.data_ptr(), workspace.numel())
 
 
 def linear_lora(x, qw_codes, qw_scales, N, a, b, scale, ids, y, workspace, use_residual=True, hidden=None, stream=None):
@@ -486,11 +471,9 @@ def linear_lora(x, qw_codes, qw_scales, N, a, b, scale, ids, y, workspace, use_r
     if hidden is not None:
         _need("rfq_linear_lora: hidden", hidden, (M, r), torch.float32, dev)
     _need_workspace("rfq_linear_lora", workspace, dev)
-    with _On(dev, stream) as st:
-        _check(load_library().rfq_linear_lora(
-            x.data_ptr(), M, K, qw_codes.data_ptr(), qw_scales.data_ptr(), N, a.data_ptr(), b.data_ptr(), scale.data_ptr(),
-            ids.data_ptr(), n, r, y.data_ptr(), y_type, int(bool(use_residual)), _ptr(hidden), workspace.data_ptr(),
-            workspace.numel(), st), "rfq_linear_lora")
+    _call("rfq_linear_lora", dev, stream, load_library().rfq_linear_lora, x.data_ptr(), M, K, qw_codes.data_ptr(),
+              qw_scales.data_ptr(), N, a.data_ptr(), b.data_ptr(), scale.data_ptr(), ids.data_ptr(), n, r,
+              y.data_ptr(), y_type, int(bool(use_residual)), _ptr(hidden), workspace.data_ptr(), workspace.numel())
 
 
 def grad_clip_workspace_bytes(count: int) -> int:
@@ -498,22 +481,18 @@ def grad_clip_workspace_bytes(count: int) -> int:
     return int(load_library().rfq_grad_clip_workspace_bytes(count))
 
 
-def _tensor_list(where, tensors, device, like=None):
+def _tensor_list(where, tensors, device):
     """Host arrays (addresses, element counts, types) of a list of contiguous bf16 / fp32 tensors on one device."""
     import torch
     T = torch.Tensor
-    dtypes = [t.dtype for t in tensors]
-    if like is not None and [t.dtype for t in like] != dtypes:
-        raise RFQError(1, f"{where}: an output has the type of its gradient")
-    if any(d is not torch.bfloat16 and d is not torch.float32 for d in dtypes):
-        raise RFQError(1, f"{where}: want bfloat16 or float32 tensors")
-    if not all(map(T.is_contiguous, tensors)) or not set(map(T.get_device, tensors)) <= {device.index}:
+    code = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+    try:
+        types = array.array("i", [code[t.dtype] for t in tensors])
+    except KeyError as e:
+        raise RFQError(1, f"{where}: want bfloat16 or float32 tensors, got {e.args[0]}") from None
+    if not all(map(T.is_contiguous, tensors)) or not {device.index}.issuperset(map(T.get_device, tensors)):
         raise RFQError(1, f"{where}: want contiguous tensors on {device}")
-    numels = array.array("q", map(T.numel, tensors))
-    if like is not None and numels != array.array("q", map(T.numel, like)):
-        raise RFQError(1, f"{where}: an output has the size of its gradient")
-    types = array.array("i", [OUT_BF16 if d is torch.bfloat16 else OUT_F32 for d in dtypes])
-    return array.array("Q", map(T.data_ptr, tensors)), numels, types
+    return array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), types
 
 
 def _norm_args(where, grads, norm, workspace):
@@ -528,9 +507,9 @@ def grad_norm(grads, norm, workspace, stream=None):
     """rfq_grad_norm: norm (one fp32 on the device) = the 2-norm over all elements of a list of bf16 / fp32 tensors."""
     grads = list(grads)
     ptrs, numels, types = _norm_args("rfq_grad_norm", grads, norm, workspace)
-    with _On(norm.device, stream) as st:
-        _check(load_library().rfq_grad_norm(ptrs.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0], len(grads),
-                                            norm.data_ptr(), workspace.data_ptr(), workspace.numel(), st), "rfq_grad_norm")
+    _call("rfq_grad_norm", norm.device, stream, load_library().rfq_grad_norm, ptrs.buffer_info()[0],
+              numels.buffer_info()[0], types.buffer_info()[0], len(grads), norm.data_ptr(), workspace.data_ptr(),
+              workspace.numel())
 
 
 def grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None):
@@ -543,12 +522,12 @@ def grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None):
         outs = list(outs)
         if len(outs) != len(grads):
             raise RFQError(1, "rfq_grad_clip: one output for each gradient")
-        out_ptrs = _tensor_list("rfq_grad_clip: outs", outs, norm.device, like=grads)[0]
-    with _On(norm.device, stream) as st:
-        _check(load_library().rfq_grad_clip(
-            ptrs.buffer_info()[0], None if out_ptrs is None else out_ptrs.buffer_info()[0], numels.buffer_info()[0],
-            types.buffer_info()[0], len(grads), float(max_norm), norm.data_ptr(), workspace.data_ptr(), workspace.numel(), st),
-            "rfq_grad_clip")
+        out_ptrs, out_numels, out_types = _tensor_list("rfq_grad_clip: outs", outs, norm.device)
+        if out_numels != numels or out_types != types:
+            raise RFQError(1, "rfq_grad_clip: an output has the type and size of its gradient")
+    _call("rfq_grad_clip", norm.device, stream, load_library().rfq_grad_clip, ptrs.buffer_info()[0], None if
+              out_ptrs is None else out_ptrs.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0],
+              len(grads), float(max_norm), norm.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def check_device_error(stream=None):

@@ -120,40 +120,40 @@ __global__ void __launch_bounds__(kThreads) rfq_clip_norm_kernel(const __grid_co
     const Piece p = find(tab, k, t);
     const void* in = tab.in[t];
     float s = 0.f, top = 0.f;
-    const bool vec = (reinterpret_cast<uintptr_t>(in) & 15u) == 0;   // p.at is a multiple of kPiece
-    if (vec && p.n == kPiece) {
-      float f[kVecs][8];
+    // Vectors of eight as far as they go (p.at is a multiple of kPiece), the rest one by one.
+    const int whole = (reinterpret_cast<uintptr_t>(in) & 15u) == 0 ? p.n & ~7 : 0;
+    float f[kVecs][8];
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) load8(in, p.at + (v * kThreads + threadIdx.x) * 8, p.f32, f[v]);
+    for (int v = 0; v < kVecs; ++v) {
+      const int i = (v * kThreads + threadIdx.x) * 8;
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v)
+      for (int e = 0; e < 8; ++e) f[v][e] = 0.f;
+      if (i < whole) load8(in, p.at + i, p.f32, f[v]);
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s = fmaf(f[v][e], f[v][e], s);
-          top = fmaxf(top, fabsf(f[v][e]));
-        }
-    } else {
-      for (int i = threadIdx.x; i < p.n; i += kThreads) {
-        const float x = element(in, p.at + i, p.f32);
-        s = fmaf(x, x, s);
-        top = fmaxf(top, fabsf(x));
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s = fmaf(f[v][e], f[v][e], s);
+        top = fmaxf(top, fabsf(f[v][e]));
       }
+    for (int i = whole + threadIdx.x; i < p.n; i += kThreads) {
+      const float x = element(in, p.at + i, p.f32);
+      s = fmaf(x, x, s);
+      top = fmaxf(top, fabsf(x));
     }
     if (s >= 1e-30f && s <= 1e37f) {
       sum += s;
     } else if (s != s || top > 0.f) {
       // Out of fp32's comfortable range (or NaN): this thread's elements once more.
-      if (vec && p.n == kPiece) {
-        for (int v = 0; v < kVecs; ++v)
-          for (int e = 0; e < 8; ++e) {
-            const double x = element(in, p.at + (v * kThreads + threadIdx.x) * 8 + e, p.f32);
-            sum += x * x;
-          }
-      } else {
-        for (int i = threadIdx.x; i < p.n; i += kThreads) {
-          const double x = element(in, p.at + i, p.f32);
+      for (int i = threadIdx.x * 8; i < whole; i += kThreads * 8)
+        for (int e = 0; e < 8; ++e) {
+          const double x = element(in, p.at + i + e, p.f32);
           sum += x * x;
         }
+      for (int i = whole + threadIdx.x; i < p.n; i += kThreads) {
+        const double x = element(in, p.at + i, p.f32);
+        sum += x * x;
       }
     }
   }
@@ -189,22 +189,26 @@ __global__ void __launch_bounds__(kThreads) rfq_clip_scale_kernel(const __grid_c
     const void* in = tab.in[t];
     void* out = tab.out[t];
     if (c == 1.f && in == out) continue;   // multiplying by one changes nothing
-    if (p.n == kPiece && ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
-      float f[kVecs][8];
+    const int whole = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 ? p.n & ~7 : 0;
+    float f[kVecs][8];
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) load8(in, p.at + (v * kThreads + threadIdx.x) * 8, p.f32, f[v]);
+    for (int v = 0; v < kVecs; ++v) {
+      const int i = (v * kThreads + threadIdx.x) * 8;
+      if (i < whole) load8(in, p.at + i, p.f32, f[v]);
+    }
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
+    for (int v = 0; v < kVecs; ++v) {
+      const int i = (v * kThreads + threadIdx.x) * 8;
+      if (i < whole) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[v][e] *= c;
-        store8(out, p.at + (v * kThreads + threadIdx.x) * 8, p.f32, f[v]);
+        store8(out, p.at + i, p.f32, f[v]);
       }
-    } else {
-      for (int i = threadIdx.x; i < p.n; i += kThreads) {
-        const float x = element(in, p.at + i, p.f32) * c;
-        if (p.f32) static_cast<float*>(out)[p.at + i] = x;
-        else static_cast<__nv_bfloat16*>(out)[p.at + i] = __float2bfloat16_rn(x);
-      }
+    }
+    for (int i = whole + threadIdx.x; i < p.n; i += kThreads) {
+      const float x = element(in, p.at + i, p.f32) * c;
+      if (p.f32) static_cast<float*>(out)[p.at + i] = x;
+      else static_cast<__nv_bfloat16*>(out)[p.at + i] = __float2bfloat16_rn(x);
     }
   }
 }

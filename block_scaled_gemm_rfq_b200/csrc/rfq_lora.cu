@@ -53,6 +53,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 256;                // rows grouped by one CTA
 constexpr int kRows = 16;                  // rows of one group
+constexpr int kMaxAdapters = RFQ_LORA_MAX_ADAPTERS;
 constexpr int kMaxStages = 6;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kStaticSmem = 24 * 1024;     // more than any kernel here has besides its dynamic part
@@ -117,13 +118,15 @@ struct Groups {
   int order[kChunk];
   int start[kChunk + 1];
   int items;
-  int flag[kChunk];            // of the grouping alone
+  int keys[kChunk];            // of the grouping alone
+  int runs[kChunk / 32];
+  int firsts[kChunk / 32];
 };
 constexpr int kTable = 3 * kChunk + 2;   // words of a Groups that the next kernel reads back
 
 __device__ void group_rows(Groups& g, const int* ids, int64_t row0, int64_t M, int n) {
-  static_assert(kThreads == kChunk, "a thread for each row");
-  const int t = threadIdx.x;
+  static_assert(kThreads == kChunk && kMaxAdapters < 0x7fffff, "a thread for each row, adapter and row in one key");
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int count = static_cast<int>(M - row0 < kChunk ? M - row0 : kChunk);
   int id = INT_MAX;
   if (t < count) {
@@ -131,45 +134,55 @@ __device__ void group_rows(Groups& g, const int* ids, int64_t row0, int64_t M, i
     if (v >= 0 && v < n) id = v;
   }
   g.ids[t] = id;
-  // Rows already in order (neighbours of one request, one adapter for all): nothing to sort, and
-  // a run's first row is the last one before t that differs from its predecessor.
+  // Adapter, then row: all keys differ; rows past the last sort behind all others.
+  int key = t >= count ? 0x7fffffff : (id == INT_MAX ? 0x7fffff00 : id << 8) | t;
+  g.keys[t] = key;
   __syncthreads();
-  const bool sorted = __syncthreads_and(t == 0 || t >= count || g.ids[t - 1] <= id);
-  if (sorted) {
-    const unsigned bits = __ballot_sync(0xffffffffu, t < count && (t == 0 || g.ids[t - 1] != id));
-    if ((t & 31) == 0) g.start[t >> 5] = static_cast<int>(bits);
+  // Rows already in order (neighbours of one request, one adapter for all) need no sorting.
+  if (!__syncthreads_and(t == 0 || t >= count || g.keys[t - 1] < key)) {
+    for (int k = 2; k <= kChunk; k <<= 1)
+      for (int j = k >> 1; j > 0; j >>= 1) {   // a bitonic sort, through shuffles below 32
+        int other;
+        if (j < 32) {
+          other = __shfl_xor_sync(0xffffffffu, key, j);
+        } else {
+          __syncthreads();
+          g.keys[t] = key;
+          __syncthreads();
+          other = g.keys[t ^ j];
+        }
+        key = ((t & j) == 0) == ((t & k) == 0) ? min(key, other) : max(key, other);
+      }
     __syncthreads();
-    if (t < count) {
-      int w = t >> 5;
-      unsigned run = static_cast<unsigned>(g.start[w]) & (0xffffffffu >> (31 - (t & 31)));
-      while (run == 0) run = static_cast<unsigned>(g.start[--w]);   // row 0 begins a run
-      g.order[t] = t;
-      g.flag[t] = (t - (w * 32 + 31 - __clz(run))) % kRows == 0;
-    }
-  } else if (t < count) {
-    int less = 0, before = 0;
-#pragma unroll 4
-    for (int j = 0; j < kChunk; j += 4) {   // entries past the last row hold INT_MAX
-      const int4 v = *reinterpret_cast<const int4*>(&g.ids[j]);
-      less += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
-      before += (v.x == id && j < t) + (v.y == id && j + 1 < t) + (v.z == id && j + 2 < t) + (v.w == id && j + 3 < t);
-    }
-    g.order[less + before] = t;
-    g.flag[less + before] = before % kRows == 0;
+    g.keys[t] = key;
+    __syncthreads();
   }
+  // Runs of one adapter, and in them every kRows-th row, begin an item.
+  const bool begins = t < count && (t == 0 || (g.keys[t - 1] >> 8) != (key >> 8));
+  const unsigned run = __ballot_sync(0xffffffffu, begins);
+  if (lane == 0) g.runs[warp] = static_cast<int>(run);
   __syncthreads();
-  if (t < 32) {
-    int items = 0;
-    for (int w = 0; w < kChunk; w += 32) {
-      const bool f = w + t < count && g.flag[w + t] != 0;
-      const unsigned bits = __ballot_sync(0xffffffffu, f);
-      if (f) g.start[items + __popc(bits & ((1u << t) - 1))] = w + t;
-      items += __popc(bits);
-    }
-    if (t == 0) {
-      g.start[items] = count;
-      g.items = items;
-    }
+  bool first = false;
+  if (t < count) {
+    int w = warp;
+    unsigned bits = run & (0xffffffffu >> (31 - lane));
+    while (bits == 0) bits = static_cast<unsigned>(g.runs[--w]);   // row 0 begins a run
+    first = (t - (w * 32 + 31 - __clz(bits))) % kRows == 0;
+    g.order[t] = key & (kChunk - 1);
+  }
+  const unsigned firsts = __ballot_sync(0xffffffffu, first);
+  if (lane == 0) g.firsts[warp] = __popc(firsts);
+  __syncthreads();
+  int before = 0, items = 0;
+#pragma unroll
+  for (int w = 0; w < kChunk / 32; ++w) {
+    if (w < warp) before += g.firsts[w];
+    items += g.firsts[w];
+  }
+  if (first) g.start[before + __popc(firsts & ((1u << lane) - 1))] = t;
+  if (t == 0) {
+    g.start[items] = count;
+    g.items = items;
   }
   __syncthreads();
 }
@@ -848,7 +861,6 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_split_kernel(const SplitPar
 constexpr int kOuterCols = 128;
 constexpr int kOuterRows = 64;        // rows of one stage
 constexpr int kMaxRange = 4096;       // rows of one range
-constexpr int kMaxAdapters = 4096;
 
 struct OuterSide {
   const __nv_bfloat16* v;     // [M][ld]: terms of r each, kT or more

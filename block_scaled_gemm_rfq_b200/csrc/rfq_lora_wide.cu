@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
         tc_fence_after();
         __syncwarp();
         const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc.stage * acc_cols;
-        for (int j = 0; j < p.r; j += 8) {
+        for (int j = __any_sync(0xffffffffu, mine == a) ? 0 : p.r; j < p.r; j += 8) {
           uint32_t v[8];
           tmem_load_32x32b_x8(at + j, v);
           tmem_wait_ld();
@@ -584,8 +584,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
           tc_fence_after();
           __syncwarp();
           const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc.stage * 128 + half * kBoxCols;
+          const bool here = __any_sync(0xffffffffu, mine == a);   // these 32 rows have the adapter
 #pragma unroll
           for (int g = 0; g < kBoxCols / 32; ++g) {
+            if (!here) break;
             uint32_t v[32];
             tmem_load_32x32b_x32(at + 32 * g, v);
             tmem_wait_ld();
@@ -751,9 +753,11 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
   }
   p.kt_per_rank = static_cast<int>(ceil_div(p.kt, p.cluster));
   const uint32_t stage = kBox + shrink_p_bytes(trans, p.r), sums = shrink_sum_bytes(p.r);
-  // As many stages as leave room for two CTAs per SM, at least three.
-  p.stages = static_cast<int>((kSmemLimit / 2 - 2048 - sums) / stage);
-  if (sums + 2048 > kSmemLimit / 2 || p.stages < 3) p.stages = 3;
+  // As many stages as leave room for two CTAs per SM, where there are that many CTAs; else, or where
+  // that would be fewer than three, as many as fit one.
+  const uint32_t room = chunks * p.cluster > num_sms ? kSmemLimit / 2 : kSmemLimit;
+  p.stages = sums + 2048 < room ? static_cast<int>((room - 2048 - sums) / stage) : 0;
+  if (p.stages < 3) p.stages = static_cast<int>((kSmemLimit - 2048 - sums) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * stage + sums;
   return trans ? launch(rfq_lora_shrink_wide_kernel<true>, maps, p, chunks * p.cluster, kShrinkThreads, smem, p.cluster, stream)
