@@ -200,8 +200,8 @@ bool lora_shape_ok(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n) {
 
 bool out_type_ok(rfq_out_t t) { return t == RFQ_OUT_F32 || t == RFQ_OUT_BF16; }
 
-// A list of gradients: every entry a bf16 or fp32 array on its own alignment, 2^43 elements in all
-// (the kernels number pieces of 8192 elements with 30 bits).
+// A list of gradients: every entry a bf16 or fp32 array on its own alignment, 2^42 elements in all
+// (the kernels number pieces of 4096 fp32 or 8192 bf16 elements with 31 bits).
 rfq_status_t check_list(const void* const* in, const void* const* out, const int64_t* numels, const rfq_out_t* types,
                         int64_t count) {
   if (count < 0 || count > (int64_t(1) << 24) || (count > 0 && (!in || !numels || !types))) return RFQ_ERR_INVALID_ARG;
@@ -209,7 +209,7 @@ rfq_status_t check_list(const void* const* in, const void* const* out, const int
   int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (numels[i] < 0 || !out_type_ok(types[i])) return RFQ_ERR_INVALID_ARG;
-    if (numels[i] > kMost || (total += (numels[i] + 8191) / 8192 * 8192) > kMost) return RFQ_ERR_UNSUPPORTED_SHAPE;
+    if (numels[i] > kMost || (total += (numels[i] + 4095) / 4096 * 4096) > kMost) return RFQ_ERR_UNSUPPORTED_SHAPE;
     if (numels[i] == 0) continue;
     const uintptr_t size = types[i] == RFQ_OUT_F32 ? 4 : 2;
     if (!in[i] || (out && !out[i])) return RFQ_ERR_INVALID_ARG;

@@ -6,12 +6,12 @@
 // Bound by memory: the list is read once for the norm and once more, written once, for the
 // scaling (which cannot start before the norm is known).  The tensors' addresses travel in
 // the kernels' parameters (a table of up to kTable tensors a launch), so nothing is copied
-// to the device and a captured graph keeps them.  Every CTA walks over pieces of kPiece
-// elements, all tensors' pieces numbered through, and leaves one partial sum; the scaling
+// to the device and a captured graph keeps them.  Every CTA walks over pieces of 16 KiB,
+// all tensors' pieces numbered through, and leaves one partial sum; the scaling
 // kernel's CTAs each add the partial sums in the same order.  The scaling walks the pieces
 // backwards: the end of the list, read last, is what L2 still holds.
 //
-// Sums: the squares of a thread's elements of one piece (32) in fp32, these sums in fp64.
+// Sums: the squares of a thread's elements of one piece (32 of bf16, 16 of fp32) in fp32, these sums in fp64.
 // Where the fp32 sum leaves [1e-30, 1e37] (values near 1e19 or below 1e-15) the piece is
 // added again in fp64, so the norm neither overflows nor underflows before its own value does.
 #include <cuda_bf16.h>
@@ -26,11 +26,11 @@ namespace rfq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 8192;                 // elements: four 8-element vectors a thread
-constexpr int kVecs = kPiece / 8 / kThreads;
+constexpr int kVecs = 4;                     // 16-byte vectors of a thread in one piece
+constexpr int kPieceBytes = kThreads * kVecs * 16;   // 16 KiB
 constexpr int kTable = 512;                  // tensors of one launch (14 KiB of parameters)
 constexpr int kPlanSms = 148;
-constexpr int kGrid = 4 * kPlanSms;
+constexpr int kGrid = 6 * kPlanSms;
 
 struct Table {
   const void* in[kTable];
@@ -40,62 +40,51 @@ struct Table {
   int count;
 };
 
-struct Piece {
-  int64_t at;                  // first element
-  int n;                       // elements
-  bool f32;
-};
-
 // Moves `t` to the tensor that holds piece `k` (pieces are visited in one direction).
-__device__ __forceinline__ Piece find(const Table& tab, int k, int& t) {
+__device__ __forceinline__ void find(const Table& tab, int k, int& t) {
   while (t + 1 < tab.count && k >= tab.first[t + 1]) ++t;
   while (t > 0 && k < tab.first[t]) --t;
-  Piece p;
-  const int64_t numel = tab.numel[t];
-  p.f32 = numel < 0;
-  p.at = static_cast<int64_t>(k - tab.first[t]) * kPiece;
-  const int64_t left = (p.f32 ? -numel : numel) - p.at;
-  p.n = static_cast<int>(left < kPiece ? left : kPiece);
-  return p;
 }
 
-__device__ __forceinline__ float element(const void* base, int64_t i, bool f32) {
-  return f32 ? static_cast<const float*>(base)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-}
-
-// Eight elements as floats; `base` + i on a 16-byte boundary.
-__device__ __forceinline__ void load8(const void* base, int64_t i, bool f32, float (&f)[8]) {
-  if (f32) {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + i);
+// One element type: a 16-byte vector as floats, and single elements.
+template <bool kF32>
+struct Type {
+  static constexpr int kPer = kF32 ? 4 : 8;                  // elements of a vector
+  static constexpr int kPiece = kPieceBytes / (kF32 ? 4 : 2);
+  __device__ static __forceinline__ void open(const uint4& u, float (&f)[kPer]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      f[2 * e] = __uint_as_float(w[e] << 16);
-      f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      if constexpr (kF32) {
+        f[e] = __uint_as_float(w[e]);
+      } else {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
     }
   }
-}
-
-__device__ __forceinline__ void store8(void* base, int64_t i, bool f32, const float (&f)[8]) {
-  if (f32) {
-    float* o = static_cast<float*>(base) + i;
-    *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(o + 4) = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
+  __device__ static __forceinline__ uint4 close(const float (&f)[kPer]) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-      w[e] = *reinterpret_cast<uint32_t*>(&b);
+      if constexpr (kF32) {
+        w[e] = __float_as_uint(f[e]);
+      } else {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&b);
+      }
     }
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
+  __device__ static __forceinline__ float get(const void* p, int i) {
+    if constexpr (kF32) return static_cast<const float*>(p)[i];
+    else return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  }
+  __device__ static __forceinline__ void put(void* p, int i, float x) {
+    if constexpr (kF32) static_cast<float*>(p)[i] = x;
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+  }
+};
 
 // Sum of the threads' values in a fixed order; the result in every thread.
 __device__ double block_sum(double v) {
@@ -110,6 +99,90 @@ __device__ double block_sum(double v) {
   return s;
 }
 
+// The squares of this thread's share of n elements at `in`.  Vectors as far as the piece is whole and
+// on a 16-byte boundary (pieces are multiples of 16 bytes from the tensor's start), else one by one.
+template <bool kF32>
+__device__ __forceinline__ double sum_piece(const uint8_t* in, int n) {
+  using T = Type<kF32>;
+  float s = 0.f, top = 0.f;
+  auto add = [&](float x) {
+    s = fmaf(x, x, s);
+    top = fmaxf(top, fabsf(x));
+  };
+  const uint4* v = reinterpret_cast<const uint4*>(in);
+  const int vecs = (reinterpret_cast<uintptr_t>(in) & 15u) == 0 ? n / T::kPer : 0;
+  if (vecs == kVecs * kThreads) {
+    uint4 u[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) u[i] = v[i * kThreads + threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float f[T::kPer];
+      T::open(u[i], f);
+#pragma unroll
+      for (int e = 0; e < T::kPer; ++e) add(f[e]);
+    }
+  } else {
+    for (int i = threadIdx.x; i < vecs; i += kThreads) {
+      float f[T::kPer];
+      T::open(v[i], f);
+#pragma unroll
+      for (int e = 0; e < T::kPer; ++e) add(f[e]);
+    }
+    for (int i = vecs * T::kPer + threadIdx.x; i < n; i += kThreads) add(T::get(in, i));
+  }
+  if (s >= 1e-30f && s <= 1e37f) return s;
+  if (s == s && top == 0.f) return 0.0;
+  // Out of fp32's comfortable range (or NaN): the same elements once more.
+  double d = 0.0;
+  for (int i = threadIdx.x; i < vecs; i += kThreads) {
+    float f[T::kPer];
+    T::open(v[i], f);
+    for (int e = 0; e < T::kPer; ++e) d += static_cast<double>(f[e]) * f[e];
+  }
+  for (int i = vecs * T::kPer + threadIdx.x; i < n; i += kThreads) {
+    const double x = T::get(in, i);
+    d += x * x;
+  }
+  return d;
+}
+
+template <bool kF32>
+__device__ __forceinline__ void scale_piece(const uint8_t* in, uint8_t* out, int n, float c) {
+  using T = Type<kF32>;
+  const uint4* v = reinterpret_cast<const uint4*>(in);
+  uint4* w = reinterpret_cast<uint4*>(out);
+  const int vecs = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 ? n / T::kPer : 0;
+  auto scaled = [&](const uint4& u) {
+    float f[T::kPer];
+    T::open(u, f);
+#pragma unroll
+    for (int e = 0; e < T::kPer; ++e) f[e] *= c;
+    return T::close(f);
+  };
+  if (vecs == kVecs * kThreads) {
+    uint4 u[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) u[i] = v[i * kThreads + threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) w[i * kThreads + threadIdx.x] = scaled(u[i]);
+  } else {
+    for (int i = threadIdx.x; i < vecs; i += kThreads) w[i] = scaled(v[i]);
+    for (int i = vecs * T::kPer + threadIdx.x; i < n; i += kThreads) T::put(out, i, T::get(in, i) * c);
+  }
+}
+
+// Calls f(byte offset, elements, is fp32) for piece k of the list, which lies in tensor t.
+template <class F>
+__device__ __forceinline__ void with_piece(const Table& tab, int k, int t, F f) {
+  const int64_t numel = tab.numel[t];
+  const bool f32 = numel < 0;
+  const int per = f32 ? Type<true>::kPiece : Type<false>::kPiece;
+  const int64_t at = static_cast<int64_t>(k - tab.first[t]);
+  const int64_t left = (f32 ? -numel : numel) - at * per;
+  f(at * kPieceBytes, static_cast<int>(left < per ? left : per), f32);
+}
+
 __global__ void __launch_bounds__(kThreads) rfq_clip_norm_kernel(const __grid_constant__ Table tab, double* partial) {
   griddep_launch_dependents();
   griddep_wait();
@@ -117,45 +190,11 @@ __global__ void __launch_bounds__(kThreads) rfq_clip_norm_kernel(const __grid_co
   double sum = 0.0;
   int t = 0;
   for (int k = blockIdx.x; k < pieces; k += gridDim.x) {
-    const Piece p = find(tab, k, t);
-    const void* in = tab.in[t];
-    float s = 0.f, top = 0.f;
-    // Vectors of eight as far as they go (p.at is a multiple of kPiece), the rest one by one.
-    const int whole = (reinterpret_cast<uintptr_t>(in) & 15u) == 0 ? p.n & ~7 : 0;
-    float f[kVecs][8];
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int i = (v * kThreads + threadIdx.x) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[v][e] = 0.f;
-      if (i < whole) load8(in, p.at + i, p.f32, f[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s = fmaf(f[v][e], f[v][e], s);
-        top = fmaxf(top, fabsf(f[v][e]));
-      }
-    for (int i = whole + threadIdx.x; i < p.n; i += kThreads) {
-      const float x = element(in, p.at + i, p.f32);
-      s = fmaf(x, x, s);
-      top = fmaxf(top, fabsf(x));
-    }
-    if (s >= 1e-30f && s <= 1e37f) {
-      sum += s;
-    } else if (s != s || top > 0.f) {
-      // Out of fp32's comfortable range (or NaN): this thread's elements once more.
-      for (int i = threadIdx.x * 8; i < whole; i += kThreads * 8)
-        for (int e = 0; e < 8; ++e) {
-          const double x = element(in, p.at + i + e, p.f32);
-          sum += x * x;
-        }
-      for (int i = whole + threadIdx.x; i < p.n; i += kThreads) {
-        const double x = element(in, p.at + i, p.f32);
-        sum += x * x;
-      }
-    }
+    find(tab, k, t);
+    with_piece(tab, k, t, [&](int64_t at, int n, bool f32) {
+      const uint8_t* in = static_cast<const uint8_t*>(tab.in[t]) + at;
+      sum += f32 ? sum_piece<true>(in, n) : sum_piece<false>(in, n);
+    });
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -185,31 +224,14 @@ __global__ void __launch_bounds__(kThreads) rfq_clip_scale_kernel(const __grid_c
   const int pieces = tab.first[tab.count];
   int t = tab.count - 1;
   for (int k = pieces - 1 - static_cast<int>(blockIdx.x); k >= 0; k -= gridDim.x) {
-    const Piece p = find(tab, k, t);
-    const void* in = tab.in[t];
-    void* out = tab.out[t];
-    if (c == 1.f && in == out) continue;   // multiplying by one changes nothing
-    const int whole = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 ? p.n & ~7 : 0;
-    float f[kVecs][8];
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int i = (v * kThreads + threadIdx.x) * 8;
-      if (i < whole) load8(in, p.at + i, p.f32, f[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int i = (v * kThreads + threadIdx.x) * 8;
-      if (i < whole) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[v][e] *= c;
-        store8(out, p.at + i, p.f32, f[v]);
-      }
-    }
-    for (int i = whole + threadIdx.x; i < p.n; i += kThreads) {
-      const float x = element(in, p.at + i, p.f32) * c;
-      if (p.f32) static_cast<float*>(out)[p.at + i] = x;
-      else static_cast<__nv_bfloat16*>(out)[p.at + i] = __float2bfloat16_rn(x);
-    }
+    find(tab, k, t);
+    if (c == 1.f && tab.in[t] == tab.out[t]) continue;   // multiplying by one changes nothing
+    with_piece(tab, k, t, [&](int64_t at, int n, bool f32) {
+      const uint8_t* in = static_cast<const uint8_t*>(tab.in[t]) + at;
+      uint8_t* out = static_cast<uint8_t*>(tab.out[t]) + at;
+      if (f32) scale_piece<true>(in, out, n, c);
+      else scale_piece<false>(in, out, n, c);
+    });
   }
 }
 
@@ -240,7 +262,8 @@ int64_t fill(Table& tab, const void* const* in, void* const* out, const int64_t*
     tab.in[t] = in[i];
     tab.out[t] = out != nullptr ? out[i] : const_cast<void*>(in[i]);
     tab.numel[t] = types[i] == RFQ_OUT_F32 ? -numels[i] : numels[i];
-    pieces += (numels[i] + kPiece - 1) / kPiece;
+    const int64_t per = types[i] == RFQ_OUT_F32 ? Type<true>::kPiece : Type<false>::kPiece;
+    pieces += (numels[i] + per - 1) / per;
     tab.first[t + 1] = static_cast<int>(pieces);
   }
   return i;

@@ -725,93 +725,118 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_direct_kernel(const 
     const int64_t row[2] = {row0 + g.order[first + (has[0] ? line : 0)], row0 + g.order[first + (has[1] ? line + 8 : 0)]};
     // Column of this lane's fragment row in tile i: 8 (g / 2) + 2 i + (g & 1).
     const __nv_bfloat16* qa = with ? p.q + (static_cast<int64_t>(a) * p.C + 8 * (line >> 1) + (line & 1)) * p.r : p.q;
-    for (int64_t c = begin + 32 * warp; c < end; c += 8 * 32) {
+    // The loads of a block (32 columns x 32 of the rank) are under way while the one before is
+    // multiplied; the base comes with the first block of its columns.
+    const int blocks = (p.r + 31) / 32;
+    constexpr int kRaw = kF32 ? 2 : 1;
+    struct Block {
+      uint2 w[2][4];
+      uint4 b[2][kRaw];
+    };
+    const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+    auto load = [&](int64_t c, int kb, Block& d) {
       const int64_t col = c + 8 * quad;
-      float f[2][8];
+      if (kb == 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+          const bool ok = p.base != nullptr && has[h] && col < p.C;
+          const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.base) + (row[h] * p.C + col) * (kF32 ? 4 : 2));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[h][e] = 0.f;
-        if (p.base != nullptr && has[h] && col < p.C) {
-          if constexpr (kF32) {
-            const float* b = static_cast<const float*>(p.base) + row[h] * p.C + col;
-            const float4 u = *reinterpret_cast<const float4*>(b), w = *reinterpret_cast<const float4*>(b + 4);
-            f[h][0] = u.x; f[h][1] = u.y; f[h][2] = u.z; f[h][3] = u.w;
-            f[h][4] = w.x; f[h][5] = w.y; f[h][6] = w.z; f[h][7] = w.w;
-          } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.base) + row[h] * p.C + col);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[h][2 * e] = __uint_as_float(w[e] << 16);
-              f[h][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-            }
-          }
+          for (int e = 0; e < kRaw; ++e) d.b[h][e] = ok ? b[e] : zero4;
         }
       }
-      if (with) {
-        float acc[4][4];
-        bool ok[4];
-        const __nv_bfloat16* q[4];
+      if (!with) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {
+        const bool ok = c + 8 * (line >> 1) + 2 * i + (line & 1) < p.C;
+        const __nv_bfloat16* q = qa + (c + 2 * i) * p.r + 32 * kb;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int k = 32 * kb + 16 * s;   // sixteen of the rank, or its last eight
+          const bool whole = k + 16 <= p.r;
+          d.w[s][i] = ok && whole ? *reinterpret_cast<const uint2*>(q + 16 * s + 4 * quad) : make_uint2(0u, 0u);
+          if (ok && !whole && k < p.r) d.w[s][i].x = *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * quad);
+        }
+      }
+    };
+    int64_t c = begin + 32 * warp;
+    int kb = 0;
+    Block next;
+    if (c < end) load(c, 0, next);
+    float acc[4][4];
+    uint4 held[2][kRaw];
+    while (c < end) {
+      const Block now = next;
+      int64_t c2 = c;
+      int kb2 = kb + 1;
+      if (kb2 == blocks) {
+        kb2 = 0;
+        c2 += 8 * 32;
+      }
+      if (c2 < end) load(c2, kb2, next);
+      if (kb == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-          ok[i] = c + 8 * (line >> 1) + 2 * i + (line & 1) < p.C;
-          q[i] = qa + (c + 2 * i) * p.r;
-        }
-        int k = 0;
-#pragma unroll 2
-        for (; k + 16 <= p.r; k += 16) {
-          uint2 w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = ok[i] ? *reinterpret_cast<const uint2*>(q[i] + k + 4 * quad) : make_uint2(0u, 0u);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
-            const uint2 sa = *reinterpret_cast<const uint2*>(&sm[e][line][k + 4 * quad]);
-            const uint2 sb = *reinterpret_cast<const uint2*>(&sm[e][line + 8][k + 4 * quad]);
-            const uint32_t fa[4] = {sa.x, sb.x, sa.y, sb.y};
+          for (int e = 0; e < kRaw; ++e) held[h][e] = now.b[h][e];
+      }
+      if (with) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma16816(acc[i], fa, w[i].x, w[i].y);
+        for (int s = 0; s < 2; ++s) {
+          const int k = 32 * kb + 16 * s;
+          if (k + 16 <= p.r) {
+#pragma unroll
+            for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
+              const uint2 sa = *reinterpret_cast<const uint2*>(&sm[e][line][k + 4 * quad]);
+              const uint2 sb = *reinterpret_cast<const uint2*>(&sm[e][line + 8][k + 4 * quad]);
+              const uint32_t fa[4] = {sa.x, sb.x, sa.y, sb.y};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma16816(acc[i], fa, now.w[s][i].x, now.w[s][i].y);
+            }
+          } else if (k < p.r) {
+#pragma unroll
+            for (int e = kT - 1; e >= 0; --e) {
+              const uint32_t fa[2] = {*reinterpret_cast<const uint32_t*>(&sm[e][line][k + 2 * quad]),
+                                      *reinterpret_cast<const uint32_t*>(&sm[e][line + 8][k + 2 * quad])};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma1688(acc[i], fa, now.w[s][i].x);
+            }
           }
-        }
-        if (k < p.r) {   // the last eight of the rank
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = ok[i] ? *reinterpret_cast<const uint32_t*>(q[i] + k + 2 * quad) : 0u;
-#pragma unroll
-          for (int e = kT - 1; e >= 0; --e) {
-            const uint32_t fa[2] = {*reinterpret_cast<const uint32_t*>(&sm[e][line][k + 2 * quad]),
-                                    *reinterpret_cast<const uint32_t*>(&sm[e][line + 8][k + 2 * quad])};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma1688(acc[i], fa, w[i]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[0][2 * i] += acc[i][0];
-          f[0][2 * i + 1] += acc[i][1];
-          f[1][2 * i] += acc[i][2];
-          f[1][2 * i + 1] += acc[i][3];
         }
       }
+      if (kb2 == 0) {   // the columns' last block
+        const int64_t col = c + 8 * quad;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (has[h] && col < p.C) {
+        for (int h = 0; h < 2; ++h) {
+          if (!has[h] || col >= p.C) continue;
+          uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (row[h] * p.C + col) * (kF32 ? 4 : 2));
           if constexpr (kF32) {
-            float* o = static_cast<float*>(p.out) + row[h] * p.C + col;
-            *reinterpret_cast<float4*>(o) = make_float4(f[h][0], f[h][1], f[h][2], f[h][3]);
-            *reinterpret_cast<float4*>(o + 4) = make_float4(f[h][4], f[h][5], f[h][6], f[h][7]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 u = held[h][e];
+              o[e] = make_uint4(__float_as_uint(__uint_as_float(u.x) + acc[2 * e][2 * h]), __float_as_uint(__uint_as_float(u.y) + acc[2 * e][2 * h + 1]),
+                                __float_as_uint(__uint_as_float(u.z) + acc[2 * e + 1][2 * h]),
+                                __float_as_uint(__uint_as_float(u.w) + acc[2 * e + 1][2 * h + 1]));
+            }
           } else {
+            const uint32_t u[4] = {held[h][0].x, held[h][0].y, held[h][0].z, held[h][0].w};
             uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(f[h][2 * e], f[h][2 * e + 1]);
-              w[e] = *reinterpret_cast<const uint32_t*>(&b);
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(u[i] << 16) + acc[i][2 * h],
+                                                             __uint_as_float(u[i] & 0xffff0000u) + acc[i][2 * h + 1]);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row[h] * p.C + col) = make_uint4(w[0], w[1], w[2], w[3]);
+            *o = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+      }
+      c = c2;
+      kb = kb2;
     }
     __syncthreads();   // the next group's s' goes where this one's was
   }
@@ -1172,11 +1197,11 @@ int64_t chunk_ctas(int64_t M, int64_t n, int64_t most) {
   return z;
 }
 
-// Splits of the shrink product's contraction: four CTAs per SM over all, 256 elements each at least.
+// Splits of the shrink product's contraction: one wave of three CTAs per SM, 256 elements each at least.
 int shrink_splits(int64_t M, int64_t C, int64_t n, int64_t* c_split, int* zs) {
   const int64_t chunks = ceil_div(M, kChunk), z = chunk_ctas(M, n, 2 * kPlanSms);
   const int64_t most = ceil_div(C, 256);
-  int64_t s = 4 * kPlanSms / (chunks * z);
+  int64_t s = 3 * kPlanSms / (chunks * z);
   if (s > most) s = most;
   if (s > 32) s = 32;
   if (s < 1) s = 1;
