@@ -76,13 +76,25 @@ struct Maps {
   CUtensorMap a, b;
 };
 
-struct Params {
-  int M, N;               // rows and columns of the product
-  int num_kt;             // k-tiles of the whole contraction
-  int kt_per_split;       // k-tiles of one split
+// How a product's tiles are shared out.  The first `whole` tiles go round the units (CTAs or
+// pairs) one by one.  What is left over when these rounds are full (kHidden alone) is cut along the
+// contraction into slices, each leaving the fp32 sums of its tile in a slot of its own; so a product
+// of few tiles, or of a few more than a round, keeps the SMs busy.  All tiles of one slice come
+// before the next slice: the units at work then read the same part of the contraction, and share it
+// through L2 (cut into equal runs of k-tiles instead, with no such order, the units read dz and the
+// head several times from memory: 657 against 561 us for 1000 x 2048 x 50001).
+struct Share {
   int num_mb, num_nb;     // tiles along M (of kBM * kPair rows) and N
   int group;              // row tiles that pass over the columns together
-  int num_tiles;          // num_mb * num_nb * splits
+  int tiles, whole;
+  int units;
+  int slices, slice_kt;   // of the rest: k-tiles of one slice
+};
+
+struct Params {
+  int M, N;               // rows and columns of the product
+  int num_kt;             // k-tiles of the contraction
+  Share share;
   // kLogits, kGrad
   const int64_t* labels;  // [M]
   int64_t ignore;
@@ -95,10 +107,11 @@ struct Params {
   const float* gmax;      // largest finite |dloss|
   __nv_bfloat16* dz;      // [M][ld_dz]
   int64_t ld_dz;
-  // kHidden: fp32 sums [split][M][N], or (out != nullptr) bf16 straight away
-  float* acc;
-  int accumulate;
-  // kHidden (one piece, one split) and kHead
+  // kHidden: whole tiles to bf16 at once (out != nullptr: one piece) or into fp32 sums; the rest to slots
+  float* acc;             // [M][N]
+  float* slots;           // [tiles - whole][slices][rows of a tile][kBN]
+  int accumulate;         // not the first piece
+  // kHidden and kHead
   __nv_bfloat16* out;     // [M][N]
 };
 
@@ -131,26 +144,41 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-struct Tile {
-  int split, mb, nb, kt0, kt1;
-};
-// Tiles run over splits, then groups of `group` row tiles, then column tiles, row tile
-// fastest: the CTAs at work share few column tiles of B (the head's rows, which are far
+// Tile number -> row and column tile.  Tiles run over groups of `group` row tiles, then column tiles,
+// row tile fastest: the CTAs at work share few column tiles of B (the head's rows, which are far
 // larger than L2) and one group of rows of A, which L2 holds.
-__device__ __forceinline__ Tile tile_at(const Params& p, int tile) {
-  Tile t;
-  const int per_split = p.num_mb * p.num_nb;
-  t.split = tile / per_split;
-  const int r = tile - t.split * per_split;
-  const int in_group = p.group * p.num_nb;
-  const int g = r / in_group;
-  const int rr = r - g * in_group;
-  const int rows = min(p.group, p.num_mb - g * p.group);
-  t.nb = rr / rows;
-  t.mb = g * p.group + (rr - t.nb * rows);
-  t.kt0 = t.split * p.kt_per_split;
-  t.kt1 = min(p.num_kt, t.kt0 + p.kt_per_split);
-  return t;
+__host__ __device__ __forceinline__ void place(const Share& s, int tile, int* mb, int* nb) {
+  const int in_group = s.group * s.num_nb;
+  const int g = tile / in_group;
+  const int rr = tile - g * in_group;
+  const int left = s.num_mb - g * s.group;
+  const int rows = s.group < left ? s.group : left;
+  *nb = rr / rows;
+  *mb = g * s.group + (rr - *nb * rows);
+}
+
+struct Work {
+  int mb, nb, kt0, kt1;
+  int slot;               // -1: a whole tile
+};
+// Item `item` of a product: the whole tiles, then the slices.  False past the last, and where a slice is
+// empty (the last piece of a vocabulary may be shorter than the one the slices were cut for).
+__device__ __forceinline__ int num_items(const Share& s) { return s.whole + (s.tiles - s.whole) * s.slices; }
+__device__ __forceinline__ bool work_at(const Params& p, int item, Work& w) {
+  if (item < p.share.whole) {
+    place(p.share, item, &w.mb, &w.nb);
+    w.kt0 = 0;
+    w.kt1 = p.num_kt;
+    w.slot = -1;
+    return true;
+  }
+  const int rest = p.share.tiles - p.share.whole;
+  const int slice = (item - p.share.whole) / rest, t = (item - p.share.whole) - slice * rest;
+  place(p.share, p.share.whole + t, &w.mb, &w.nb);
+  w.kt0 = slice * p.share.slice_kt;
+  w.kt1 = min(p.num_kt, w.kt0 + p.share.slice_kt);
+  w.slot = t * p.share.slices + slice;
+  return w.kt0 < w.kt1;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -178,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
   const uint32_t rank = kPair == 2 ? cluster_cta_rank() : 0u;
   const bool leader = rank == 0;
   const int unit = static_cast<int>(blockIdx.x) / kPair;
-  const int num_units = static_cast<int>(gridDim.x) / kPair;
+  const int items = num_items(p.share);
+  Work t;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -214,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
     if (lane == 0) {
       // ------------------------------------------------------------ TMA producer
       uint32_t stage = 0, phase = 0, filled = 0, last_parity = 0;
-      for (int tile = unit; tile < p.num_tiles; tile += num_units) {
-        const Tile t = tile_at(p, tile);
+      for (int item = unit; item < items; item += p.share.units) {
+        if (!work_at(p, item, t)) continue;
         const int row_a = (t.mb * kPair + static_cast<int>(rank)) * kBM;
         const int row_b = t.nb * kBN + static_cast<int>(rank) * (kBN / kPair);
         for (int kt = t.kt0; kt < t.kt1; ++kt) {
@@ -265,8 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       constexpr uint32_t idesc = mma_idesc<kPair, kAMn, kBMn>();
       uint32_t stage = 0, phase = 0, buf = 0, acc_phase = 0;
       bool ok = true;
-      for (int tile = unit; tile < p.num_tiles && ok; tile += num_units) {
-        const Tile t = tile_at(p, tile);
+      for (int item = unit; item < items && ok; item += p.share.units) {
+        if (!work_at(p, item, t)) continue;
         const int part = kMode == kLogits ? kLogitsPart : t.kt1 - t.kt0;
         for (int kp = t.kt0; kp < t.kt1 && ok; kp += part) {
           if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, &g_ce_error, kErrWaitAccEmpty)) {
@@ -317,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
     uint32_t buf = 0, acc_phase = 0;
     float gmax = 0.f;
     if constexpr (kMode != kLogits) gmax = *p.gmax;
-    for (int tile = unit; tile < p.num_tiles; tile += num_units) {
-      const Tile t = tile_at(p, tile);
+    for (int item = unit; item < items; item += p.share.units) {
+      if (!work_at(p, item, t)) continue;
       const int row = (t.mb * kPair + static_cast<int>(rank)) * kBM + quad * 32 + lane;
       const int col0 = t.nb * kBN + half * 128;
       uint32_t v[4][32];
@@ -414,8 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
                 make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
         }
       } else if constexpr (kMode == kHidden) {
-        if (p.out == nullptr) {
-          float* dst = p.acc + (static_cast<int64_t>(t.split) * p.M + row) * p.N + col0;
+        if (p.out == nullptr || t.slot >= 0) {
+          float* dst = t.slot < 0 ? p.acc + static_cast<int64_t>(row) * p.N + col0
+                                  : p.slots + (static_cast<int64_t>(t.slot) * (kBM * kPair) + rank * kBM + quad * 32 + lane) * kBN + half * 128;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             if (col0 + 4 * i < p.N) {
@@ -434,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
         }
       }
       if constexpr (kMode == kHidden || kMode == kHead) {
-        if (kMode == kHead || p.out != nullptr) {
+        if (kMode == kHead || (p.out != nullptr && t.slot < 0)) {
           __nv_bfloat16* dst = p.out + static_cast<int64_t>(row) * p.N + col0;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -525,23 +555,39 @@ __global__ void __launch_bounds__(1024) rfq_ce_gmax_kernel(const float* dloss, c
   }
 }
 
-// dh = gmax * sum over the splits of the fp32 sums, in order.
-__global__ void __launch_bounds__(256) rfq_ce_hidden_kernel(const float* acc, int splits, int64_t n4, const float* gmax,
-                                                            __nv_bfloat16* dh) {
+// dh of the tiles that the product left in fp32: gmax * the sum of a tile's slots, in order, or (whole
+// tiles of a product over several pieces) gmax * its sums.  One block per 32 rows of a tile.
+__global__ void __launch_bounds__(256) rfq_ce_hidden_kernel(const Share share, int tile0, int tile_rows, const float* acc, const float* slots,
+                                                            const float* gmax, int M, int N, __nv_bfloat16* dh) {
   griddep_launch_dependents();
   griddep_wait();
+  const int blocks = tile_rows / 32;
+  const int tile = tile0 + static_cast<int>(blockIdx.x) / blocks;
+  const int r0 = static_cast<int>(blockIdx.x) % blocks * 32;
+  int mb, nb;
+  place(share, tile, &mb, &nb);
+  const int rest = tile - share.whole;
   const float g = *gmax;
-  const float4* src = reinterpret_cast<const float4*>(acc);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n4; i += static_cast<int64_t>(gridDim.x) * 256) {
-    float4 f = src[i];
-    for (int s = 1; s < splits; ++s) {
-      const float4 o = src[s * n4 + i];
-      f.x += o.x;
-      f.y += o.y;
-      f.z += o.z;
-      f.w += o.w;
+  const int col = nb * kBN + (threadIdx.x & 63) * 4;
+  if (col >= N) return;
+  for (int r = r0 + (threadIdx.x >> 6); r < r0 + 32; r += 4) {
+    const int row = mb * tile_rows + r;
+    if (row >= M) break;
+    float4 f;
+    if (rest < 0) {
+      f = *reinterpret_cast<const float4*>(acc + static_cast<int64_t>(row) * N + col);
+    } else {
+      const float* src = slots + (static_cast<int64_t>(rest) * share.slices * tile_rows + r) * kBN + (threadIdx.x & 63) * 4;
+      f = *reinterpret_cast<const float4*>(src);
+      for (int s = 1; s < share.slices; ++s) {
+        const float4 o = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(s) * tile_rows * kBN);
+        f.x += o.x;
+        f.y += o.y;
+        f.z += o.z;
+        f.w += o.w;
+      }
     }
-    reinterpret_cast<uint2*>(dh)[i] = make_uint2(pack_bf16(f.x * g, f.y * g), pack_bf16(f.z * g, f.w * g));
+    *reinterpret_cast<uint2*>(dh + static_cast<int64_t>(row) * N + col) = make_uint2(pack_bf16(f.x * g, f.y * g), pack_bf16(f.z * g, f.w * g));
   }
 }
 
@@ -567,28 +613,61 @@ cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, size_t smem, int cl
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int kPlanSms = 148;                      // work is shared out for a B200, whatever runs it
+
+// Pairs of CTAs above 128 rows.
+int pair_of(int64_t M) { return M > kBM ? 2 : 1; }
+
+Share share_out(int64_t M, int64_t N, int64_t K, bool cut_rest) {
+  const int pair = pair_of(M);
+  Share s = {};
+  s.num_mb = static_cast<int>(ceil_div(M, kBM * pair));
+  s.num_nb = static_cast<int>(ceil_div(N, kBN));
+  s.group = 16;
+  s.tiles = s.whole = s.num_mb * s.num_nb;
+  s.units = kPlanSms / pair;
+  s.slices = 1;
+  s.slice_kt = static_cast<int>(ceil_div(K, kBK));
+  if (cut_rest && s.tiles % s.units != 0) {
+    // The number of slices that leaves the fewest k-tiles to the unit with the most, each slice
+    // charged 4 for its epilogue.
+    s.whole = s.tiles / s.units * s.units;
+    const int64_t rest = s.tiles - s.whole, kt = s.slice_kt;
+    int64_t best = INT64_MAX;
+    for (int n = 1; n <= 32 && n <= kt; ++n) {
+      const int64_t per = ceil_div(kt, n);
+      if (ceil_div(kt, per) != n) continue;
+      const int64_t cost = ceil_div(rest * n, s.units) * (per + 4);
+      if (cost < best) {
+        best = cost;
+        s.slices = n;
+        s.slice_kt = static_cast<int>(per);
+      }
+    }
+    if (s.slices == 1) s.whole = s.tiles;
+  }
+  return s;
+}
+
 template <int kPair, int kMode>
-cudaError_t launch_mode(const Maps& maps, Params p, int splits, int num_sms, cudaStream_t stream) {
+cudaError_t launch_mode(const Maps& maps, const Params& p, cudaStream_t stream) {
   using L = Layout<kPair>;
   auto kernel = rfq_ce_kernel<kPair, kMode>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  p.num_mb = static_cast<int>(ceil_div(p.M, kBM * kPair));
-  p.num_nb = static_cast<int>(ceil_div(p.N, kBN));
-  p.group = 16;
-  p.num_tiles = p.num_mb * p.num_nb * splits;
-  int units = num_sms / kPair;
-  if (units > p.num_tiles) units = p.num_tiles;
+  int units = p.share.units;
+  if (units > p.share.whole + (p.share.tiles - p.share.whole) * p.share.slices)
+    units = p.share.whole + (p.share.tiles - p.share.whole) * p.share.slices;
   return launch_pdl(kernel, dim3(units * kPair), dim3(kThreads), L::kSmem, kPair, stream, maps, p);
 }
 
 // A [M] x B [N] product over K; a_ld / b_ld: elements between the rows of the matrix in memory.
 template <int kMode>
 cudaError_t product(EncodeTiledFn encode, const void* a, int64_t a_ld, const void* b, int64_t b_ld, int64_t M, int64_t N,
-                    int64_t K, int splits, Params p, int num_sms, cudaStream_t stream) {
+                    int64_t K, const Share& share, Params p, cudaStream_t stream) {
   constexpr bool kAMn = kMode == kHead;
   constexpr bool kBMn = kMode == kHidden || kMode == kHead;
-  const bool pair = M > kBM;
+  const bool pair = pair_of(M) == 2;
   Maps maps;
   const bool ok = (kAMn ? encode_bf16_map(encode, &maps.a, a, K, M, a_ld, kBK) : encode_bf16_map(encode, &maps.a, a, M, K, a_ld, kBM)) &&
                   (kBMn ? encode_bf16_map(encode, &maps.b, b, K, N, b_ld, kBK)
@@ -597,25 +676,22 @@ cudaError_t product(EncodeTiledFn encode, const void* a, int64_t a_ld, const voi
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.num_kt = static_cast<int>(ceil_div(K, kBK));
-  p.kt_per_split = static_cast<int>(ceil_div(p.num_kt, splits));
-  splits = static_cast<int>(ceil_div(p.num_kt, p.kt_per_split));   // a short last piece may fill fewer
-  return pair ? launch_mode<2, kMode>(maps, p, splits, num_sms, stream) : launch_mode<1, kMode>(maps, p, splits, num_sms, stream);
+  p.share = share;
+  return pair ? launch_mode<2, kMode>(maps, p, stream) : launch_mode<1, kMode>(maps, p, stream);
 }
 
 constexpr int64_t kForwardRows = 32768;            // rows of one forward pass (bounds the statistics)
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 constexpr int64_t kMinPiece = 2048;
-constexpr int kPlanSms = 148;                      // the cut does not depend on the device that runs it
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// How the backward pass is cut: vocabulary entries per piece, splits of the dh product, and
+// How the backward pass is cut: vocabulary entries per piece, how the dh product is shared out, and
 // the offsets of the workspace's parts.
 struct Plan {
   int64_t piece, pieces, ld_dz;
-  int splits;
-  bool direct;        // dh straight from the product (one piece, one split)
-  size_t off_acc, off_gmax, bytes;
+  Share hidden;
+  size_t off_acc, off_slots, off_gmax, bytes;
 };
 
 Plan plan_backward(int64_t T, int64_t D, int64_t V, bool want_dh) {
@@ -627,26 +703,12 @@ Plan plan_backward(int64_t T, int64_t D, int64_t V, bool want_dh) {
   else q.piece = ceil_div(ceil_div(V, q.pieces), kBN) * kBN;      // even pieces
   q.pieces = ceil_div(V, q.piece);
   q.ld_dz = (q.piece + 7) / 8 * 8;
-  // Splits of the dh product's contraction (the piece): the number that leaves the fewest
-  // k-tiles in the longest chain of one CTA (or pair), each tile charged 4 for its epilogue.
-  const int pair = T > kBM ? 2 : 1;
-  const int64_t tiles = ceil_div(T, kBM * pair) * ceil_div(D, kBN), units = kPlanSms / pair;
-  const int64_t kt = ceil_div(q.piece, kBK);
-  int64_t best = INT64_MAX;
-  q.splits = 1;
-  for (int s = 1; s <= 32 && s <= kt; ++s) {
-    const int64_t per = ceil_div(kt, s);
-    if (ceil_div(kt, per) != s) continue;
-    const int64_t cost = ceil_div(tiles * s, units) * (per + 4);
-    if (cost < best) {
-      best = cost;
-      q.splits = s;
-    }
-  }
-  q.direct = q.pieces == 1 && q.splits == 1;
+  q.hidden = share_out(T, D, q.piece, true);
   size_t at = align256(static_cast<size_t>(T) * q.ld_dz * 2);
   q.off_acc = at;
-  if (want_dh && !q.direct) at += align256(static_cast<size_t>(q.splits) * T * D * 4);
+  if (want_dh && q.pieces > 1 && q.hidden.whole > 0) at += align256(static_cast<size_t>(T) * D * 4);
+  q.off_slots = at;
+  if (want_dh) at += static_cast<size_t>(q.hidden.tiles - q.hidden.whole) * q.hidden.slices * (kBM * pair_of(T)) * kBN * 4;
   q.off_gmax = at;
   q.bytes = at + 256;
   return q;
@@ -664,8 +726,7 @@ size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh) {
 }
 
 cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
-                              int64_t ignore, float* loss, float* lse, void* ws, int num_sms, void* encode_tiled,
-                              cudaStream_t stream) {
+                              int64_t ignore, float* loss, float* lse, void* ws, void* encode_tiled, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
   const int parts = static_cast<int>(2 * ceil_div(V, kBN));
   for (int64_t t0 = 0; t0 < T; t0 += kForwardRows) {
@@ -676,7 +737,7 @@ cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* label
     p.vocab = V;
     p.stats = static_cast<float2*>(ws);
     p.target = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(parts) * rows * sizeof(float2)));
-    cudaError_t e = product<kLogits>(encode, static_cast<const __nv_bfloat16*>(h) + t0 * D, D, w, D, rows, V, D, 1, p, num_sms, stream);
+    cudaError_t e = product<kLogits>(encode, static_cast<const __nv_bfloat16*>(h) + t0 * D, D, w, D, rows, V, D, share_out(rows, V, D, false), p, stream);
     if (e != cudaSuccess) return e;
     e = launch_pdl(rfq_ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 32))), dim3(32, 32), 0, 1, stream,
                    static_cast<const float2*>(p.stats), static_cast<const float*>(p.target), p.labels, static_cast<int>(rows),
@@ -687,13 +748,14 @@ cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* label
 }
 
 cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labels, const float* lse, const float* dloss,
-                               int64_t T, int64_t D, int64_t V, int64_t ignore, void* dh, void* dw, void* ws, int num_sms,
-                               void* encode_tiled, cudaStream_t stream) {
+                               int64_t T, int64_t D, int64_t V, int64_t ignore, void* dh, void* dw, void* ws, void* encode_tiled,
+                               cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
   const Plan q = plan_backward(T, D, V, dh != nullptr);
   uint8_t* base = static_cast<uint8_t*>(ws);
   __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
   float* acc = reinterpret_cast<float*>(base + q.off_acc);
+  float* slots = reinterpret_cast<float*>(base + q.off_slots);
   float* gmax = reinterpret_cast<float*>(base + q.off_gmax);
   cudaError_t e = launch_pdl(rfq_ce_gmax_kernel, dim3(1), dim3(1024), 0, 1, stream, dloss, labels, static_cast<int>(T), ignore, gmax);
   for (int64_t v0 = 0; v0 < V && e == cudaSuccess; v0 += q.piece) {
@@ -709,23 +771,26 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
     p.gmax = gmax;
     p.dz = dz;
     p.ld_dz = q.ld_dz;
-    e = product<kGrad>(encode, h, D, wp, D, T, n, D, 1, p, num_sms, stream);
+    e = product<kGrad>(encode, h, D, wp, D, T, n, D, share_out(T, n, D, false), p, stream);
     if (e == cudaSuccess && dh != nullptr) {
       p.acc = acc;
+      p.slots = slots;
       p.accumulate = v0 > 0;
-      p.out = q.direct ? static_cast<__nv_bfloat16*>(dh) : nullptr;
-      e = product<kHidden>(encode, dz, q.ld_dz, wp, D, T, D, n, q.splits, p, num_sms, stream);
+      p.out = q.pieces == 1 ? static_cast<__nv_bfloat16*>(dh) : nullptr;
+      e = product<kHidden>(encode, dz, q.ld_dz, wp, D, T, D, n, q.hidden, p, stream);
     }
     if (e == cudaSuccess && dw != nullptr) {
       p.out = static_cast<__nv_bfloat16*>(dw) + v0 * D;
-      e = product<kHead>(encode, dz, q.ld_dz, h, D, n, D, T, 1, p, num_sms, stream);
+      e = product<kHead>(encode, dz, q.ld_dz, h, D, n, D, T, share_out(n, D, T, false), p, stream);
     }
   }
-  if (e == cudaSuccess && dh != nullptr && !q.direct) {
-    const int64_t n4 = T * D / 4;
-    const int64_t blocks = ceil_div(n4, 256) < 8 * num_sms ? ceil_div(n4, 256) : 8 * num_sms;
-    e = launch_pdl(rfq_ce_hidden_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, stream, static_cast<const float*>(acc),
-                   q.splits, n4, static_cast<const float*>(gmax), static_cast<__nv_bfloat16*>(dh));
+  // Tiles of dh still in fp32: all of them after several pieces, else the rest.
+  const int tile0 = q.pieces > 1 ? 0 : q.hidden.whole;
+  if (e == cudaSuccess && dh != nullptr && tile0 < q.hidden.tiles) {
+    const int tile_rows = kBM * pair_of(T);
+    e = launch_pdl(rfq_ce_hidden_kernel, dim3(static_cast<unsigned>((q.hidden.tiles - tile0) * (tile_rows / 32))), dim3(256), 0, 1, stream,
+                   q.hidden, tile0, tile_rows, static_cast<const float*>(acc), static_cast<const float*>(slots),
+                   static_cast<const float*>(gmax), static_cast<int>(T), static_cast<int>(D), static_cast<__nv_bfloat16*>(dh));
   }
   return e;
 }
