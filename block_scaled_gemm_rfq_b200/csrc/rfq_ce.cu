@@ -59,14 +59,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 // the contraction at a time and the epilogue adds those parts with rounding.
 constexpr int kLogitsPart = 16;          // k-tiles
 
-template <int kPair>
+// Products that write a matrix pass its rows through 4 KiB of shared memory per epilogue warp, so that
+// they leave in whole 128-byte lines: a thread holds 128 columns of one row, and 16-byte stores of
+// 32 rows at a time held a head gradient of 64 tokens to 2.1 TB/s.
+template <int kPair, int kMode>
 struct Layout {
   static constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KiB
   static constexpr uint32_t kBTile = (kBN / kPair) * kBK * 2;     // 32 KiB (single) or 16 KiB (pair)
   static constexpr uint32_t kStage = kATile + kBTile;
   static constexpr uint32_t kBarrierBytes = 256;
-  static constexpr int kStages = static_cast<int>((kSmemLimit - 1024 - kBarrierBytes) / kStage);   // 4 or 7
-  static constexpr uint32_t kSmem = kStages * kStage + kBarrierBytes + 1024;
+  static constexpr uint32_t kOut = kMode == kLogits ? 0u : 8u * 4096u;
+  static constexpr int kStages = static_cast<int>((kSmemLimit - 1024 - kBarrierBytes - kOut) / kStage);   // 4 (single); 7 or 6
+  static constexpr uint32_t kSmem = kStages * kStage + kOut + kBarrierBytes + 1024;
   static_assert(kStage % 1024 == 0, "stage buffers must keep 1 KiB alignment");
   static_assert(kSmem <= kSmemLimit, "exceeds the 227 KiB shared-memory limit");
   static_assert((2 * kStages + 5) * 8 + 8 <= kBarrierBytes, "barrier area too small");
@@ -188,12 +192,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 template <int kPair, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_constant__ Maps maps, const Params p) {
-  using L = Layout<kPair>;
+  using L = Layout<kPair, kMode>;
   constexpr bool kAMn = kMode == kHead;
   constexpr bool kBMn = kMode == kHidden || kMode == kHead;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kStages * L::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kStages * L::kStage + L::kOut);
   uint64_t* empty = full + L::kStages;
   uint64_t* acc_full = empty + L::kStages;    // [2]
   uint64_t* acc_empty = acc_full + 2;         // [2]
@@ -388,9 +392,27 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       if constexpr (kMode == kLogits)
         for (int kp = t.kt0 + kLogitsPart; kp < t.kt1 && ok; kp += kLogitsPart) ok = take(false);
       if (!ok) break;
-      if (row >= p.M) continue;
+      // Hands this warp's rows over for storing, 128 bytes of each at a time: fill(c) gives this thread's
+      // 16-byte piece c, keep(r, c, piece) stores piece c of row r of the warp's 32.
+      auto turn = [&](int pieces, auto fill, auto keep) {
+        uint8_t* mine = smem + L::kStages * L::kStage + (warp - 2) * 4096;
+#pragma unroll
+        for (int c0 = 0; c0 < pieces; c0 += 8) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) = fill(c0 + c);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), c = lane & 7;
+            keep(r, c0 + c, *reinterpret_cast<const uint4*>(mine + r * 128 + ((c ^ (r & 7)) << 4)));
+          }
+          __syncwarp();
+        }
+      };
+      const int row_w = row - lane;   // the warp's first row
 
       if constexpr (kMode == kLogits) {
+        if (row >= p.M) continue;
         const int64_t label = p.labels[row] - p.v0 - col0;   // position inside this thread's columns, if 0..127
         const int cols = min(128, p.N - col0);               // may be <= 0 in the last column tile
         float m = -INFINITY;
@@ -420,16 +442,15 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
           p.target[row] = z;
         }
       } else if constexpr (kMode == kGrad) {
-        const int64_t label = p.labels[row];
+        const int at_row = min(row, p.M - 1);
+        const int64_t label = p.labels[at_row];
         const int64_t at = label - p.v0 - col0;
         const bool counted = label != p.ignore;
-        float g = p.dloss[row];
+        float g = p.dloss[at_row];
         g = gmax > 0.f ? g / gmax : g;          // gmax == 0: every finite entry is zero
         if (label < 0 || label >= p.vocab) g = NAN;
-        const float l2 = p.lse[row] * kLog2e;
-        __nv_bfloat16* dst = p.dz + static_cast<int64_t>(row) * p.ld_dz + col0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        const float l2 = p.lse[at_row] * kLog2e;
+        turn(16, [&](int i) {
           float d[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -438,47 +459,43 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
             if (k == at) q -= 1.f;
             d[e] = counted ? q * g : 0.f;
           }
-          if (col0 + 8 * i < p.N)
-            *reinterpret_cast<uint4*>(dst + 8 * i) =
-                make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
-        }
-      } else if constexpr (kMode == kHidden) {
-        if (p.out == nullptr || t.slot >= 0) {
-          float* dst = t.slot < 0 ? p.acc + static_cast<int64_t>(row) * p.N + col0
-                                  : p.slots + (static_cast<int64_t>(t.slot) * (kBM * kPair) + rank * kBM + quad * 32 + lane) * kBN + half * 128;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (col0 + 4 * i < p.N) {
-              float4 f = make_float4(__uint_as_float(v[i >> 3][(4 * i) & 31]), __uint_as_float(v[i >> 3][(4 * i + 1) & 31]),
-                                     __uint_as_float(v[i >> 3][(4 * i + 2) & 31]), __uint_as_float(v[i >> 3][(4 * i + 3) & 31]));
-              if (p.accumulate) {
-                const float4 o = *reinterpret_cast<const float4*>(dst + 4 * i);
-                f.x += o.x;
-                f.y += o.y;
-                f.z += o.z;
-                f.w += o.w;
-              }
-              *reinterpret_cast<float4*>(dst + 4 * i) = f;
-            }
+          return make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+        }, [&](int r, int c, const uint4& piece) {
+          if (row_w + r < p.M && col0 + 8 * c < p.N)
+            *reinterpret_cast<uint4*>(p.dz + static_cast<int64_t>(row_w + r) * p.ld_dz + col0 + 8 * c) = piece;
+        });
+      } else if (kMode == kHidden && (p.out == nullptr || t.slot >= 0)) {
+        float* dst = t.slot < 0 ? p.acc + static_cast<int64_t>(row_w) * p.N + col0
+                                : p.slots + (static_cast<int64_t>(t.slot) * (kBM * kPair) + rank * kBM + quad * 32) * kBN + half * 128;
+        const int64_t ld = t.slot < 0 ? p.N : kBN;
+        turn(32, [&](int i) {
+          return make_uint4(v[i >> 3][(4 * i) & 31], v[i >> 3][(4 * i + 1) & 31], v[i >> 3][(4 * i + 2) & 31], v[i >> 3][(4 * i + 3) & 31]);
+        }, [&](int r, int c, const uint4& piece) {
+          if (row_w + r >= p.M || col0 + 4 * c >= p.N) return;
+          float4 f = make_float4(__uint_as_float(piece.x), __uint_as_float(piece.y), __uint_as_float(piece.z), __uint_as_float(piece.w));
+          float4* o = reinterpret_cast<float4*>(dst + r * ld + 4 * c);
+          if (p.accumulate) {
+            const float4 was = *o;
+            f.x += was.x;
+            f.y += was.y;
+            f.z += was.z;
+            f.w += was.w;
           }
-        }
-      }
-      if constexpr (kMode == kHidden || kMode == kHead) {
-        if (kMode == kHead || (p.out != nullptr && t.slot < 0)) {
-          __nv_bfloat16* dst = p.out + static_cast<int64_t>(row) * p.N + col0;
+          *o = f;
+        });
+      } else {   // kHidden (one piece) and kHead
+        turn(16, [&](int i) {
+          uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (col0 + 8 * i < p.N) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int k = 8 * i + 2 * e;
-                w[e] = pack_bf16(__uint_as_float(v[k >> 5][k & 31]) * gmax, __uint_as_float(v[(k + 1) >> 5][(k + 1) & 31]) * gmax);
-              }
-              *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int k = 8 * i + 2 * e;
+            w[e] = pack_bf16(__uint_as_float(v[k >> 5][k & 31]) * gmax, __uint_as_float(v[(k + 1) >> 5][(k + 1) & 31]) * gmax);
           }
-        }
+          return make_uint4(w[0], w[1], w[2], w[3]);
+        }, [&](int r, int c, const uint4& piece) {
+          if (row_w + r < p.M && col0 + 8 * c < p.N)
+            *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row_w + r) * p.N + col0 + 8 * c) = piece;
+        });
       }
     }
   }
@@ -556,39 +573,37 @@ __global__ void __launch_bounds__(1024) rfq_ce_gmax_kernel(const float* dloss, c
 }
 
 // dh of the tiles that the product left in fp32: gmax * the sum of a tile's slots, in order, or (whole
-// tiles of a product over several pieces) gmax * its sums.  One block per 32 rows of a tile.
+// tiles of a product over several pieces) gmax * its sums.  One block per 4 rows of a tile, so that small
+// outputs of many slices have their loads under way at once.
 __global__ void __launch_bounds__(256) rfq_ce_hidden_kernel(const Share share, int tile0, int tile_rows, const float* acc, const float* slots,
                                                             const float* gmax, int M, int N, __nv_bfloat16* dh) {
   griddep_launch_dependents();
   griddep_wait();
-  const int blocks = tile_rows / 32;
+  const int blocks = tile_rows / 4;
   const int tile = tile0 + static_cast<int>(blockIdx.x) / blocks;
-  const int r0 = static_cast<int>(blockIdx.x) % blocks * 32;
+  const int r = static_cast<int>(blockIdx.x) % blocks * 4 + (threadIdx.x >> 6);
   int mb, nb;
   place(share, tile, &mb, &nb);
   const int rest = tile - share.whole;
+  const int in_tile = (threadIdx.x & 63) * 4, col = nb * kBN + in_tile, row = mb * tile_rows + r;
+  if (col >= N || row >= M) return;
   const float g = *gmax;
-  const int col = nb * kBN + (threadIdx.x & 63) * 4;
-  if (col >= N) return;
-  for (int r = r0 + (threadIdx.x >> 6); r < r0 + 32; r += 4) {
-    const int row = mb * tile_rows + r;
-    if (row >= M) break;
-    float4 f;
-    if (rest < 0) {
-      f = *reinterpret_cast<const float4*>(acc + static_cast<int64_t>(row) * N + col);
-    } else {
-      const float* src = slots + (static_cast<int64_t>(rest) * share.slices * tile_rows + r) * kBN + (threadIdx.x & 63) * 4;
-      f = *reinterpret_cast<const float4*>(src);
-      for (int s = 1; s < share.slices; ++s) {
-        const float4 o = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(s) * tile_rows * kBN);
-        f.x += o.x;
-        f.y += o.y;
-        f.z += o.z;
-        f.w += o.w;
-      }
+  float4 f;
+  if (rest < 0) {
+    f = *reinterpret_cast<const float4*>(acc + static_cast<int64_t>(row) * N + col);
+  } else {
+    const float* src = slots + (static_cast<int64_t>(rest) * share.slices * tile_rows + r) * kBN + in_tile;
+    f = *reinterpret_cast<const float4*>(src);
+#pragma unroll 8
+    for (int s = 1; s < share.slices; ++s) {
+      const float4 o = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(s) * tile_rows * kBN);
+      f.x += o.x;
+      f.y += o.y;
+      f.z += o.z;
+      f.w += o.w;
     }
-    *reinterpret_cast<uint2*>(dh + static_cast<int64_t>(row) * N + col) = make_uint2(pack_bf16(f.x * g, f.y * g), pack_bf16(f.z * g, f.w * g));
   }
+  *reinterpret_cast<uint2*>(dh + static_cast<int64_t>(row) * N + col) = make_uint2(pack_bf16(f.x * g, f.y * g), pack_bf16(f.z * g, f.w * g));
 }
 
 template <class Kernel, class... Args>
@@ -651,7 +666,7 @@ Share share_out(int64_t M, int64_t N, int64_t K, bool cut_rest) {
 
 template <int kPair, int kMode>
 cudaError_t launch_mode(const Maps& maps, const Params& p, cudaStream_t stream) {
-  using L = Layout<kPair>;
+  using L = Layout<kPair, kMode>;
   auto kernel = rfq_ce_kernel<kPair, kMode>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
@@ -788,7 +803,7 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
   const int tile0 = q.pieces > 1 ? 0 : q.hidden.whole;
   if (e == cudaSuccess && dh != nullptr && tile0 < q.hidden.tiles) {
     const int tile_rows = kBM * pair_of(T);
-    e = launch_pdl(rfq_ce_hidden_kernel, dim3(static_cast<unsigned>((q.hidden.tiles - tile0) * (tile_rows / 32))), dim3(256), 0, 1, stream,
+    e = launch_pdl(rfq_ce_hidden_kernel, dim3(static_cast<unsigned>((q.hidden.tiles - tile0) * (tile_rows / 4))), dim3(256), 0, 1, stream,
                    q.hidden, tile0, tile_rows, static_cast<const float*>(acc), static_cast<const float*>(slots),
                    static_cast<const float*>(gmax), static_cast<int>(T), static_cast<int>(D), static_cast<__nv_bfloat16*>(dh));
   }
