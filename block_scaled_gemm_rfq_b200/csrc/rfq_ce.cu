@@ -535,19 +535,26 @@ __global__ void __launch_bounds__(1024) rfq_ce_join_kernel(const float2* stats, 
   sc[strand][lane] = c;
   ss[strand][lane] = s;
   __syncthreads();
-  if (strand == 0 && row < M) {
-    float top = -INFINITY;
-    for (int k = 0; k < 32; ++k) top = fmaxf(top, sc[k][lane]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    for (int k = 0; k < 32; ++k) sum += ss[k][lane] * ex2(sc[k][lane] - base);
-    const double l = static_cast<double>(base) * 0.69314718055994530942 + log(static_cast<double>(sum));
-    lse[row] = static_cast<float>(l);
-    const int64_t label = labels[row];
+  // A warp for each row, a lane for each strand.
+  const int out_row = blockIdx.x * 32 + strand;
+  if (out_row >= M) return;
+  c = sc[lane][strand];
+  s = ss[lane][strand];
+  float top = c;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -INFINITY ? 0.f : top;
+  s *= ex2(c - base);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (lane == 0) {
+    const double l = static_cast<double>(base) * 0.69314718055994530942 + log(static_cast<double>(s));
+    lse[out_row] = static_cast<float>(l);
+    const int64_t label = labels[out_row];
     float out = 0.f;
     if (label != ignore)
-      out = label >= 0 && label < vocab ? static_cast<float>(l - static_cast<double>(target[row])) : NAN;
-    loss[row] = out;
+      out = label >= 0 && label < vocab ? static_cast<float>(l - static_cast<double>(target[out_row])) : NAN;
+    loss[out_row] = out;
   }
 }
 
