@@ -56,7 +56,7 @@ constexpr int kRows = 16;                  // rows of one group
 constexpr int kMaxAdapters = RFQ_LORA_MAX_ADAPTERS;
 constexpr int kMaxStages = 6;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kStaticSmem = 24 * 1024;     // more than any kernel here has besides its dynamic part
+constexpr int kStaticSmem = 21 * 1024;     // as much as any kernel here has besides its dynamic part
 
 __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Row stride in shared memory of rows of `bytes` bytes: an odd number of 16-byte units, so that
@@ -887,6 +887,8 @@ constexpr int kOuterCols = 128;
 constexpr int kOuterRows = 64;        // rows of one stage
 constexpr int kMaxRange = 4096;       // rows of one range
 
+constexpr int kOuterStatic = kMaxAdapters + 4 * kMaxRange + 64;   // its fixed shared memory
+
 struct OuterSide {
   const __nv_bfloat16* v;     // [M][ld]: terms of r each, kT or more
   int ld;
@@ -1157,7 +1159,7 @@ constexpr int kPlanSms = 148;   // the cut does not depend on the device that ru
 
 template <class Kernel, class Params>
 cudaError_t launch(Kernel kernel, const Params& p, dim3 grid, size_t smem, cudaStream_t stream) {
-  if (smem > kStaticSmem) {   // with the static part it may pass the default limit of 48 KiB
+  if (smem > 48 * 1024 - kStaticSmem) {   // with the static part it may pass the default limit
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
@@ -1175,11 +1177,11 @@ cudaError_t launch(Kernel kernel, const Params& p, dim3 grid, size_t smem, cudaS
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Stages of a ring: four if two CTAs then share an SM, else as many as fit one (2 to 6).
+// Stages of a ring: three or four if two CTAs then share an SM, else as many as fit one (2 to 6).
 int ring_stages(int stage_bytes, int other_bytes) {
-  const int half = (kSmemLimit / 2 - kStaticSmem / 4 - other_bytes) / stage_bytes;
+  const int half = (kSmemLimit / 2 - 1024 - other_bytes) / stage_bytes;
   if (half >= 3) return half < 4 ? half : 4;
-  const int whole = (kSmemLimit - kStaticSmem - other_bytes) / stage_bytes;
+  const int whole = (kSmemLimit - 1024 - other_bytes) / stage_bytes;
   return whole < kMaxStages ? whole : kMaxStages;
 }
 
@@ -1231,7 +1233,7 @@ cudaError_t shrink(const void* src, const void* w, bool trans, const int* ids, i
     return launch(rfq_lora_shrink_direct_kernel<16>, p, grid, 0, stream);
   }
   const int stage = kRows * kRowStride + shrink_p_bytes(p.r), red = shrink_red_bytes(p.r);
-  p.stages = ring_stages(stage, red);
+  p.stages = ring_stages(stage, red + static_cast<int>(sizeof(Groups)));
   const size_t smem = static_cast<size_t>(p.stages) * stage + red;
   if (r <= 16) return launch(rfq_lora_shrink_kernel<2>, p, grid, smem, stream);
   if (r <= 32) return launch(rfq_lora_shrink_kernel<4>, p, grid, smem, stream);
@@ -1254,7 +1256,7 @@ cudaError_t expand_typed(ExpandParams p, bool trans, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(chunks * z), static_cast<unsigned>(ceil_div(tiles, p.tiles)));
   if (!trans) return launch(rfq_lora_expand_direct_kernel<kF32>, p, grid, 0, stream);
   const int stage = expand_stage_bytes<kF32>(p.r), other = expand_s_bytes<kF32>(p.r);
-  p.stages = ring_stages(stage, other);
+  p.stages = ring_stages(stage, other + static_cast<int>(sizeof(Groups)));
   return launch(rfq_lora_expand_kernel<kF32>, p, grid, static_cast<size_t>(p.stages) * stage + other, stream);
 }
 
@@ -1279,7 +1281,7 @@ cudaError_t expand(const float* part, int splits, const float* scale, const void
 template <int kT>
 cudaError_t outer_rank(OuterParams p, dim3 grid, cudaStream_t stream) {
   const int stage = outer_stage_bytes<kT>(p.r);
-  p.stages = ring_stages(stage, kStaticSmem);
+  p.stages = ring_stages(stage, kOuterStatic + 64);
   const size_t smem = static_cast<size_t>(p.stages) * stage + 64;   // the last row's fragments may reach past its end
   if (p.r <= 16) return launch(rfq_lora_outer_kernel<1, kT>, p, grid, smem, stream);
   if (p.r <= 32) return launch(rfq_lora_outer_kernel<2, kT>, p, grid, smem, stream);

@@ -17,12 +17,14 @@
 //
 // shrink: the contraction is split over a cluster of up to 8 CTAs, whose partial sums are added
 // through distributed shared memory in the order of the ranks.  The accumulator takes 1024
-// elements of the contraction at a time (the tensor cores add by truncation) and the epilogue
-// adds those parts with rounding.
+// elements of the contraction at a time (256 for fp32 results: the tensor cores add by
+// truncation) and the epilogue adds those parts with rounding.
 // shrink leaves s as bf16 terms (one for a bf16 output; three, 24 bits, for an fp32 one), which are
 // expand's operand as they are.
 // expand: base tiles come in by TMA, are added to in shared memory and leave from there by TMA.
 //
+// (by a warp of its own: behind the loads of Q in one queue, chunks of two adapters held the base back
+// and cost 1.3 times those of one).
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, the others epilogue.  Every wait on an mbarrier
 // is bounded (rfq_ptx.cuh); after one that ran out the epilogue runs through its loops without
 // waiting, so that no warp is left alone at a barrier.  No TMA multicast.
@@ -46,7 +48,8 @@ constexpr int kChunk = 128;
 constexpr uint32_t kBox = kChunk * 128;    // 128 rows of 128 bytes
 constexpr uint32_t kSmemLimit = 232448;
 constexpr int kMaxStages = 8;
-constexpr int kPartTiles = 16;             // k-tiles of 64 per accumulation
+// k-tiles of 64 per accumulation, for bf16 and for fp32 results.
+constexpr int kPartTiles = 16, kPartTilesF32 = 4;
 
 // Shared-memory operand descriptors, 128-byte swizzle (K-major: 8-row groups 1024 bytes apart;
 // M/N-major: chunks of 64 elements `lead` bytes apart, 8 contraction rows 1024 bytes apart).
@@ -61,38 +64,44 @@ __device__ __forceinline__ uint32_t idesc(uint32_t n, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(b_mn) << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// The adapters of a chunk in the order of their first rows; a warp's lanes hold the 128 ids.
-struct Walk {
+// The adapters of a chunk in the order of their first rows.  A warp's lanes hold the 128 ids (lane + 32 i)
+// and the list (adapter d in lane d % 32, word d / 32), so that a look is one shuffle; all lanes of
+// the warp call these together.
+struct Adapters {
   int id[4];
-  unsigned left;   // bit i: row lane + 32 i not yet taken
+  int list[4];
+  int count;
   __device__ __forceinline__ void load(const int* ids, int64_t row0, int64_t M, int n) {
     const int lane = threadIdx.x & 31;
+    unsigned left = 0;   // bit i: row lane + 32 i not yet taken
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t row = row0 + lane + 32 * i;
       const int v = row < M ? ids[row] : -1;
       id[i] = v >= 0 && v < n ? v : -1;
+      left |= static_cast<unsigned>(id[i] >= 0) << i;
     }
-    restart();
-  }
-  __device__ __forceinline__ void restart() {
-    left = 0;
+    count = 0;
+    while (true) {
+      int a = -1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) left |= static_cast<unsigned>(id[i] >= 0) << i;
-  }
-  // The next adapter, or -1.  All lanes of the warp call it together.
-  __device__ __forceinline__ int next() {
-    int a = -1;
+      for (int i = 3; i >= 0; --i) {
+        const unsigned m = __ballot_sync(0xffffffffu, left >> i & 1u);
+        const int v = __shfl_sync(0xffffffffu, id[i], m ? __ffs(m) - 1 : 0);
+        if (m) a = v;
+      }
+      if (a < 0) break;
 #pragma unroll
-    for (int i = 3; i >= 0; --i) {
-      const unsigned m = __ballot_sync(0xffffffffu, left >> i & 1u);
-      const int v = __shfl_sync(0xffffffffu, id[i], m ? __ffs(m) - 1 : 0);
-      if (m) a = v;
+      for (int i = 0; i < 4; ++i) {
+        if (id[i] == a) left &= ~(1u << i);
+        if (lane == (count & 31) && i == count >> 5) list[i] = a;
+      }
+      ++count;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (id[i] == a) left &= ~(1u << i);
-    return a;
+  }
+  __device__ __forceinline__ int at(int d) const {
+    const int w = d >> 5;
+    return __shfl_sync(0xffffffffu, w == 0 ? list[0] : w == 1 ? list[1] : w == 2 ? list[2] : list[3], d & 31);
   }
 };
 
@@ -133,7 +142,7 @@ struct ShrinkParams {
   __nv_bfloat16* terms;    // [M][num_terms][r]: s as a sum of bf16 terms
   int num_terms;
   int64_t M;
-  int n, r, kt, kt_per_rank, cluster, stages;
+  int n, r, kt, kt_per_rank, part, cluster, stages;
 };
 
 constexpr int kShrinkThreads = 192;   // TMA, MMA, four epilogue warps
@@ -189,14 +198,15 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.cluster) * kChunk;
   const int kt0 = static_cast<int>(rank) * p.kt_per_rank;
   const int kt1 = min(p.kt, kt0 + p.kt_per_rank);
-  Walk walk;
+  Adapters walk;
   walk.load(p.ids, row0, p.M, p.n);
 
   if (warp == 0) {
     Cursor c;
     Filled filled;
     bool ok = true;
-    for (int a = walk.next(); a >= 0 && ok; a = walk.next()) {
+    for (int d = 0; d < walk.count && ok; ++d) {
+      const int a = walk.at(d);
       if (lane == 0) {
         for (int kt = kt0; kt < kt1; ++kt) {
           ok = mbar_wait(&empty[c.stage], c.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
@@ -222,14 +232,14 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
     Cursor c, acc;
     bool ok = true;
     const uint32_t id = idesc(r16, kTrans);
-    for (int a = walk.next(); a >= 0 && ok; a = walk.next()) {
+    for (int pass = 0; pass < walk.count && ok; ++pass) {
       if (lane == 0) {
-        for (int kp = kt0; kp < kt1 && ok; kp += kPartTiles) {
+        for (int kp = kt0; kp < kt1 && ok; kp += p.part) {
           ok = mbar_wait(&acc_empty[acc.stage], acc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitAccEmpty);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + acc.stage * acc_cols;
-          for (int kt = kp; kt < min(kp + kPartTiles, kt1); ++kt) {
+          for (int kt = kp; kt < min(kp + p.part, kt1); ++kt) {
             ok = mbar_wait(&full[c.stage], c.phase, abort_flag, &g_lora_error, kErrWaitFull);
             if (!ok) break;
             tc_fence_after();
@@ -261,8 +271,9 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
     const int mine = walk.id[0] * (quad == 0) + walk.id[1] * (quad == 1) + walk.id[2] * (quad == 2) + walk.id[3] * (quad == 3);
     float* out = sums + row * (p.r + 4);
     Cursor acc;
-    for (int a = walk.next(); a >= 0; a = walk.next()) {
-      for (int kp = kt0; kp < kt1; kp += kPartTiles) {
+    for (int d = 0; d < walk.count; ++d) {
+      const int a = walk.at(d);
+      for (int kp = kt0; kp < kt1; kp += p.part) {
         mbar_wait(&acc_full[acc.stage], acc.phase, abort_flag, &g_lora_error, kErrWaitAccFull, 2 * kWaitLimitNs);
         tc_fence_after();
         __syncwarp();
@@ -349,7 +360,9 @@ struct ExpandParams {
   int s_stages, base_stages, q_stages;
 };
 
-constexpr int kExpandThreads = 320;    // TMA, MMA, eight epilogue warps
+constexpr int kExpandThreads = 352;    // TMA of s and Q, MMA, eight epilogue warps, TMA of the base
+constexpr int kBaseWarp = 10;
+constexpr int kAccs = 4;               // accumulators of 128 columns in tensor memory
 // Columns of a tile: 256 bytes of a row, two boxes of 128 bytes.
 template <bool kF32>
 constexpr int kCols = kF32 ? 64 : 128;
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
   constexpr int kN = kCols<kF32>;
   constexpr int kBoxCols = kN / 2;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t b_full[kMaxStages], b_empty[kMaxStages], q_full[kMaxStages], q_empty[kMaxStages], acc_full[2], acc_empty[2],
+  __shared__ uint64_t b_full[kMaxStages], b_empty[kMaxStages], q_full[kMaxStages], q_empty[kMaxStages], acc_full[kAccs], acc_empty[kAccs],
       s_full[2], s_empty[2], drained;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -396,7 +409,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 8);
     }
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
     prefetch_tmap(&maps.out);
   }
   if (warp == 1) {
-    tmem_alloc_g<1>(&tmem_slot, 256);
+    tmem_alloc_g<1>(&tmem_slot, kAccs * 128);
     tmem_relinquish_g<1>();
   }
   tc_fence_before();
@@ -425,18 +438,17 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
 
   // A unit is a chunk of rows and a run of column tiles.  Where a chunk has no adapter and the
   // base is the output, there is nothing to do; every role finds that out for itself.
-  Walk walk;
+  Adapters walk;
   if (warp == 0) {
-    Cursor sc, bc, qc;
-    Filled s_filled, b_filled, q_filled;
+    Cursor sc, qc;
+    Filled s_filled, q_filled;
     bool ok = true;
     for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
       const int64_t row0 = unit / p.col_units * kChunk;
       const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
       walk.load(p.ids, row0, p.M, p.n);
-      const bool any = __any_sync(0xffffffffu, walk.left != 0);
-      if (!any && p.in_place) continue;
-      if (any && lane == 0) {
+      if (walk.count == 0) continue;
+      if (lane == 0) {
         ok = mbar_wait(&s_empty[sc.stage], sc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
         if (ok) {
           uint8_t* ss = s_mem + sc.stage * s_bytes;
@@ -451,20 +463,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
       ok = __shfl_sync(0xffffffffu, ok, 0);
       for (int t = t0; t < t1 && ok; ++t) {
         const int col = t * kN;
-        if (p.has_base && lane == 0) {
-          ok = mbar_wait(&b_empty[bc.stage], bc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
-          if (ok) {
-            uint8_t* sb = b_mem + bc.stage * 2 * kBox;
-            mbar_arrive_expect_tx(&b_full[bc.stage], 2 * kBox);
-            tma_load_2d(sb, &maps.base, &b_full[bc.stage], col, static_cast<int>(row0));
-            tma_load_2d(sb + kBox, &maps.base, &b_full[bc.stage], col + kBoxCols, static_cast<int>(row0));
-            b_filled.add(bc);
-            bc.next(p.base_stages);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        walk.restart();
-        for (int a = walk.next(); a >= 0 && ok; a = walk.next()) {
+        for (int d = 0; d < walk.count && ok; ++d) {
+          const int a = walk.at(d);
           if (lane == 0) {
             ok = mbar_wait(&q_empty[qc.stage], qc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
             if (ok) {
@@ -487,9 +487,36 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
     }
     if (lane == 0) {
       s_filled.drain(s_full, p.s_stages);
-      b_filled.drain(b_full, p.base_stages);
       q_filled.drain(q_full, p.q_stages);
     }
+    __syncwarp();
+  } else if (warp == kBaseWarp) {
+    Cursor bc;
+    Filled b_filled;
+    bool ok = p.has_base != 0;
+    for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
+      const int64_t row0 = unit / p.col_units * kChunk;
+      const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
+      if (p.in_place) {
+        walk.load(p.ids, row0, p.M, p.n);
+        if (walk.count == 0) continue;
+      }
+      if (lane == 0) {
+        for (int t = t0; t < t1; ++t) {
+          ok = mbar_wait(&b_empty[bc.stage], bc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
+          if (!ok) break;
+          const int col = t * kN;
+          uint8_t* sb = b_mem + bc.stage * 2 * kBox;
+          mbar_arrive_expect_tx(&b_full[bc.stage], 2 * kBox);
+          tma_load_2d(sb, &maps.base, &b_full[bc.stage], col, static_cast<int>(row0));
+          tma_load_2d(sb + kBox, &maps.base, &b_full[bc.stage], col + kBoxCols, static_cast<int>(row0));
+          b_filled.add(bc);
+          bc.next(p.base_stages);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) b_filled.drain(b_full, p.base_stages);
     __syncwarp();
   } else if (warp == 1) {
     Cursor sc, qc, acc;
@@ -501,15 +528,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
       const int64_t row0 = unit / p.col_units * kChunk;
       const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
       walk.load(p.ids, row0, p.M, p.n);
-      if (!__any_sync(0xffffffffu, walk.left != 0)) continue;
+      if (walk.count == 0) continue;
       if (lane == 0) {
         ok = mbar_wait(&s_full[sc.stage], sc.phase, abort_flag, &g_lora_error, kErrWaitFull);
         tc_fence_after();
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       for (int t = t0; t < t1 && ok; ++t) {
-        walk.restart();
-        for (int a = walk.next(); a >= 0 && ok; a = walk.next()) {
+        for (int pass = 0; pass < walk.count && ok; ++pass) {
           if (lane == 0) {
             ok = mbar_wait(&acc_empty[acc.stage], acc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitAccEmpty) &&
                  mbar_wait(&q_full[qc.stage], qc.phase, abort_flag, &g_lora_error, kErrWaitFull);
@@ -530,7 +556,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
               tc_commit(&acc_full[acc.stage]);
             }
             qc.next(p.q_stages);
-            acc.next(2);
+            acc.next(kAccs);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
@@ -563,7 +589,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
       const int64_t row0 = unit / p.col_units * kChunk;
       const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
       walk.load(p.ids, row0, p.M, p.n);
-      const bool any = __any_sync(0xffffffffu, walk.left != 0);
+      const bool any = walk.count > 0;
       if (!any && p.in_place) continue;
       const int mine = quad == 0 ? walk.id[0] : quad == 1 ? walk.id[1] : quad == 2 ? walk.id[2] : walk.id[3];
       for (int t = t0; t < t1; ++t) {
@@ -578,8 +604,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(line + c * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
-        walk.restart();
-        for (int a = walk.next(); a >= 0; a = walk.next()) {
+        for (int d = 0; d < walk.count; ++d) {
+          const int a = walk.at(d);
           mbar_wait(&acc_full[acc.stage], acc.phase, abort_flag, &g_lora_error, kErrWaitAccFull, 2 * kWaitLimitNs);
           tc_fence_after();
           __syncwarp();
@@ -628,7 +654,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[acc.stage]);
-          acc.next(2);
+          acc.next(kAccs);
         }
         fence_proxy_async_smem();
         asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -657,7 +683,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    tmem_dealloc_g<1>(tmem, 256);
+    tmem_dealloc_g<1>(tmem, kAccs * 128);
   }
 }
 
@@ -739,6 +765,7 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
   p.s = s;
   p.terms = static_cast<__nv_bfloat16*>(terms);
   p.num_terms = num_terms;
+  p.part = num_terms == 3 ? kPartTilesF32 : kPartTiles;
   p.M = M;
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
