@@ -98,6 +98,9 @@ __device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[2], u
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16_bytes(uint32_t dst, const void* src, int bytes) {   // 16, or 0 for zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most stages - 2 groups of this thread are on their way (stages: 2 to kMaxStages).
 __device__ __forceinline__ void cp_wait_stage(int stages) {
@@ -903,7 +906,6 @@ struct OuterParams {
   int* present;               // [ranges][n]
   int64_t M;
   int n, r, range;            // range: rows of one range
-  int stages;
 };
 
 constexpr int kWStride = odd_stride(kOuterCols * 2);
@@ -915,6 +917,12 @@ template <int kT>
 __host__ __device__ constexpr int outer_stage_bytes(int r) {
   return kOuterRows * (kWStride + outer_v_stride<kT>(r));
 }
+// Stages of the ring: four where two CTAs then share an SM, else what fits one, at most four.
+template <int kJ16, int kT>
+constexpr int kOuterStages =
+    4 * outer_stage_bytes<kT>(16 * kJ16) + kOuterStatic + 1088 <= kSmemLimit / 2
+        ? 4
+        : (kSmemLimit - kOuterStatic - 1088) / outer_stage_bytes<kT>(16 * kJ16) < 4 ? (kSmemLimit - kOuterStatic - 1088) / outer_stage_bytes<kT>(16 * kJ16) : 4;
 
 template <int kJ16, int kT>   // kJ16: 16-row tiles of the rank, at most
 __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterParams p) {
@@ -942,6 +950,10 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
   const int qx = tid & 15;
   const bool qx_ok = c0 + 8 * qx < s.C;
   // This thread's 16-byte pieces of a stage's v: row, element in v, place in the stage.
+  constexpr int kS = kOuterStages<kJ16, kT>;
+  const uint32_t w_to = (tid >> 4) * kWStride + 16 * qx;
+  const int w_size = qx_ok ? 16 : 0;
+  const int64_t w_step = 16 * s.C;
   constexpr int kVCopies = (kOuterRows * kT * kJ16 * 2 + kThreads - 1) / kThreads;
   int v_m[kVCopies], v_from[kVCopies];
   uint32_t v_to[kVCopies];
@@ -993,12 +1005,25 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
     // Rows that are neighbours (one request, one adapter for all) are stepped through; others are looked
     // up in the list for each copy.
     const bool run = list[total - 1] - list[0] == total - 1;
-    const __nv_bfloat16* w_at = s.w + (row0 + list[0] + (tid >> 4)) * s.C + c0 + 8 * qx;
+    const __nv_bfloat16* w_at = qx_ok ? s.w + (row0 + list[0] + (tid >> 4)) * s.C + c0 + 8 * qx : s.w;
     const __nv_bfloat16* v_at = s.v + (row0 + list[0]) * s.ld;
     int load_stage = 0, load_at = 0;
+    uint32_t load_to = base;
     auto load = [&]() {
-      if (load_at < total) {
-        const uint32_t sw = base + load_stage * stage_bytes, sv = sw + kOuterRows * kWStride;
+      if (run && load_at + kOuterRows <= total) {   // whole stages of neighbours, the usual ones
+        const __nv_bfloat16* from = w_at;
+#pragma unroll
+        for (int u = 0; u < kOuterRows / 16; ++u) {
+          cp_async16_bytes(load_to + w_to + 16 * u * kWStride, from, w_size);
+          from += w_step;
+        }
+        w_at = from;
+#pragma unroll
+        for (int u = 0; u < kVCopies; ++u)
+          if (v_m[u] < kOuterRows) cp_async16_bytes(load_to + kOuterRows * kWStride + v_to[u], v_at + v_from[u], 16);
+        v_at += kOuterRows * s.ld;
+      } else if (load_at < total) {
+        const uint32_t sw = load_to, sv = sw + kOuterRows * kWStride;
 #pragma unroll
         for (int u = 0; u < kOuterRows / 16; ++u) {   // rows past the last: zeros
           const int m = (tid >> 4) + 16 * u;
@@ -1020,7 +1045,11 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
       }
       cp_commit();
       load_at += kOuterRows;
-      if (++load_stage == p.stages) load_stage = 0;
+      load_to += stage_bytes;
+      if (++load_stage == kS) {
+        load_stage = 0;
+        load_to = base;
+      }
     };
     // fp32 results: the MMAs add by truncation, so each stage's 64 rows are summed on their own and
     // added to the rest with rounding.
@@ -1035,13 +1064,14 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
           acc[j][h][e] = 0.f;
           if constexpr (kFlush) sum[j][h][e] = 0.f;
         }
-    for (int it = 0; it < p.stages - 1; ++it) load();
+    for (int it = 0; it < kS - 1; ++it) load();
     int stage = 0;
+    uint32_t sw = base;
     for (int it = 0; it < iters; ++it) {
-      cp_wait_stage(p.stages);
+      cp_wait_stage(kS);
       __syncthreads();
       load();
-      const uint32_t sw = base + stage * stage_bytes, sv = sw + kOuterRows * kWStride;
+      const uint32_t sv = sw + kOuterRows * kWStride;
 #pragma unroll
       for (int ks = 0; ks < kOuterRows / 16; ++ks) {
         uint32_t fb[4];   // w: rows along the contraction; tiles of columns 16 * warp, + 8
@@ -1071,7 +1101,11 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
               acc[j][h][e] = 0.f;
             }
       }
-      if (++stage == p.stages) stage = 0;
+      sw += stage_bytes;
+      if (++stage == kS) {
+        stage = 0;
+        sw = base;
+      }
     }
     if constexpr (kFlush) {
 #pragma unroll
@@ -1278,15 +1312,17 @@ cudaError_t expand(const float* part, int splits, const float* scale, const void
   return f32 ? expand_typed<true>(p, trans, stream) : expand_typed<false>(p, trans, stream);
 }
 
+template <int kJ16, int kT>
+cudaError_t outer_typed(const OuterParams& p, dim3 grid, cudaStream_t stream) {
+  // The last row's fragments may reach past its end.
+  return launch(rfq_lora_outer_kernel<kJ16, kT>, p, grid, static_cast<size_t>(kOuterStages<kJ16, kT>) * outer_stage_bytes<kT>(p.r) + 64, stream);
+}
 template <int kT>
-cudaError_t outer_rank(OuterParams p, dim3 grid, cudaStream_t stream) {
-  const int stage = outer_stage_bytes<kT>(p.r);
-  p.stages = ring_stages(stage, kOuterStatic + 64);
-  const size_t smem = static_cast<size_t>(p.stages) * stage + 64;   // the last row's fragments may reach past its end
-  if (p.r <= 16) return launch(rfq_lora_outer_kernel<1, kT>, p, grid, smem, stream);
-  if (p.r <= 32) return launch(rfq_lora_outer_kernel<2, kT>, p, grid, smem, stream);
-  if (p.r <= 64) return launch(rfq_lora_outer_kernel<4, kT>, p, grid, smem, stream);
-  return launch(rfq_lora_outer_kernel<8, kT>, p, grid, smem, stream);
+cudaError_t outer_rank(const OuterParams& p, dim3 grid, cudaStream_t stream) {
+  if (p.r <= 16) return outer_typed<1, kT>(p, grid, stream);
+  if (p.r <= 32) return outer_typed<2, kT>(p, grid, stream);
+  if (p.r <= 64) return outer_typed<4, kT>(p, grid, stream);
+  return outer_typed<8, kT>(p, grid, stream);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
