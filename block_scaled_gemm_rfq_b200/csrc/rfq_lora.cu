@@ -887,10 +887,10 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_split_kernel(const SplitPar
 // part[range][a][j][c] = sum over the range's rows of adapter a of v[m][j] w[m][c], for the two
 // pairs (v, w) = (ds', x) and (s', dy).
 constexpr int kOuterCols = 128;
-constexpr int kOuterRows = 64;        // rows of one stage
+constexpr int kOuterRows = 32;        // rows of one stage
 constexpr int kMaxRange = 4096;       // rows of one range
 
-constexpr int kOuterStatic = kMaxAdapters + 4 * kMaxRange + 64;   // its fixed shared memory
+constexpr int kOuterStatic = kMaxAdapters + 2 * kMaxRange + 64;   // its fixed shared memory
 
 struct OuterSide {
   const __nv_bfloat16* v;     // [M][ld]: terms of r each, kT or more
@@ -917,19 +917,16 @@ template <int kT>
 __host__ __device__ constexpr int outer_stage_bytes(int r) {
   return kOuterRows * (kWStride + outer_v_stride<kT>(r));
 }
-// Stages of the ring: four where two CTAs then share an SM, else what fits one, at most four.
+// Stages of the ring (four of the largest, rank 128 in three terms, fill one SM's shared memory).
 template <int kJ16, int kT>
-constexpr int kOuterStages =
-    4 * outer_stage_bytes<kT>(16 * kJ16) + kOuterStatic + 1088 <= kSmemLimit / 2
-        ? 4
-        : (kSmemLimit - kOuterStatic - 1088) / outer_stage_bytes<kT>(16 * kJ16) < 4 ? (kSmemLimit - kOuterStatic - 1088) / outer_stage_bytes<kT>(16 * kJ16) : 4;
+constexpr int kOuterStages = 4;
+static_assert(4 * outer_stage_bytes<3>(128) + kOuterStatic + 1088 <= kSmemLimit, "the largest ring fits");
 
 template <int kJ16, int kT>   // kJ16: 16-row tiles of the rank, at most
 __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint8_t here[kMaxAdapters];
   __shared__ uint16_t list[kMaxRange];
-  __shared__ int16_t rid[kMaxRange];
   __shared__ int warp_count[8];
   griddep_launch_dependents();
   griddep_wait();
@@ -969,9 +966,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
   __syncthreads();
   for (int i = tid; i < count; i += kThreads) {
     const int id = p.ids[row0 + i];
-    const bool ok = id >= 0 && id < p.n;
-    rid[i] = ok ? static_cast<int16_t>(id) : int16_t(-1);
-    if (ok) here[id] = 1;
+    if (id >= 0 && id < p.n) here[id] = 1;
   }
   __syncthreads();
   if (blockIdx.x == 0 && blockIdx.z == 0)
@@ -982,7 +977,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
     if (!here[a]) continue;
     // The rows of this adapter, in order.
     int mine = 0;
-    for (int i = tid * per; i < min(count, (tid + 1) * per); ++i) mine += rid[i] == a;
+    for (int i = tid * per; i < min(count, (tid + 1) * per); ++i) mine += p.ids[row0 + i] == a;
     int before = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -998,7 +993,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
       total += warp_count[w];
     }
     for (int i = tid * per; i < min(count, (tid + 1) * per); ++i)
-      if (rid[i] == a) list[offset++] = static_cast<uint16_t>(i);
+      if (p.ids[row0 + i] == a) list[offset++] = static_cast<uint16_t>(i);
     __syncthreads();
 
     const int iters = (total + kOuterRows - 1) / kOuterRows;
@@ -1327,9 +1322,9 @@ cudaError_t outer_rank(const OuterParams& p, dim3 grid, cudaStream_t stream) {
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Rows of one range of the outer products: one wave of two CTAs per SM over all column tiles.
+// Rows of one range of the outer products: one wave of three CTAs per SM over all column tiles.
 int outer_range(int64_t M, int64_t tiles) {
-  const int64_t want = tiles < 2 * kPlanSms ? 2 * kPlanSms / tiles : 1;
+  const int64_t want = tiles < 3 * kPlanSms ? 3 * kPlanSms / tiles : 1;
   int64_t rows = ceil_div(ceil_div(M, want), kOuterRows) * kOuterRows;
   if (rows < 256) rows = 256;
   if (rows > kMaxRange) rows = kMaxRange;
