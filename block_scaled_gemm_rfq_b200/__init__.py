@@ -83,6 +83,8 @@ def library_path() -> str:
 def load_library():
     """Load librfq.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -150,10 +152,10 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _need(where, t, shape, dtype, device):
+def _need(where, name, t, shape, dtype, device):
     """Refuse a tensor that is not what the C call will read: its type, shape, packing or device."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise RFQError(1, f"{where}: want a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
+        raise RFQError(1, f"{where}: {name}: want a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
                           f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
@@ -342,11 +344,11 @@ def linear_ce(h, w, labels, loss, lse, workspace, ignore_index=-100, stream=None
     T, D = h.shape
     V = w.shape[0]
     dev = h.device
-    _need("rfq_linear_ce: h", h, (T, D), torch.bfloat16, dev)
-    _need("rfq_linear_ce: w", w, (V, D), torch.bfloat16, dev)
-    _need("rfq_linear_ce: labels", labels, (T,), torch.int64, dev)
-    _need("rfq_linear_ce: loss", loss, (T,), torch.float32, dev)
-    _need("rfq_linear_ce: lse", lse, (T,), torch.float32, dev)
+    _need("rfq_linear_ce", "h", h, (T, D), torch.bfloat16, dev)
+    _need("rfq_linear_ce", "w", w, (V, D), torch.bfloat16, dev)
+    _need("rfq_linear_ce", "labels", labels, (T,), torch.int64, dev)
+    _need("rfq_linear_ce", "loss", loss, (T,), torch.float32, dev)
+    _need("rfq_linear_ce", "lse", lse, (T,), torch.float32, dev)
     _need_workspace("rfq_linear_ce", workspace, dev)
     _call("rfq_linear_ce", dev, stream, load_library().rfq_linear_ce, h.data_ptr(), w.data_ptr(), labels.data_ptr(),
               T, D, V, ignore_index, loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
@@ -359,15 +361,15 @@ def linear_ce_backward(h, w, labels, lse, dloss, dh, dw, workspace, ignore_index
     T, D = h.shape
     V = w.shape[0]
     dev = h.device
-    _need("rfq_linear_ce_backward: h", h, (T, D), torch.bfloat16, dev)
-    _need("rfq_linear_ce_backward: w", w, (V, D), torch.bfloat16, dev)
-    _need("rfq_linear_ce_backward: labels", labels, (T,), torch.int64, dev)
-    _need("rfq_linear_ce_backward: lse", lse, (T,), torch.float32, dev)
-    _need("rfq_linear_ce_backward: dloss", dloss, (T,), torch.float32, dev)
+    _need("rfq_linear_ce_backward", "h", h, (T, D), torch.bfloat16, dev)
+    _need("rfq_linear_ce_backward", "w", w, (V, D), torch.bfloat16, dev)
+    _need("rfq_linear_ce_backward", "labels", labels, (T,), torch.int64, dev)
+    _need("rfq_linear_ce_backward", "lse", lse, (T,), torch.float32, dev)
+    _need("rfq_linear_ce_backward", "dloss", dloss, (T,), torch.float32, dev)
     if dh is not None:
-        _need("rfq_linear_ce_backward: dh", dh, (T, D), torch.bfloat16, dev)
+        _need("rfq_linear_ce_backward", "dh", dh, (T, D), torch.bfloat16, dev)
     if dw is not None:
-        _need("rfq_linear_ce_backward: dw", dw, (V, D), torch.bfloat16, dev)
+        _need("rfq_linear_ce_backward", "dw", dw, (V, D), torch.bfloat16, dev)
     _need_workspace("rfq_linear_ce_backward", workspace, dev)
     _call("rfq_linear_ce_backward", dev, stream, load_library().rfq_linear_ce_backward, h.data_ptr(), w.data_ptr(),
               labels.data_ptr(), lse.data_ptr(), dloss.data_ptr(), T, D, V, ignore_index, _ptr(dh), _ptr(dw),
@@ -391,21 +393,21 @@ def _lora_shapes(where, x, a, b, scale, ids, M, K):
     N = b.shape[1]
     dev = a.device
     if x is not None:
-        _need(f"{where}: x", x, (M, K), torch.bfloat16, dev)
-    _need(f"{where}: a", a, (n, r, K), torch.bfloat16, dev)
-    _need(f"{where}: b", b, (n, N, r), torch.bfloat16, dev)
-    _need(f"{where}: scale", scale, (n,), torch.float32, dev)
-    _need(f"{where}: ids", ids, (M,), torch.int32, dev)
+        _need(where, "x", x, (M, K), torch.bfloat16, dev)
+    _need(where, "a", a, (n, r, K), torch.bfloat16, dev)
+    _need(where, "b", b, (n, N, r), torch.bfloat16, dev)
+    _need(where, "scale", scale, (n,), torch.float32, dev)
+    _need(where, "ids", ids, (M,), torch.int32, dev)
     return n, r, N
 
 
-def _out_type(where, t):
+def _out_type(where, name, t):
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return OUT_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return OUT_F32
-    raise RFQError(1, f"{where}: want bfloat16 or float32, got {t.dtype}")
+    raise RFQError(1, f"{where}: {name}: want bfloat16 or float32, got {t.dtype}")
 
 
 def lora(x, a, b, scale, ids, y, workspace, base=None, hidden=None, stream=None):
@@ -416,12 +418,12 @@ def lora(x, a, b, scale, ids, y, workspace, base=None, hidden=None, stream=None)
     M, K = x.shape
     dev = x.device
     n, r, N = _lora_shapes("rfq_lora", x, a, b, scale, ids, M, K)
-    y_type = _out_type("rfq_lora: y", y)
-    _need("rfq_lora: y", y, (M, N), y.dtype, dev)
+    y_type = _out_type("rfq_lora", "y", y)
+    _need("rfq_lora", "y", y, (M, N), y.dtype, dev)
     if base is not None:
-        _need("rfq_lora: base", base, (M, N), y.dtype, dev)
+        _need("rfq_lora", "base", base, (M, N), y.dtype, dev)
     if hidden is not None:
-        _need("rfq_lora: hidden", hidden, (M, r), torch.float32, dev)
+        _need("rfq_lora", "hidden", hidden, (M, r), torch.float32, dev)
     _need_workspace("rfq_lora", workspace, dev)
     _call("rfq_lora", dev, stream, load_library().rfq_lora, x.data_ptr(), M, K, a.data_ptr(), b.data_ptr(),
               scale.data_ptr(), ids.data_ptr(), n, r, N, _ptr(base), y.data_ptr(), y_type, _ptr(hidden),
@@ -437,19 +439,19 @@ def lora_backward(x, a, b, scale, ids, dy, hidden, workspace, dx=None, dx_base=N
     dev = dy.device
     where = "rfq_lora_backward"
     n, r, N = _lora_shapes(where, x, a, b, scale, ids, M, K)
-    _need(f"{where}: dy", dy, (M, N), torch.bfloat16, a.device)
+    _need(where, "dy", dy, (M, N), torch.bfloat16, a.device)
     if hidden is not None:
-        _need(f"{where}: hidden", hidden, (M, r), torch.float32, dev)
+        _need(where, "hidden", hidden, (M, r), torch.float32, dev)
     dx_type = grad_type = OUT_F32
     if dx is not None:
-        dx_type = _out_type(f"{where}: dx", dx)
-        _need(f"{where}: dx", dx, (M, K), dx.dtype, dev)
+        dx_type = _out_type(where, "dx", dx)
+        _need(where, "dx", dx, (M, K), dx.dtype, dev)
         if dx_base is not None:
-            _need(f"{where}: dx_base", dx_base, (M, K), dx.dtype, dev)
+            _need(where, "dx_base", dx_base, (M, K), dx.dtype, dev)
     for name, t, shape in (("da", da, (n, r, K)), ("db", db, (n, N, r))):
         if t is not None:
-            grad_type = _out_type(f"{where}: {name}", t)
-            _need(f"{where}: {name}", t, shape, t.dtype if name == "da" or da is None else da.dtype, dev)
+            grad_type = _out_type(where, name, t)
+            _need(where, name, t, shape, t.dtype if name == "da" or da is None else da.dtype, dev)
     _need_workspace(where, workspace, dev)
     _call("rfq_lora_backward", dev, stream, load_library().rfq_lora_backward, _ptr(x), M, K, a.data_ptr(),
               b.data_ptr(), scale.data_ptr(), ids.data_ptr(), n, r, N, dy.data_ptr(), _ptr(hidden), _ptr(dx_base),
@@ -462,14 +464,14 @@ def linear_lora(x, qw_codes, qw_scales, N, a, b, scale, ids, y, workspace, use_r
     M, K = x.shape
     dev = x.device
     n, r, Nb = _lora_shapes("rfq_linear_lora", x, a, b, scale, ids, M, K)
-    y_type = _out_type("rfq_linear_lora: y", y)
-    _need("rfq_linear_lora: b", b, (n, N, r), torch.bfloat16, dev)
-    _need("rfq_linear_lora: y", y, (M, N), y.dtype, dev)
+    y_type = _out_type("rfq_linear_lora", "y", y)
+    _need("rfq_linear_lora", "b", b, (n, N, r), torch.bfloat16, dev)
+    _need("rfq_linear_lora", "y", y, (M, N), y.dtype, dev)
     for name, t, size in (("qw_codes", qw_codes, codes_bytes(N, K)), ("qw_scales", qw_scales, scales_bytes(N, K))):
         if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != dev or t.numel() < size:
             raise RFQError(1, f"rfq_linear_lora: {name} is a contiguous uint8 tensor of at least {size} bytes on {dev}")
     if hidden is not None:
-        _need("rfq_linear_lora: hidden", hidden, (M, r), torch.float32, dev)
+        _need("rfq_linear_lora", "hidden", hidden, (M, r), torch.float32, dev)
     _need_workspace("rfq_linear_lora", workspace, dev)
     _call("rfq_linear_lora", dev, stream, load_library().rfq_linear_lora, x.data_ptr(), M, K, qw_codes.data_ptr(),
               qw_scales.data_ptr(), N, a.data_ptr(), b.data_ptr(), scale.data_ptr(), ids.data_ptr(), n, r,
@@ -482,17 +484,21 @@ def grad_clip_workspace_bytes(count: int) -> int:
 
 
 def _tensor_list(where, tensors, device):
-    """Host arrays (addresses, element counts, types) of a list of contiguous bf16 / fp32 tensors on one device."""
+    """Addresses, element counts and types of a list of contiguous tensors on one device."""
     import torch
     T = torch.Tensor
-    code = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
-    try:
-        types = array.array("i", [code[t.dtype] for t in tensors])
-    except KeyError as e:
-        raise RFQError(1, f"{where}: want bfloat16 or float32 tensors, got {e.args[0]}") from None
     if not all(map(T.is_contiguous, tensors)) or not {device.index}.issuperset(map(T.get_device, tensors)):
         raise RFQError(1, f"{where}: want contiguous tensors on {device}")
-    return array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), types
+    return array.array("Q", list(map(T.data_ptr, tensors))), list(map(T.numel, tensors)), [t.dtype for t in tensors]
+
+
+def _type_codes(where, dtypes):
+    import torch
+    code = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+    try:
+        return array.array("i", [code[d] for d in dtypes])
+    except KeyError as e:
+        raise RFQError(1, f"{where}: want bfloat16 or float32 tensors, got {e.args[0]}") from None
 
 
 def _norm_args(where, grads, norm, workspace):
@@ -506,7 +512,8 @@ def _norm_args(where, grads, norm, workspace):
 def grad_norm(grads, norm, workspace, stream=None):
     """rfq_grad_norm: norm (one fp32 on the device) = the 2-norm over all elements of a list of bf16 / fp32 tensors."""
     grads = list(grads)
-    ptrs, numels, types = _norm_args("rfq_grad_norm", grads, norm, workspace)
+    ptrs, numels, dtypes = _norm_args("rfq_grad_norm", grads, norm, workspace)
+    numels, types = array.array("q", numels), _type_codes("rfq_grad_norm", dtypes)
     _call("rfq_grad_norm", norm.device, stream, load_library().rfq_grad_norm, ptrs.buffer_info()[0],
               numels.buffer_info()[0], types.buffer_info()[0], len(grads), norm.data_ptr(), workspace.data_ptr(),
               workspace.numel())
@@ -516,15 +523,16 @@ def grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None):
     """rfq_grad_clip: the list scaled by min(1, max_norm / (norm + 1e-6)), in place or into `outs`, and its norm
     before that (one fp32 on the device)."""
     grads = list(grads)
-    ptrs, numels, types = _norm_args("rfq_grad_clip", grads, norm, workspace)
+    ptrs, numels, dtypes = _norm_args("rfq_grad_clip", grads, norm, workspace)
     out_ptrs = None
     if outs is not None:
         outs = list(outs)
         if len(outs) != len(grads):
             raise RFQError(1, "rfq_grad_clip: one output for each gradient")
-        out_ptrs, out_numels, out_types = _tensor_list("rfq_grad_clip: outs", outs, norm.device)
-        if out_numels != numels or out_types != types:
+        out_ptrs, out_numels, out_dtypes = _tensor_list("rfq_grad_clip: outs", outs, norm.device)
+        if out_numels != numels or out_dtypes != dtypes:
             raise RFQError(1, "rfq_grad_clip: an output has the type and size of its gradient")
+    numels, types = array.array("q", numels), _type_codes("rfq_grad_clip", dtypes)
     _call("rfq_grad_clip", norm.device, stream, load_library().rfq_grad_clip, ptrs.buffer_info()[0], None if
               out_ptrs is None else out_ptrs.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0],
               len(grads), float(max_norm), norm.data_ptr(), workspace.data_ptr(), workspace.numel())
