@@ -293,6 +293,35 @@ def test_another_stream(rfq):
         assert all(torch.equal(a, b) for a, b in zip(base + grads, o))
 
 
+def test_offsets_past_32_bits(rfq):
+    """A head of more than 2^31 elements: the last entries of the vocabulary and the last rows of its gradient."""
+    T, D, V = 3, 2048, (1 << 20) + 1001
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    h = torch.randn((T, D), generator=g, device="cuda").bfloat16()
+    w = torch.empty((V, D), dtype=torch.bfloat16, device="cuda")
+    for part in w.split(1 << 16):
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda") * (1.5 / D ** 0.5))
+    labels = torch.tensor([V - 1, 5, V - 700], device="cuda")
+    dloss = torch.tensor([1.0, 0.5, 2.0], device="cuda")
+    z = torch.cat([h.double() @ part.double().T for part in w.split(1 << 16)], 1)
+    lse64 = torch.logsumexp(z, 1)
+    z_tol = 1e-5 * float((h.double().abs() @ w[-1000:].double().abs().T).max()) * 1.5
+    loss, lse = rfq.linear_ce_alloc(h, w, labels)
+    tol = z_tol + 1e-5 + 4 * 2.0 ** -24 * lse64.abs()
+    assert ((lse.double() - lse64).abs() <= tol).all()
+    assert ((loss.double() - (lse64 - z.gather(1, labels[:, None])[:, 0])).abs() <= tol + z_tol).all()
+    _, dw = rfq.linear_ce_backward_alloc(h, w, labels, lse, dloss, want_dh=False)
+    p = torch.exp(z[:, -1000:] - lse64[:, None])
+    onehot = torch.zeros_like(p)
+    onehot[0, 999] = 1.0
+    onehot[2, 300] = 1.0
+    gd = dloss.double()[:, None]
+    want = (gd * (p - onehot)).T @ h.double()
+    bound = (2.0 ** -8 + 2 * float(tol.max()) + 1e-5) * ((gd * (p + onehot)).T @ h.double().abs()) + 2.0 ** -8 * want.abs()
+    assert ((dw[-1000:].double() - want).abs() <= bound).all()
+
+
 def test_no_rows(rfq):
     h = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     w = torch.randn((100, 64), device="cuda").bfloat16()

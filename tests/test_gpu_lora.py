@@ -89,7 +89,9 @@ def run_all(rfq, c, out=BF16, grad=BF16, base=True):
 SHAPES = [(1, 8, 8, 8, 1, "one"), (1, 64, 40, 16, 3, "mixed"), (2, 136, 264, 24, 5, "mixed"), (15, 264, 8, 32, 2, "runs"),
           (16, 512, 520, 16, 16, "mixed"), (17, 72, 1032, 40, 4, "mixed"), (64, 1032, 256, 64, 1, "one"), (65, 256, 136, 128, 2, "runs"),
           (128, 200, 200, 8, 40, "mixed"), (129, 520, 72, 72, 3, "runs"), (300, 264, 312, 16, 200, "mixed"), (300, 264, 312, 128, 2, "mixed"),
-          (700, 384, 1000, 56, 3, "runs"), (1000, 128, 136, 8, 6, "mixed"), (2500, 64, 72, 16, 4, "runs"), (5000, 40, 136, 32, 300, "mixed")]
+          (700, 384, 1000, 56, 3, "runs"), (1000, 128, 136, 8, 6, "mixed"), (2500, 64, 72, 16, 4, "runs"), (5000, 40, 136, 32, 300, "mixed"),
+          (200, 8, 8, 8, 1, "one"), (200, 16, 24, 128, 1, "one"), (140, 72, 8, 40, 2, "mixed"), (257, 2056, 64, 24, 40, "runs"),
+          (1500, 1032, 264, 104, 40, "mixed"), (33, 200, 136, 120, 4, "mixed")]
 
 
 @pytest.mark.parametrize("M,K,N,r,n,kind", SHAPES)
@@ -275,6 +277,32 @@ def test_another_stream(rfq):
     got = rfq.lora_alloc(c["x"], c["a"], c["b"], c["scale"], c["ids"], base=c["base"], stream=side)
     side.synchronize()
     assert torch.equal(base, got)
+
+
+def test_offsets_past_32_bits(rfq):
+    """More than 2^31 elements of base and output: the last rows are those of a small call on them."""
+    M, K, N, r, n = 66000, 64, 32776, 8, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    c = make(300, K, N, r, n, "runs", seed=23)
+    x = torch.zeros((M, K), dtype=BF16, device="cuda")
+    base = torch.zeros((M, N), dtype=BF16, device="cuda")
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    x[-300:], base[-300:], ids[-300:] = c["x"], c["base"], c["ids"]
+    y = rfq.lora_alloc(x, c["a"], c["b"], c["scale"], ids, base=base)
+    want = reference(c)
+    check("y", y[-300:], want["y"])
+    assert not y[:-300].any()
+    # the same through the gradients: dy is the wide one
+    hidden = torch.zeros((M, r), device="cuda")
+    hidden[-300:] = rfq.lora_alloc(c["x"], c["a"], c["b"], c["scale"], c["ids"], want_hidden=True)[1]
+    base.zero_()
+    base[-300:] = c["dy"]
+    dx, da, db = rfq.lora_backward_alloc(x, c["a"], c["b"], c["scale"], ids, base, hidden)
+    want = reference(c, base=False)
+    check("dx", dx[-300:], want["dx"])
+    check("da", da, want["da"])
+    check("db", db, want["db"])
 
 
 def test_no_rows(rfq):
