@@ -23,18 +23,18 @@
 // Long batches take the shrink and expand of rfq_lora_wide.cu (tcgen05, 128 neighbouring
 // rows).  Here are those of short batches, where rows have adapters of their own and time goes
 // into reading the adapters' weights, and the adapters' gradients; all on warp-level m16n8k16
-// MMAs.  The rows of a 128-row chunk are grouped by adapter inside the CTA that works on them (no
+// MMAs.  The rows of a 256-row chunk are grouped by adapter inside the CTA that works on them (no
 // host knowledge of the ids, no order asked of them): groups of up to 16 rows share an
 // adapter's weights.
 //
-// Weights that run along the contraction (A in shrink, B in expand: the forward pass) go from
-// global memory straight into MMA fragments, each used by one warp once: a thread's fragment
-// takes any four contraction elements of its row as long as the other operand takes the
-// same, so it loads neighbouring ones, 8 or 16 bytes at a time.  Weights that run across it (the
-// backward pass) and the gradients' operands go through shared memory with 16-byte
-// asynchronous copies and are transposed on the way out (ldmatrix).  Each thread keeps the
-// addresses of the pieces it copies and steps them along: with the addresses formed anew for
-// each copy the kernels issued 1600 instructions a warp for 8 KiB and ran at 1.9 TB/s; with one
+// Going forward the weights run along the contraction (A in shrink, B in expand) and go from global
+// memory straight into MMA fragments, each used by one warp once: a thread's fragment takes any
+// four contraction elements of its row as long as the other operand takes the same, so it
+// loads neighbouring ones, 8 or 16 bytes at a time.  Both products are one launch.
+// Going back they run across it: they, and the operands of the gradients, go through shared memory
+// with 16-byte asynchronous copies and are transposed on the way out (ldmatrix).  Each thread
+// keeps the addresses of the pieces it copies and steps them along: with the addresses formed anew
+// for each copy the kernels issued 1600 instructions a warp for 8 KiB and ran at 1.9 TB/s; with one
 // bulk copy for each 256-byte row piece they were slower still (about 65 ns a copy and SM).
 //
 // No atomics: a result does not depend on timing.
@@ -143,7 +143,7 @@ __device__ void group_rows(Groups& g, const int* ids, int64_t row0, int64_t M, i
   __syncthreads();
   // Rows already in order (neighbours of one request, one adapter for all) need no sorting.
   if (!__syncthreads_and(t == 0 || t >= count || g.keys[t - 1] < key)) {
-    for (int k = 2; k <= kChunk; k <<= 1)
+    for (int k = 2; k < 2 * count; k <<= 1)    // rows past the last are in place
       for (int j = k >> 1; j > 0; j >>= 1) {   // a bitonic sort, through shuffles below 32
         int other;
         if (j < 32) {
@@ -200,11 +200,10 @@ __device__ __forceinline__ void take_groups(Groups& g, const int* table) {
 }
 
 // ---------------------------------------------------------------- shrink
-// part[split][m][j] = sum over the split's k of src[m][k] P_a[j][k], P = A (rows j, k along the
-// row; the direct kernel) or B^T (rows k, j along the row).
+// ds of short batches: part[split][m][j] = sum over the split's k of src[m][k] B_a[k][j].
 struct ShrinkParams {
   const __nv_bfloat16* src;   // [M][C]
-  const __nv_bfloat16* p;     // [n][r][C] (direct) or [n][C][r]
+  const __nv_bfloat16* p;     // [n][C][r]
   const int* ids;
   float* part;                // [splits][M][r]
   int64_t M, C, c_split;      // c_split: contraction elements of one split (a multiple of kBK)
@@ -368,97 +367,6 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
   }
 }
 
-// The forward shrink: P = A, whose rows run along the contraction.  Each warp takes 32 elements of
-// it at a time: lane (g, q) loads elements 8 q .. 8 q + 7 of row g of the adapter (for each
-// eight of the rank) and of the rows g and g + 8 of src; the halves of these 16 bytes are the
-// fragments of two MMAs.
-template <int kJ>   // 8-column tiles of the rank, at most
-__global__ void __launch_bounds__(kThreads) rfq_lora_shrink_direct_kernel(const ShrinkParams p) {
-  __shared__ __align__(16) Groups g;
-  __shared__ float red[4][16][kJ * 8];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
-  const int z = static_cast<int>(blockIdx.x % p.zs);
-  group_rows(g, p.ids, row0, p.M, p.n);
-  if (z == 0 && blockIdx.y == 0) leave_groups(g, p.table + (blockIdx.x / p.zs) * kTable);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int jt = p.r / 8, quad = lane & 3, line = lane >> 2;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * p.c_split;
-  const int64_t c1 = min(p.C, c0 + p.c_split);
-  for (int item = z; item < g.items; item += p.zs) {
-    const int first = g.start[item], rows = g.start[item + 1] - first;
-    const int a = g.ids[g.order[first]];
-    if (a == INT_MAX) break;   // rows without an adapter come last
-    const bool has_a = line < rows, has_b = line + 8 < rows;
-    const int64_t row_a = row0 + g.order[first + (has_a ? line : 0)], row_b = row0 + g.order[first + (has_b ? line + 8 : 0)];
-    const __nv_bfloat16* xa = p.src + row_a * p.C;
-    const __nv_bfloat16* xb = p.src + row_b * p.C;
-    const __nv_bfloat16* pa = p.p + (static_cast<int64_t>(a) * p.r + line) * p.C;
-    float acc[kJ][4];
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-#pragma unroll 2
-    for (int64_t c = c0 + 32 * warp + 8 * quad; c < c1 + 8 * quad; c += 8 * 32) {
-      const bool ok = c < c1;
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      const uint4 ua = ok && has_a ? *reinterpret_cast<const uint4*>(xa + c) : zero;
-      const uint4 ub = ok && has_b ? *reinterpret_cast<const uint4*>(xb + c) : zero;
-      const uint32_t f0[4] = {ua.x, ub.x, ua.y, ub.y}, f1[4] = {ua.z, ub.z, ua.w, ub.w};
-      uint4 w[kJ];
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) w[j] = ok && j < jt ? *reinterpret_cast<const uint4*>(pa + 8 * j * p.C + c) : zero;
-#pragma unroll
-      for (int j = 0; j < kJ; ++j)
-        if (j < jt) {
-          mma16816(acc[j], f0, w[j].x, w[j].y);
-          mma16816(acc[j], f1, w[j].z, w[j].w);
-        }
-    }
-    // Join the warps, four and four, then the others to the first, which writes [rows][r].
-    auto give = [&](int slot) {
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const int col = j * 8 + 2 * quad;
-        *reinterpret_cast<float2*>(&red[slot][line][col]) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(&red[slot][line + 8][col]) = make_float2(acc[j][2], acc[j][3]);
-      }
-    };
-    auto take = [&](int slot) {
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const int col = j * 8 + 2 * quad;
-        const float2 ua = *reinterpret_cast<const float2*>(&red[slot][line][col]);
-        const float2 ub = *reinterpret_cast<const float2*>(&red[slot][line + 8][col]);
-        acc[j][0] += ua.x;
-        acc[j][1] += ua.y;
-        acc[j][2] += ub.x;
-        acc[j][3] += ub.y;
-      }
-    };
-    if (warp >= 4) give(warp - 4);
-    __syncthreads();
-    if (warp < 4) take(warp);
-    __syncthreads();
-    if (warp > 0 && warp < 4) give(warp);
-    __syncthreads();
-    if (warp == 0) {
-      for (int w = 1; w < 4; ++w) take(w);
-      float* out = p.part + static_cast<int64_t>(blockIdx.y) * p.M * p.r;
-#pragma unroll
-      for (int j = 0; j < kJ; ++j)
-        if (j < jt) {
-          const int col = j * 8 + 2 * quad;
-          if (has_a) *reinterpret_cast<float2*>(out + row_a * p.r + col) = make_float2(acc[j][0], acc[j][1]);
-          if (has_b) *reinterpret_cast<float2*>(out + row_b * p.r + col) = make_float2(acc[j][2], acc[j][3]);
-        }
-    }
-    __syncthreads();
-  }
-}
-
 // s'[m][j] = scale_a * sum of the splits, in order.
 __device__ __forceinline__ float join_parts(const float* part, int splits, int64_t stride, int64_t at, float scale) {
   float v = part[at];
@@ -477,20 +385,19 @@ __device__ __forceinline__ void split_terms(float v, __nv_bfloat16 (&t)[kT]) {
 }
 
 // ---------------------------------------------------------------- expand
-// out[m][c] = base[m][c] + sum_j s'[m][j] Q_a, Q = B (rows c, j along the row; the direct kernel)
-// or A^T (rows j, c along the row).  There a stage holds a [kRows][kBN] tile of the base and the adapter's
-// weights for its columns; the sum is formed in place and copied out from there, in whole row pieces.
+// dx of short batches: out[m][c] = base[m][c] + sum_j ds'[m][j] A_a[j][c].  A stage holds a [kRows][kBN]
+// tile of the base and the adapter's weights for its columns; the sum is formed in place and copied
+// out from there, in whole row pieces.
 struct ExpandParams {
   const float* part;          // [splits][M][r]
   const float* scale;         // [n]
-  const __nv_bfloat16* q;     // [n][C][r] (direct) or [n][r][C]
+  const __nv_bfloat16* q;     // [n][r][C]
   const int* table;           // [chunks][kTable], from shrink
   const void* base;           // [M][C] or nullptr
   void* out;                  // [M][C]
-  float* hidden;              // [M][r] or nullptr
   int64_t M, C;
   int n, r, splits, zs;
-  int tiles;                  // column tiles of one CTA (of 32 columns in the direct kernel)
+  int tiles;                  // column tiles of one CTA
   int stages;
 };
 
@@ -548,8 +455,6 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
     const int first = g.start[item], rows = g.start[item + 1] - first;
     const int a = g.ids[g.order[first]];
     const bool with = a != INT_MAX;
-    if (p.hidden != nullptr && blockIdx.y == 0 && !with)
-      for (int i = tid; i < rows * p.r; i += kThreads) p.hidden[(row0 + g.order[first + i / p.r]) * p.r + i % p.r] = 0.f;
     // Rows without an adapter (they come last) keep what they have where the base is the output itself.
     if (!with && p.base == p.out) continue;
     int64_t at[kCopies];        // byte offset of this thread's pieces, in the base and in the output
@@ -593,7 +498,6 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
         const int m = i / p.r, j = i - m * p.r;
         const int64_t sat = (row0 + g.order[first + m]) * p.r + j;
         const float v = join_parts(p.part, p.splits, p.M * p.r, sat, scale);
-        if (p.hidden != nullptr && blockIdx.y == 0) p.hidden[sat] = v;
         __nv_bfloat16 t[kT];
         split_terms<kT>(v, t);
 #pragma unroll
@@ -686,162 +590,247 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
   }
 }
 
-// The forward expand: Q = B, whose rows run along the rank.  A warp takes 32 columns at a time as
-// four 8-column tiles whose columns are interleaved, so that lane (g, q) ends up with columns
-// 8 q .. 8 q + 7 of the rows g and g + 8: 16 bytes of bf16.
-template <bool kF32>
-__global__ void __launch_bounds__(kThreads) rfq_lora_expand_direct_kernel(const ExpandParams p) {
-  constexpr int kT = kExpandTerms<kF32>;
+// ---------------------------------------------------------------- forward
+// Both products of the forward pass in one launch: a cluster of CTAs takes an item, its ranks the
+// contraction of shrink by ranges, exchange their sums through distributed shared memory, and take
+// the columns of expand by ranges.  (Asking for the weights' way to L2 ahead of time made it slower, 29.6
+// against 26.6 us for 256 rows of 48 adapters: the loads of 16 warps an SM keep memory as busy.)
+//
+// shrink: each warp takes 32 elements of the contraction at a time: lane (g, q) loads elements
+// 8 q .. 8 q + 7 of row g of the adapter (for each eight of the rank) and of the item's rows g and
+// g + 8; the halves of these 16 bytes are the fragments of two MMAs.
+// expand: a warp takes 32 columns at a time as four 8-column tiles whose columns are interleaved,
+// so that lane (g, q) ends up with columns 8 q .. 8 q + 7 of the rows g and g + 8: 16 bytes of bf16.
+struct ForwardParams {
+  const __nv_bfloat16* x;     // [M][K]
+  const __nv_bfloat16* a;     // [n][r][K]
+  const __nv_bfloat16* b;     // [n][N][r]
+  const float* scale;         // [n]
+  const int* ids;
+  const void* base;           // [M][N] or nullptr
+  void* out;                  // [M][N]
+  float* hidden;              // [M][r] or nullptr
+  int64_t M, K, N;
+  int n, r, zs;               // zs: clusters (or groups of `parts`) that share the items of one chunk
+  int cluster, parts;         // parts: clusters that share the columns of one item, each with all of its shrink
+};
+
+template <int kJ, bool kF32>   // kJ: 8-column tiles of the rank, at most
+__global__ void __launch_bounds__(kThreads, kJ <= 8 ? 2 : 1) rfq_lora_forward_kernel(const ForwardParams p) {
+  constexpr int kT = kF32 ? 3 : 1;   // bf16 terms of s, see rfq_lora_expand_kernel
+  constexpr int kSmRow = kJ * 8 + 8;
+  constexpr int kRedBytes = 4 * kRows * kJ * 8 * 4, kSmBytes = kT * kRows * kSmRow * 2;
   __shared__ __align__(16) Groups g;
-  __shared__ __align__(16) __nv_bfloat16 sm[kT][kRows][RFQ_LORA_MAX_RANK + 8];
+  __shared__ __align__(16) float sums[kRows * kJ * 8];
+  __shared__ __align__(16) uint8_t pool[kRedBytes > kSmBytes ? kRedBytes : kSmBytes];
+  float (*red)[kRows][kJ * 8] = reinterpret_cast<float (*)[kRows][kJ * 8]>(pool);              // shrink: [4]
+  __nv_bfloat16 (*sm)[kRows][kSmRow] = reinterpret_cast<__nv_bfloat16 (*)[kRows][kSmRow]>(pool);   // expand: [kT]
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.zs) * kChunk;
-  const int z = static_cast<int>(blockIdx.x % p.zs);
-  take_groups(g, p.table + (blockIdx.x / p.zs) * kTable);
+  const int rank = static_cast<int>(cluster_cta_rank());
+  const int64_t cluster = blockIdx.x / p.cluster;
+  const int part = static_cast<int>(cluster % p.parts);
+  const int64_t row0 = cluster / p.parts / p.zs * kChunk;
+  const int z = static_cast<int>(cluster / p.parts % p.zs);
+  group_rows(g, p.ids, row0, p.M, p.n);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3, line = lane >> 2;
-  const int64_t begin = static_cast<int64_t>(blockIdx.y) * p.tiles * 32;
-  const int64_t end = min(p.C, begin + static_cast<int64_t>(p.tiles) * 32);
-  for (int item = z; item < g.items; item += p.zs) {
+  const int jt = p.r / 8;
+  // This rank's part of the contraction (of 32 elements a step) and of the columns (of 32).
+  const int64_t k_per = ceil_div(ceil_div(p.K, 32), p.cluster) * 32, k0 = rank * k_per, k1 = min(p.K, k0 + k_per);
+  const int64_t n_per = ceil_div(ceil_div(p.N, 32), p.cluster * p.parts) * 32, begin = (part * p.cluster + rank) * n_per,
+                end = min(p.N, begin + n_per);
+  const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+
+  for (int item = z; item < g.items; item += p.zs) {   // the same items in every rank
     const int first = g.start[item], rows = g.start[item + 1] - first;
     const int a = g.ids[g.order[first]];
     const bool with = a != INT_MAX;
-    if (p.hidden != nullptr && blockIdx.y == 0 && !with)
+    if (p.hidden != nullptr && rank + part == 0 && !with)
       for (int i = tid; i < rows * p.r; i += kThreads) p.hidden[(row0 + g.order[first + i / p.r]) * p.r + i % p.r] = 0.f;
     // Rows without an adapter (they come last) keep what they have where the base is the output itself.
     if (!with && p.base == p.out) continue;
-    if (with) {
-      const float scale = p.scale[a];
-      for (int i = tid; i < rows * p.r; i += kThreads) {
-        const int m = i / p.r, j = i - m * p.r;
-        const int64_t at = (row0 + g.order[first + m]) * p.r + j;
-        const float v = join_parts(p.part, p.splits, p.M * p.r, at, scale);
-        if (p.hidden != nullptr && blockIdx.y == 0) p.hidden[at] = v;
-        __nv_bfloat16 t[kT];
-        split_terms<kT>(v, t);
-#pragma unroll
-        for (int e = 0; e < kT; ++e) sm[e][m][j] = t[e];
-      }
-      __syncthreads();
-    }
     const bool has[2] = {line < rows, line + 8 < rows};
     const int64_t row[2] = {row0 + g.order[first + (has[0] ? line : 0)], row0 + g.order[first + (has[1] ? line + 8 : 0)]};
-    // Column of this lane's fragment row in tile i: 8 (g / 2) + 2 i + (g & 1).
-    const __nv_bfloat16* qa = with ? p.q + (static_cast<int64_t>(a) * p.C + 8 * (line >> 1) + (line & 1)) * p.r : p.q;
-    // The loads of a block (32 columns x 32 of the rank) are under way while the one before is
-    // multiplied; the base comes with the first block of its columns.
-    const int blocks = (p.r + 31) / 32;
+    // Column of this lane's fragment row in tile i of expand: 8 (g / 2) + 2 i + (g & 1).
+    const __nv_bfloat16* qa = with ? p.b + (static_cast<int64_t>(a) * p.N + 8 * (line >> 1) + (line & 1)) * p.r : p.b;
+    if (with) {
+      float acc[kJ][4];
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+      const __nv_bfloat16* xa = p.x + row[0] * p.K;
+      const __nv_bfloat16* xb = p.x + row[1] * p.K;
+      const __nv_bfloat16* pa = p.a + (static_cast<int64_t>(a) * p.r + line) * p.K;
+#pragma unroll(kJ <= 4 ? 2 : 1)
+      for (int64_t c = k0 + 32 * warp + 8 * quad; c < k1 + 8 * quad; c += 8 * 32) {
+        const bool ok = c < k1;
+        const uint4 ua = ok && has[0] ? *reinterpret_cast<const uint4*>(xa + c) : zero4;
+        const uint4 ub = ok && has[1] ? *reinterpret_cast<const uint4*>(xb + c) : zero4;
+        const uint32_t f0[4] = {ua.x, ub.x, ua.y, ub.y}, f1[4] = {ua.z, ub.z, ua.w, ub.w};
+        uint4 w[kJ];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) w[j] = ok && j < jt ? *reinterpret_cast<const uint4*>(pa + 8 * j * p.K + c) : zero4;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+          if (j < jt) {
+            mma16816(acc[j], f0, w[j].x, w[j].y);
+            mma16816(acc[j], f1, w[j].z, w[j].w);
+          }
+      }
+      // The warps' sums: four and four, then the others to the first.
+      auto give = [&](int slot) {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const int col = j * 8 + 2 * quad;
+          *reinterpret_cast<float2*>(&red[slot][line][col]) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(&red[slot][line + 8][col]) = make_float2(acc[j][2], acc[j][3]);
+        }
+      };
+      auto take = [&](int slot) {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const int col = j * 8 + 2 * quad;
+          const float2 ua = *reinterpret_cast<const float2*>(&red[slot][line][col]);
+          const float2 ub = *reinterpret_cast<const float2*>(&red[slot][line + 8][col]);
+          acc[j][0] += ua.x;
+          acc[j][1] += ua.y;
+          acc[j][2] += ub.x;
+          acc[j][3] += ub.y;
+        }
+      };
+      if (warp >= 4) give(warp - 4);
+      __syncthreads();
+      if (warp < 4) take(warp);
+      __syncthreads();
+      if (warp > 0 && warp < 4) give(warp);
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = 1; w < 4; ++w) take(w);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const int col = j * 8 + 2 * quad;
+          *reinterpret_cast<float2*>(&sums[line * kJ * 8 + col]) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(&sums[(line + 8) * kJ * 8 + col]) = make_float2(acc[j][2], acc[j][3]);
+        }
+      }
+      cluster_sync();   // every rank's sums are there
+      const float scale = p.scale[a];
+      const uint32_t sums_addr = smem_addr(sums);
+      for (int i = tid; i < rows * p.r / 4; i += kThreads) {
+        const int m = i / (p.r / 4), j = (i - m * (p.r / 4)) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < p.cluster; ++k) {
+          const float4 u = ld_shared_cluster_f32x4(map_to_cta(sums_addr + (m * kJ * 8 + j) * 4, k));
+          v.x += u.x;
+          v.y += u.y;
+          v.z += u.z;
+          v.w += u.w;
+        }
+        const float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+        if (p.hidden != nullptr && rank + part == 0) *reinterpret_cast<float4*>(p.hidden + (row0 + g.order[first + m]) * p.r + j) = make_float4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          __nv_bfloat16 t[kT];
+          split_terms<kT>(f[e4], t);
+#pragma unroll
+          for (int e = 0; e < kT; ++e) sm[e][m][j + e4] = t[e];
+        }
+      }
+      __syncthreads();
+      cluster_arrive();   // this CTA is done with the others' sums; waited for before its own change
+    }
+
+    // All loads of 32 columns, then their MMAs.
+    constexpr int kK = kJ / 2;             // steps of 16 along the rank, at most
     constexpr int kRaw = kF32 ? 2 : 1;
-    struct Block {
-      uint2 w[2][4];
-      uint4 b[2][kRaw];
-    };
-    const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
-    auto load = [&](int64_t c, int kb, Block& d) {
-      const int64_t col = c + 8 * quad;
-      if (kb == 0) {
+    const int whole = p.r / 16;
+    const bool half = (p.r & 8) != 0;
+    const __nv_bfloat16* q0 = qa + (begin + 32 * warp) * p.r + 4 * quad;
+    int64_t at[2] = {(row[0] * p.N + begin + 32 * warp + 8 * quad) * (kF32 ? 4 : 2), (row[1] * p.N + begin + 32 * warp + 8 * quad) * (kF32 ? 4 : 2)};
+    for (int64_t c = begin + 32 * warp; c < end; c += 8 * 32) {
+      const bool full = c + 32 <= p.N;       // else the last columns, some of them missing
+      const bool col_ok = full || c + 8 * quad < p.N;
+      uint4 raw[2][kRaw];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool ok = p.base != nullptr && has[h] && col < p.C;
-          const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.base) + (row[h] * p.C + col) * (kF32 ? 4 : 2));
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < kRaw; ++e) d.b[h][e] = ok ? b[e] : zero4;
-        }
-      }
-      if (!with) return;
+        for (int e = 0; e < kRaw; ++e)
+          raw[h][e] = p.base != nullptr && has[h] && col_ok ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.base) + at[h] + 16 * e) : zero4;
+      float acc[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool ok = c + 8 * (line >> 1) + 2 * i + (line & 1) < p.C;
-        const __nv_bfloat16* q = qa + (c + 2 * i) * p.r + 32 * kb;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int k = 32 * kb + 16 * s;   // sixteen of the rank, or its last eight
-          const bool whole = k + 16 <= p.r;
-          d.w[s][i] = ok && whole ? *reinterpret_cast<const uint2*>(q + 16 * s + 4 * quad) : make_uint2(0u, 0u);
-          if (ok && !whole && k < p.r) d.w[s][i].x = *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * quad);
-        }
-      }
-    };
-    int64_t c = begin + 32 * warp;
-    int kb = 0;
-    Block next;
-    if (c < end) load(c, 0, next);
-    float acc[4][4];
-    uint4 held[2][kRaw];
-    while (c < end) {
-      const Block now = next;
-      int64_t c2 = c;
-      int kb2 = kb + 1;
-      if (kb2 == blocks) {
-        kb2 = 0;
-        c2 += 8 * 32;
-      }
-      if (c2 < end) load(c2, kb2, next);
-      if (kb == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < kRaw; ++e) held[h][e] = now.b[h][e];
-      }
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
       if (with) {
+        uint2 w[kK][4];
+        const __nv_bfloat16* q = q0;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int k = 32 * kb + 16 * s;
-          if (k + 16 <= p.r) {
+        for (int i = 0; i < 4; ++i) {
+          const bool ok = full || c + 8 * (line >> 1) + 2 * i + (line & 1) < p.N;
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            w[k][i] = make_uint2(0u, 0u);
+            if (k < whole) {
+              if (ok) w[k][i] = *reinterpret_cast<const uint2*>(q + 16 * k);
+            } else if (k == whole && half) {   // the last eight of the rank
+              if (ok) w[k][i].x = *reinterpret_cast<const uint32_t*>(q + 16 * k - 2 * quad);
+            }
+          }
+          q += 2 * p.r;
+        }
+        q0 += 8 * 32 * p.r;
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          if (k < whole) {
 #pragma unroll
             for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
-              const uint2 sa = *reinterpret_cast<const uint2*>(&sm[e][line][k + 4 * quad]);
-              const uint2 sb = *reinterpret_cast<const uint2*>(&sm[e][line + 8][k + 4 * quad]);
+              const uint2 sa = *reinterpret_cast<const uint2*>(&sm[e][line][16 * k + 4 * quad]);
+              const uint2 sb = *reinterpret_cast<const uint2*>(&sm[e][line + 8][16 * k + 4 * quad]);
               const uint32_t fa[4] = {sa.x, sb.x, sa.y, sb.y};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma16816(acc[i], fa, now.w[s][i].x, now.w[s][i].y);
+              for (int i = 0; i < 4; ++i) mma16816(acc[i], fa, w[k][i].x, w[k][i].y);
             }
-          } else if (k < p.r) {
+          } else if (k == whole && half) {
 #pragma unroll
             for (int e = kT - 1; e >= 0; --e) {
-              const uint32_t fa[2] = {*reinterpret_cast<const uint32_t*>(&sm[e][line][k + 2 * quad]),
-                                      *reinterpret_cast<const uint32_t*>(&sm[e][line + 8][k + 2 * quad])};
+              const uint32_t fa[2] = {*reinterpret_cast<const uint32_t*>(&sm[e][line][16 * k + 2 * quad]),
+                                      *reinterpret_cast<const uint32_t*>(&sm[e][line + 8][16 * k + 2 * quad])};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma1688(acc[i], fa, now.w[s][i].x);
+              for (int i = 0; i < 4; ++i) mma1688(acc[i], fa, w[k][i].x);
             }
           }
         }
       }
-      if (kb2 == 0) {   // the columns' last block
-        const int64_t col = c + 8 * quad;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!has[h] || col >= p.C) continue;
-          uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (row[h] * p.C + col) * (kF32 ? 4 : 2));
-          if constexpr (kF32) {
+      for (int h = 0; h < 2; ++h) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at[h]);
+        at[h] += 8 * 32 * (kF32 ? 4 : 2);
+        if (!has[h] || !col_ok) continue;
+        if constexpr (kF32) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint4 u = held[h][e];
-              o[e] = make_uint4(__float_as_uint(__uint_as_float(u.x) + acc[2 * e][2 * h]), __float_as_uint(__uint_as_float(u.y) + acc[2 * e][2 * h + 1]),
-                                __float_as_uint(__uint_as_float(u.z) + acc[2 * e + 1][2 * h]),
-                                __float_as_uint(__uint_as_float(u.w) + acc[2 * e + 1][2 * h + 1]));
-            }
-          } else {
-            const uint32_t u[4] = {held[h][0].x, held[h][0].y, held[h][0].z, held[h][0].w};
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(u[i] << 16) + acc[i][2 * h],
-                                                             __uint_as_float(u[i] & 0xffff0000u) + acc[i][2 * h + 1]);
-              w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            *o = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 2; ++e) {
+            const uint4 u = raw[h][e];
+            o[e] = make_uint4(__float_as_uint(__uint_as_float(u.x) + acc[2 * e][2 * h]), __float_as_uint(__uint_as_float(u.y) + acc[2 * e][2 * h + 1]),
+                              __float_as_uint(__uint_as_float(u.z) + acc[2 * e + 1][2 * h]),
+                              __float_as_uint(__uint_as_float(u.w) + acc[2 * e + 1][2 * h + 1]));
           }
+        } else {
+          const uint32_t u[4] = {raw[h][0].x, raw[h][0].y, raw[h][0].z, raw[h][0].w};
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(u[i] << 16) + acc[i][2 * h],
+                                                           __uint_as_float(u[i] & 0xffff0000u) + acc[i][2 * h + 1]);
+            v[i] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          *o = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
-      c = c2;
-      kb = kb2;
     }
-    __syncthreads();   // the next group's s' goes where this one's was
+    __syncthreads();          // the next item's sums go where this one's terms were
+    if (with) cluster_wait();
   }
 }
 
@@ -1241,7 +1230,7 @@ int shrink_splits(int64_t M, int64_t C, int64_t n, int64_t* c_split, int* zs) {
   return static_cast<int>(ceil_div(C, *c_split));
 }
 
-cudaError_t shrink(const void* src, const void* w, bool trans, const int* ids, int* table, float* part, int64_t M, int64_t C, int64_t n, int64_t r,
+cudaError_t shrink(const void* src, const void* w, const int* ids, int* table, float* part, int64_t M, int64_t C, int64_t n, int64_t r,
                    int* splits, cudaStream_t stream) {
   ShrinkParams p = {};
   p.src = static_cast<const __nv_bfloat16*>(src);
@@ -1255,12 +1244,6 @@ cudaError_t shrink(const void* src, const void* w, bool trans, const int* ids, i
   p.r = static_cast<int>(r);
   *splits = shrink_splits(M, C, n, &p.c_split, &p.zs);
   const dim3 grid(static_cast<unsigned>(ceil_div(M, kChunk) * p.zs), static_cast<unsigned>(*splits));
-  if (!trans) {
-    if (r <= 16) return launch(rfq_lora_shrink_direct_kernel<2>, p, grid, 0, stream);
-    if (r <= 32) return launch(rfq_lora_shrink_direct_kernel<4>, p, grid, 0, stream);
-    if (r <= 64) return launch(rfq_lora_shrink_direct_kernel<8>, p, grid, 0, stream);
-    return launch(rfq_lora_shrink_direct_kernel<16>, p, grid, 0, stream);
-  }
   const int stage = kRows * kRowStride + shrink_p_bytes(p.r), red = shrink_red_bytes(p.r);
   p.stages = ring_stages(stage, red + static_cast<int>(sizeof(Groups)));
   const size_t smem = static_cast<size_t>(p.stages) * stage + red;
@@ -1271,26 +1254,23 @@ cudaError_t shrink(const void* src, const void* w, bool trans, const int* ids, i
 }
 
 template <bool kF32>
-cudaError_t expand_typed(ExpandParams p, bool trans, cudaStream_t stream) {
+cudaError_t expand_typed(ExpandParams p, cudaStream_t stream) {
   const int64_t chunks = ceil_div(p.M, kChunk), z = chunk_ctas(p.M, p.n, 2 * kPlanSms);
   p.zs = static_cast<int>(z);
-  // Column tiles of a CTA: one wave of CTAs, three per SM for the direct kernel (and a tile a warp at
-  // least), two for the other.
-  const int64_t tiles = ceil_div(p.C, trans ? kBN<kF32> : 32);
-  int64_t parts = (trans ? 2 : 3) * kPlanSms / (chunks * z);
-  if (!trans && parts > ceil_div(tiles, 8)) parts = ceil_div(tiles, 8);
+  // Column tiles of a CTA: one wave of two CTAs per SM.
+  const int64_t tiles = ceil_div(p.C, kBN<kF32>);
+  int64_t parts = 2 * kPlanSms / (chunks * z);
   if (parts > tiles) parts = tiles;
   if (parts < 1) parts = 1;
   p.tiles = static_cast<int>(ceil_div(tiles, parts));
   const dim3 grid(static_cast<unsigned>(chunks * z), static_cast<unsigned>(ceil_div(tiles, p.tiles)));
-  if (!trans) return launch(rfq_lora_expand_direct_kernel<kF32>, p, grid, 0, stream);
   const int stage = expand_stage_bytes<kF32>(p.r), other = expand_s_bytes<kF32>(p.r);
   p.stages = ring_stages(stage, other + static_cast<int>(sizeof(Groups)));
   return launch(rfq_lora_expand_kernel<kF32>, p, grid, static_cast<size_t>(p.stages) * stage + other, stream);
 }
 
-cudaError_t expand(const float* part, int splits, const float* scale, const void* w, bool trans, const int* table, const void* base,
-                   void* out, bool f32, float* hidden, int64_t M, int64_t C, int64_t n, int64_t r, cudaStream_t stream) {
+cudaError_t expand(const float* part, int splits, const float* scale, const void* w, const int* table, const void* base, void* out,
+                   bool f32, int64_t M, int64_t C, int64_t n, int64_t r, cudaStream_t stream) {
   ExpandParams p = {};
   p.part = part;
   p.scale = scale;
@@ -1298,13 +1278,34 @@ cudaError_t expand(const float* part, int splits, const float* scale, const void
   p.table = table;
   p.base = base;
   p.out = out;
-  p.hidden = hidden;
   p.M = M;
   p.C = C;
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
   p.splits = splits;
-  return f32 ? expand_typed<true>(p, trans, stream) : expand_typed<false>(p, trans, stream);
+  return f32 ? expand_typed<true>(p, stream) : expand_typed<false>(p, stream);
+}
+
+template <bool kF32>
+cudaError_t forward_typed(const ForwardParams& p, int64_t clusters, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * p.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see griddep_wait()
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = p.r <= 16   ? cudaLaunchKernelEx(&cfg, rfq_lora_forward_kernel<2, kF32>, p)
+                  : p.r <= 32 ? cudaLaunchKernelEx(&cfg, rfq_lora_forward_kernel<4, kF32>, p)
+                  : p.r <= 64 ? cudaLaunchKernelEx(&cfg, rfq_lora_forward_kernel<8, kF32>, p)
+                              : cudaLaunchKernelEx(&cfg, rfq_lora_forward_kernel<16, kF32>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int kJ16, int kT>
@@ -1362,12 +1363,10 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
 
 }  // namespace
 
+// Long batches leave s as bf16 terms; short ones need nothing (256 bytes, so that a workspace is one).
 size_t lora_forward_workspace(int64_t M, int64_t K, int64_t r, int64_t n) {
-  if (wide(M, n)) return align256(static_cast<size_t>(3) * M * r * 2);
-  int64_t cs;
-  int z;
-  return align256(static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4) +
-         align256(static_cast<size_t>(shrink_splits(M, K, n, &cs, &z)) * M * r * 4);
+  (void)K;
+  return wide(M, n) ? align256(static_cast<size_t>(3) * M * r * 2) : 256;
 }
 
 size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
@@ -1384,12 +1383,32 @@ cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, con
     if (e != cudaSuccess) return e;
     return launch_lora_expand_wide(ws, terms, b, false, ids, base, y, !y_bf16, M, N, n, r, num_sms, encode_tiled, stream);
   }
-  int* table = static_cast<int*>(ws);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4));
-  int splits = 1;
-  e = shrink(x, a, false, ids, table, part, M, K, n, r, &splits, stream);
-  if (e != cudaSuccess) return e;
-  return expand(part, splits, scale, b, false, table, base, y, !y_bf16, hidden, M, N, n, r, stream);
+  ForwardParams p = {};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.a = static_cast<const __nv_bfloat16*>(a);
+  p.b = static_cast<const __nv_bfloat16*>(b);
+  p.scale = scale;
+  p.ids = ids;
+  p.base = base;
+  p.out = y;
+  p.hidden = hidden;
+  p.M = M;
+  p.K = K;
+  p.N = N;
+  p.n = static_cast<int>(n);
+  p.r = static_cast<int>(r);
+  // Clusters of eight, fewer where the items alone fill the device.
+  const int64_t chunks = ceil_div(M, kChunk), z = chunk_ctas(M, n, 2 * kPlanSms);
+  p.zs = static_cast<int>(z);
+  const int64_t slots = (r <= 64 ? 2 : 1) * kPlanSms;   // CTAs that are resident at once
+  p.cluster = 8;
+  while (p.cluster > 1 && chunks * z * p.cluster > slots) p.cluster /= 2;
+  // Few items: several clusters share the columns of one (256 columns a CTA at least).
+  int64_t parts = slots / (chunks * z * p.cluster);
+  const int64_t most = ceil_div(N, 256 * p.cluster);
+  p.parts = static_cast<int>(parts < most ? parts : most);
+  if (p.parts < 1) p.parts = 1;
+  return y_bf16 ? forward_typed<false>(p, chunks * z * p.parts, stream) : forward_typed<true>(p, chunks * z * p.parts, stream);
 }
 
 cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* dy,
@@ -1410,12 +1429,12 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   cudaError_t e = cudaSuccess;
   if (dx != nullptr || da != nullptr) {
     e = chunks ? launch_lora_shrink_wide(dy, b, true, ids, scale, nullptr, ds, ds_terms, M, N, n, r, num_sms, encode_tiled, stream)
-               : shrink(dy, b, true, ids, table, part, M, N, n, r, &splits, stream);
+               : shrink(dy, b, ids, table, part, M, N, n, r, &splits, stream);
     if (e != cudaSuccess) return e;
   }
   if (dx != nullptr) {
     e = chunks ? launch_lora_expand_wide(ds, ds_terms, a, true, ids, dx_base, dx, !dx_bf16, M, K, n, r, num_sms, encode_tiled, stream)
-               : expand(part, splits, scale, a, true, table, dx_base, dx, !dx_bf16, nullptr, M, K, n, r, stream);
+               : expand(part, splits, scale, a, table, dx_base, dx, !dx_bf16, M, K, n, r, stream);
     if (e != cudaSuccess) return e;
   }
   if (da == nullptr && db == nullptr) return e;
