@@ -448,7 +448,7 @@ rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, cons
 
 size_t rfq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n_adapters, int backward) {
   if (M <= 0 || !lora_shape_ok(M, K, N, rank, n_adapters)) return 0;
-  const size_t f = rfq::lora_forward_workspace(M, K, rank, n_adapters);
+  const size_t f = rfq::lora_forward_workspace(M, K, N, rank, n_adapters);
   const size_t b = backward ? rfq::lora_backward_workspace(M, K, N, rank, n_adapters) : 0;
   return f > b ? f : b;
 }
@@ -464,7 +464,7 @@ rfq_status_t rfq_lora(const void* x_bf16, int64_t M, int64_t K, const void* a_bf
   if (!aligned16(x_bf16) || !aligned16(a_bf16) || !aligned16(b_bf16) || !aligned_to(scale, 4) || !aligned_to(ids, 4) ||
       !aligned16(base) || !aligned16(y) || !aligned_to(hidden, 4))
     return RFQ_ERR_MISALIGNED;
-  rfq_status_t st = check_workspace(workspace, workspace_bytes, rfq::lora_forward_workspace(M, K, rank, n_adapters));
+  rfq_status_t st = check_workspace(workspace, workspace_bytes, rfq::lora_forward_workspace(M, K, N, rank, n_adapters));
   if (st != RFQ_OK) return st;
   int sms = 0;
   if ((st = current_device(&sms)) != RFQ_OK) return st;

@@ -70,7 +70,7 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
                                cudaStream_t stream);
 
 // Low-rank adapters beside a projection (rfq_lora.cu).  base, hidden, dx, da, db may be nullptr.
-size_t lora_forward_workspace(int64_t M, int64_t K, int64_t r, int64_t n);
+size_t lora_forward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n);
 size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n);
 cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, const float* scale, const int* ids, const void* base,
                                 void* y, bool y_bf16, float* hidden, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n,

@@ -1204,9 +1204,19 @@ int ring_stages(int stage_bytes, int other_bytes) {
 }
 
 // Whether a batch goes by chunks of 128 neighbouring rows (rfq_lora_wide.cu) or by groups of up to 16
-// rows of one adapter: the latter up to 64 rows, and where an adapter has no more than 32 rows on
-// average, since a chunk is passed over once for each adapter in it.
-bool wide(int64_t M, int64_t n) { return M > 64 && M > 32 * n; }
+// rows of one adapter.  A chunk is passed over once for each adapter in it, so there have to be more
+// than 32 rows for each on average; and the two wide kernels take 15 us whatever they do, which is
+// worth it from a size on that goes with M r (K + N).  Measured at K = N = 4096, one adapter, groups
+// against chunks.  Forward: rank 16, 2000 rows 19 against 27 us, 3000 rows 31 against 24; rank 64, 300
+// rows 15 against 17, 500 rows 19 against 17.  Backward (dx): rank 16, 128 rows 12 against 15 us,
+// 1000 rows 25 against 16; rank 64, 128 rows 19 against 17.  An fp32 y counts half as much again (rank
+// 16, 1000 rows 15 against 19 us, 2000 rows 24 against 26).
+bool wide_forward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, bool f32) {
+  return M > 64 && M > 32 * n && M * r * (K + N) / 2 * (f32 ? 3 : 2) > 250000000;
+}
+bool wide_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
+  return M > 64 && M > 32 * n && M * r * (K + N) > 60000000;
+}
 
 // CTAs that share the groups of one chunk: one for each there can be, up to `most` over all chunks.
 int64_t chunk_ctas(int64_t M, int64_t n, int64_t most) {
@@ -1349,7 +1359,7 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
   };
   b.range = outer_range(M, ceil_div(K, kOuterCols) + ceil_div(N, kOuterCols));
   b.ranges = static_cast<int>(ceil_div(M, b.range));
-  const bool chunks = wide(M, n);
+  const bool chunks = wide_backward(M, K, N, r, n);
   b.table = take(chunks ? 0 : static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4);
   b.part = take(chunks ? 0 : static_cast<size_t>(shrink_splits(M, N, n, &cs, &z)) * M * r * 4);
   b.ds = take(static_cast<size_t>(3) * M * r * 2);
@@ -1364,9 +1374,8 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
 }  // namespace
 
 // Long batches leave s as bf16 terms; short ones need nothing (256 bytes, so that a workspace is one).
-size_t lora_forward_workspace(int64_t M, int64_t K, int64_t r, int64_t n) {
-  (void)K;
-  return wide(M, n) ? align256(static_cast<size_t>(3) * M * r * 2) : 256;
+size_t lora_forward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
+  return wide_forward(M, K, N, r, n, true) ? align256(static_cast<size_t>(3) * M * r * 2) : 256;   // whatever y's type
 }
 
 size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
@@ -1377,7 +1386,7 @@ cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, con
                                 void* y, bool y_bf16, float* hidden, int64_t M, int64_t K, int64_t N, int64_t r, int64_t n,
                                 void* ws, int num_sms, void* encode_tiled, cudaStream_t stream) {
   cudaError_t e;
-  if (wide(M, n)) {
+  if (wide_forward(M, K, N, r, n, !y_bf16)) {
     const int terms = y_bf16 ? 1 : 3;
     e = launch_lora_shrink_wide(x, a, false, ids, scale, hidden, ws, terms, M, K, n, r, num_sms, encode_tiled, stream);
     if (e != cudaSuccess) return e;
@@ -1421,7 +1430,7 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   int* table = reinterpret_cast<int*>(base + pl.table);
   __nv_bfloat16* ds = reinterpret_cast<__nv_bfloat16*>(base + pl.ds);
   __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(base + pl.s);
-  const bool chunks = wide(M, n);
+  const bool chunks = wide_backward(M, K, N, r, n);
   const int terms = grad_bf16 ? 2 : 3;
   // Terms of ds' as shrink leaves them: what the adapters' gradients or an fp32 dx need.
   const int ds_terms = dx != nullptr && !dx_bf16 ? 3 : terms;

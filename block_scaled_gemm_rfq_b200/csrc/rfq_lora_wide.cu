@@ -780,9 +780,10 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
   }
   p.kt_per_rank = static_cast<int>(ceil_div(p.kt, p.cluster));
   const uint32_t stage = kBox + shrink_p_bytes(trans, p.r), sums = shrink_sum_bytes(p.r);
-  // As many stages as leave room for two CTAs per SM, where there are that many CTAs; else, or where
-  // that would be fewer than three, as many as fit one.
-  const uint32_t room = chunks * p.cluster > num_sms ? kSmemLimit / 2 : kSmemLimit;
+  // As many stages as leave room for two CTAs per SM; as many as fit one where there are few CTAs (clusters
+  // of 8 do not fill every SM alone: 16 of them took two rounds, 27 us for 2000 rows against 24 for 3000)
+  // or two would have fewer than three each.
+  const uint32_t room = chunks * p.cluster > num_sms / 2 ? kSmemLimit / 2 : kSmemLimit;
   p.stages = sums + 2048 < room ? static_cast<int>((room - 2048 - sums) / stage) : 0;
   if (p.stages < 3) p.stages = static_cast<int>((kSmemLimit - 2048 - sums) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
