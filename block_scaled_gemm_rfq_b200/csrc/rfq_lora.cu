@@ -1206,13 +1206,13 @@ int ring_stages(int stage_bytes, int other_bytes) {
 // Whether a batch goes by chunks of 128 neighbouring rows (rfq_lora_wide.cu) or by groups of up to 16
 // rows of one adapter.  A chunk is passed over once for each adapter in it, so there have to be more
 // than 32 rows for each on average; and the two wide kernels take 15 us whatever they do, which is
-// worth it from a size on that goes with M r (K + N).  Measured at K = N = 4096, one adapter, groups
-// against chunks.  Forward: rank 16, 2000 rows 19 against 27 us, 3000 rows 31 against 24; rank 64, 300
-// rows 15 against 17, 500 rows 19 against 17.  Backward (dx): rank 16, 128 rows 12 against 15 us,
-// 1000 rows 25 against 16; rank 64, 128 rows 19 against 17.  An fp32 y counts half as much again (rank
-// 16, 1000 rows 15 against 19 us, 2000 rows 24 against 26).
+// worth it from a size on.  Measured with one adapter, groups against chunks.  Forward, K = N = 4096:
+// rank 16, 1000 rows 11 against 16 us, 3000 rows 31 against 24; rank 64, 300 rows 15 against 17,
+// 1000 rows 21 against 18; 5120 -> 13824, rank 8, 1111 rows 30 against 25; an fp32 y counts half as
+// much again (rank 16, 1000 rows 15 against 19 us, 2000 rows 24 against 26).  Backward (dx), K = N =
+// 4096: rank 16, 128 rows 12 against 15 us, 1000 rows 25 against 16; rank 64, 128 rows 19 against 17.
 bool wide_forward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, bool f32) {
-  return M > 64 && M > 32 * n && M * r * (K + N) / 2 * (f32 ? 3 : 2) > 250000000;
+  return M > 64 && M > 32 * n && M * (r + 8) * (K + N) / 2 * (f32 ? 3 : 2) > 330000000;
 }
 bool wide_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
   return M > 64 && M > 32 * n && M * r * (K + N) > 60000000;
@@ -1406,12 +1406,12 @@ cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, con
   p.N = N;
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
-  // Clusters of eight, fewer where the items alone fill the device.
+  // Clusters of up to eight, as many as are resident at once.
   const int64_t chunks = ceil_div(M, kChunk), z = chunk_ctas(M, n, 2 * kPlanSms);
   p.zs = static_cast<int>(z);
   const int64_t slots = (r <= 64 ? 2 : 1) * kPlanSms;   // CTAs that are resident at once
-  p.cluster = 8;
-  while (p.cluster > 1 && chunks * z * p.cluster > slots) p.cluster /= 2;
+  const int64_t ranks = slots / (chunks * z);
+  p.cluster = static_cast<int>(ranks < 1 ? 1 : ranks > 8 ? 8 : ranks);
   // Few items: several clusters share the columns of one (256 columns a CTA at least).
   int64_t parts = slots / (chunks * z * p.cluster);
   const int64_t most = ceil_div(N, 256 * p.cluster);
