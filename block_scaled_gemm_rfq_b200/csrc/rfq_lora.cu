@@ -1223,8 +1223,8 @@ int64_t chunk_ctas(int64_t M, int64_t n, int64_t most) {
   const int64_t chunks = ceil_div(M, kChunk), rows = M < kChunk ? M : kChunk;
   int64_t z = n + 1 + rows / kRows;   // every adapter, the rows without one, and groups that are full
   if (z > rows) z = rows;
-  while (z > 1 && chunks * z > most) z = (z + 1) / 2;
-  return z;
+  if (chunks * z > most) z = most / chunks;
+  return z > 1 ? z : 1;
 }
 
 // Splits of the shrink product's contraction: one wave of three CTAs per SM, 256 elements each at least.
