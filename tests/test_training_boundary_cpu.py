@@ -3,9 +3,13 @@ check comes before a device is touched (no address here is ever dereferenced).""
 import ctypes
 
 import pytest
+import torch
 
 import block_scaled_gemm_rfq_b200 as rfq
 from block_scaled_gemm_rfq_b200 import build as rfq_build
+
+# The addresses are made up: beside a GPU a call whose arguments pass would be launched on them.
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="needs a host without a GPU")
 
 A = 1 << 20   # an aligned address
 NO_DEVICE = (4, 5)   # what a call says here once its arguments have passed
