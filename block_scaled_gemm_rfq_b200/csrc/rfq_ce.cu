@@ -33,6 +33,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "rfq_internal.h"
 #include "rfq_ptx.cuh"
@@ -55,9 +56,20 @@ constexpr uint32_t kSmemLimit = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
 // The tensor cores add into the fp32 accumulator by truncation, so a long contraction drifts
 // towards zero: 3e-6 of lse at D = 4096 when one accumulator takes all of it.  Where the
-// logits themselves are the result (kLogits) the accumulator therefore takes 1024 elements of
-// the contraction at a time and the epilogue adds those parts with rounding.
-constexpr int kLogitsPart = 16;          // k-tiles
+// logits themselves are the result (kLogits) the accumulator therefore takes a part of the
+// contraction at a time and the epilogue adds those parts with rounding: 1024 elements above 128 rows (512 cost
+// 4 % of 2048 rows against 131072 x 4096), 128 up to 128 rows, where reading the head hides it (22.0 us both for
+// 8 rows against 32003 x 1024) and a loss of few rows has no others to average with (3e-6 -> 3e-7 for one row).
+template <int kPair>
+constexpr int kLogitsPart = kPair == 2 ? 16 : 2;          // k-tiles
+// dz is rounded to bf16 for the next products.  Over many rows those roundings average out; a few rows leave
+// a gradient that is off by one rounding of its largest entries, beside its own.  Up to 16 rows dz is therefore
+// kept as the sum of two bf16 terms: rows T .. 2 T - 1 of dz are what rows 0 .. T - 1 left out.  dh takes both
+// in the one tile of 128 rows that it fills anyway and adds its rows at the end; dw takes a second k-tile.  Error
+// of dh against 64 bits with one and with two terms: 1 row 0.0031 and 0.0018, 6 rows 0.0020 and 0.0017 (a bf16
+// rounding alone is 0.0017).  It costs 1 row of 112492 x 2824 nothing (557 us), 3 of 3863 x 3112 72 -> 82 us; at 64
+// rows of 50000 x 2048 189 -> 217 us, for an error that is 0.0020 without.
+constexpr int64_t kTwoTermRows = 16;
 
 // Products that write a matrix pass its rows through 4 KiB of shared memory per epilogue warp, so that
 // they leave in whole 128-byte lines: a thread holds 128 columns of one row, and 16-byte stores of
@@ -117,6 +129,7 @@ struct Params {
   int accumulate;         // not the first piece
   // kHidden and kHead
   __nv_bfloat16* out;     // [M][N]
+  int term;               // kGrad and kHead: rows of dz before its second terms begin, or 0: it has none
 };
 
 // Shared-memory operand descriptors (128-byte swizzle).  K-major: rows of 128 bytes, 8-row
@@ -264,13 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
             };
             if constexpr (kAMn) {
 #pragma unroll
-              for (int c = 0; c < kBM / 64; ++c) load(sa + c * kChunk, &maps.a, row_a + 64 * c, kt * kBK);
+              for (int c = 0; c < kBM / 64; ++c) load(sa + c * kChunk, &maps.a, row_a + 64 * c, kt * (p.term > 0 ? p.term : kBK));
             } else {
               load(sa, &maps.a, kt * kBK, row_a);
             }
             if constexpr (kBMn) {
 #pragma unroll
-              for (int c = 0; c < kBN / kPair / 64; ++c) load(sb + c * kChunk, &maps.b, row_b + 64 * c, kt * kBK);
+              for (int c = 0; c < kBN / kPair / 64; ++c)   // the second terms meet the same rows of h; past its end are zeros
+                load(sb + c * kChunk, &maps.b, row_b + 64 * c, kMode == kHead && p.term > 0 ? 0 : kt * kBK);
             } else {
               load(sb, &maps.b, kt * kBK, row_b);
             }
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       bool ok = true;
       for (int item = unit; item < items && ok; item += p.share.units) {
         if (!work_at(p, item, t)) continue;
-        const int part = kMode == kLogits ? kLogitsPart : t.kt1 - t.kt0;
+        const int part = kMode == kLogits ? kLogitsPart<kPair> : t.kt1 - t.kt0;
         for (int kp = t.kt0; kp < t.kt1 && ok; kp += part) {
           if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, &g_ce_error, kErrWaitAccEmpty)) {
             ok = false;
@@ -390,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       };
       bool ok = take(true);
       if constexpr (kMode == kLogits)
-        for (int kp = t.kt0 + kLogitsPart; kp < t.kt1 && ok; kp += kLogitsPart) ok = take(false);
+        for (int kp = t.kt0 + kLogitsPart<kPair>; kp < t.kt1 && ok; kp += kLogitsPart<kPair>) ok = take(false);
       if (!ok) break;
       // Hands this warp's rows over for storing, 128 bytes of each at a time: fill(c) gives this thread's
       // 16-byte piece c, keep(r, c, piece) stores piece c of row r of the warp's 32.
@@ -410,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
         }
       };
       const int row_w = row - lane;   // the warp's first row
+      if (row_w >= p.M) continue;
 
       if constexpr (kMode == kLogits) {
         if (row >= p.M) continue;
@@ -450,20 +465,30 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
         g = gmax > 0.f ? g / gmax : g;          // gmax == 0: every finite entry is zero
         if (label < 0 || label >= p.vocab) g = NAN;
         const float l2 = p.lse[at_row] * kLog2e;
-        turn(16, [&](int i) {
-          float d[8];
+        auto leave = [&](auto second) {
+          constexpr bool kSecond = decltype(second)::value;
+          turn(16, [&](int i) {
+            float d[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = 8 * i + e;
-            float q = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), kLog2e, -l2));
-            if (k == at) q -= 1.f;
-            d[e] = counted ? q * g : 0.f;
-          }
-          return make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
-        }, [&](int r, int c, const uint4& piece) {
-          if (row_w + r < p.M && col0 + 8 * c < p.N)
-            *reinterpret_cast<uint4*>(p.dz + static_cast<int64_t>(row_w + r) * p.ld_dz + col0 + 8 * c) = piece;
-        });
+            for (int e = 0; e < 8; ++e) {
+              const int k = 8 * i + e;
+              float q = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), kLog2e, -l2));
+              if (k == at) q -= 1.f;
+              d[e] = counted ? q * g : 0.f;
+              if constexpr (kSecond) {   // of an infinite or NaN entry the first term says all
+                const float left = d[e] - __bfloat162float(__float2bfloat16_rn(d[e]));
+                d[e] = fabsf(left) <= 1.f ? left : 0.f;
+              }
+            }
+            return make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+          }, [&](int r, int c, const uint4& piece) {
+            if (row_w + r < p.M && col0 + 8 * c < p.N)
+              *reinterpret_cast<uint4*>(p.dz + static_cast<int64_t>(row_w + r + (kSecond ? p.term : 0)) * p.ld_dz + col0 + 8 * c) = piece;
+          });
+        };
+        leave(std::false_type{});
+        if constexpr (kPair == 1)
+          if (p.term > 0) leave(std::true_type{});
       } else if (kMode == kHidden && (p.out == nullptr || t.slot >= 0)) {
         float* dst = t.slot < 0 ? p.acc + static_cast<int64_t>(row_w) * p.N + col0
                                 : p.slots + (static_cast<int64_t>(t.slot) * (kBM * kPair) + rank * kBM + quad * 32) * kBN + half * 128;
@@ -579,11 +604,11 @@ __global__ void __launch_bounds__(1024) rfq_ce_gmax_kernel(const float* dloss, c
   }
 }
 
-// dh of the tiles that the product left in fp32: gmax * the sum of a tile's slots, in order, or (whole
-// tiles of a product over several pieces) gmax * its sums.  One block per 4 rows of a tile, so that small
+// dh of the tiles that the product left in fp32: gmax * the sum of a tile's slots, in order (of two rows where
+// dz has two terms), or (whole tiles of a product over several pieces) gmax * its sums.  One block per 4 rows of a tile, so that small
 // outputs of many slices have their loads under way at once.
 __global__ void __launch_bounds__(256) rfq_ce_hidden_kernel(const Share share, int tile0, int tile_rows, const float* acc, const float* slots,
-                                                            const float* gmax, int M, int N, __nv_bfloat16* dh) {
+                                                            const float* gmax, int M, int N, int term, __nv_bfloat16* dh) {
   griddep_launch_dependents();
   griddep_wait();
   const int blocks = tile_rows / 4;
@@ -608,6 +633,17 @@ __global__ void __launch_bounds__(256) rfq_ce_hidden_kernel(const Share share, i
       f.y += o.y;
       f.z += o.z;
       f.w += o.w;
+    }
+    if (term > 0) {
+      src += static_cast<int64_t>(term) * kBN;
+#pragma unroll 8
+      for (int s = 0; s < share.slices; ++s) {
+        const float4 o = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(s) * tile_rows * kBN);
+        f.x += o.x;
+        f.y += o.y;
+        f.z += o.z;
+        f.w += o.w;
+      }
     }
   }
   *reinterpret_cast<uint2*>(dh + static_cast<int64_t>(row) * N + col) = make_uint2(pack_bf16(f.x * g, f.y * g), pack_bf16(f.z * g, f.w * g));
@@ -640,7 +676,9 @@ constexpr int kPlanSms = 148;                      // work is shared out for a B
 // Pairs of CTAs above 128 rows.
 int pair_of(int64_t M) { return M > kBM ? 2 : 1; }
 
-Share share_out(int64_t M, int64_t N, int64_t K, bool cut_rest) {
+enum Cut { kWhole, kCutRest, kAllSlots };
+
+Share share_out(int64_t M, int64_t N, int64_t K, Cut cut) {
   const int pair = pair_of(M);
   Share s = {};
   s.num_mb = static_cast<int>(ceil_div(M, kBM * pair));
@@ -650,10 +688,10 @@ Share share_out(int64_t M, int64_t N, int64_t K, bool cut_rest) {
   s.units = kPlanSms / pair;
   s.slices = 1;
   s.slice_kt = static_cast<int>(ceil_div(K, kBK));
-  if (cut_rest && s.tiles % s.units != 0) {
+  if (cut == kAllSlots || (cut == kCutRest && s.tiles % s.units != 0)) {
     // The number of slices that leaves the fewest k-tiles to the unit with the most, each slice
     // charged 4 for its epilogue.
-    s.whole = s.tiles / s.units * s.units;
+    s.whole = cut == kAllSlots ? 0 : s.tiles / s.units * s.units;
     const int64_t rest = s.tiles - s.whole, kt = s.slice_kt;
     int64_t best = INT64_MAX;
     for (int n = 1; n <= 32 && n <= kt; ++n) {
@@ -666,7 +704,7 @@ Share share_out(int64_t M, int64_t N, int64_t K, bool cut_rest) {
         s.slice_kt = static_cast<int>(per);
       }
     }
-    if (s.slices == 1) s.whole = s.tiles;
+    if (s.slices == 1 && cut != kAllSlots) s.whole = s.tiles;
   }
   return s;
 }
@@ -691,13 +729,14 @@ cudaError_t product(EncodeTiledFn encode, const void* a, int64_t a_ld, const voi
   constexpr bool kBMn = kMode == kHidden || kMode == kHead;
   const bool pair = pair_of(M) == 2;
   Maps maps;
-  const bool ok = (kAMn ? encode_bf16_map(encode, &maps.a, a, K, M, a_ld, kBK) : encode_bf16_map(encode, &maps.a, a, M, K, a_ld, kBM)) &&
+  const int64_t a_rows = p.term > 0 ? 2 * K : K;
+  const bool ok = (kAMn ? encode_bf16_map(encode, &maps.a, a, a_rows, M, a_ld, kBK) : encode_bf16_map(encode, &maps.a, a, M, K, a_ld, kBM)) &&
                   (kBMn ? encode_bf16_map(encode, &maps.b, b, K, N, b_ld, kBK)
                         : encode_bf16_map(encode, &maps.b, b, N, K, b_ld, pair ? kBN / 2 : kBN));
   if (!ok) return cudaErrorInvalidValue;
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
-  p.num_kt = static_cast<int>(ceil_div(K, kBK));
+  p.num_kt = kAMn && p.term > 0 ? 2 : static_cast<int>(ceil_div(K, kBK));
   p.share = share;
   return pair ? launch_mode<2, kMode>(maps, p, stream) : launch_mode<1, kMode>(maps, p, stream);
 }
@@ -712,21 +751,23 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 // the offsets of the workspace's parts.
 struct Plan {
   int64_t piece, pieces, ld_dz;
+  int64_t rows;           // of dz
   Share hidden;
   size_t off_acc, off_slots, off_gmax, bytes;
 };
 
 Plan plan_backward(int64_t T, int64_t D, int64_t V, bool want_dh) {
   Plan q;
-  q.piece = kPieceBytes / 2 / T / kBN * kBN;
+  q.rows = T <= kTwoTermRows ? 2 * T : T;
+  q.piece = kPieceBytes / 2 / q.rows / kBN * kBN;
   if (q.piece < kMinPiece) q.piece = kMinPiece;
   q.pieces = ceil_div(V, q.piece);
   if (q.pieces == 1) q.piece = V;
   else q.piece = ceil_div(ceil_div(V, q.pieces), kBN) * kBN;      // even pieces
   q.pieces = ceil_div(V, q.piece);
   q.ld_dz = (q.piece + 7) / 8 * 8;
-  q.hidden = share_out(T, D, q.piece, true);
-  size_t at = align256(static_cast<size_t>(T) * q.ld_dz * 2);
+  q.hidden = share_out(q.rows, D, q.piece, q.rows > T ? kAllSlots : kCutRest);
+  size_t at = align256(static_cast<size_t>(q.rows) * q.ld_dz * 2);
   q.off_acc = at;
   if (want_dh && q.pieces > 1 && q.hidden.whole > 0) at += align256(static_cast<size_t>(T) * D * 4);
   q.off_slots = at;
@@ -759,7 +800,7 @@ cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* label
     p.vocab = V;
     p.stats = static_cast<float2*>(ws);
     p.target = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(parts) * rows * sizeof(float2)));
-    cudaError_t e = product<kLogits>(encode, static_cast<const __nv_bfloat16*>(h) + t0 * D, D, w, D, rows, V, D, share_out(rows, V, D, false), p, stream);
+    cudaError_t e = product<kLogits>(encode, static_cast<const __nv_bfloat16*>(h) + t0 * D, D, w, D, rows, V, D, share_out(rows, V, D, kWhole), p, stream);
     if (e != cudaSuccess) return e;
     e = launch_pdl(rfq_ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 32))), dim3(32, 32), 0, 1, stream,
                    static_cast<const float2*>(p.stats), static_cast<const float*>(p.target), p.labels, static_cast<int>(rows),
@@ -793,17 +834,18 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
     p.gmax = gmax;
     p.dz = dz;
     p.ld_dz = q.ld_dz;
-    e = product<kGrad>(encode, h, D, wp, D, T, n, D, share_out(T, n, D, false), p, stream);
+    p.term = q.rows > T ? static_cast<int>(T) : 0;
+    e = product<kGrad>(encode, h, D, wp, D, T, n, D, share_out(T, n, D, kWhole), p, stream);
     if (e == cudaSuccess && dh != nullptr) {
       p.acc = acc;
       p.slots = slots;
       p.accumulate = v0 > 0;
       p.out = q.pieces == 1 ? static_cast<__nv_bfloat16*>(dh) : nullptr;
-      e = product<kHidden>(encode, dz, q.ld_dz, wp, D, T, D, n, q.hidden, p, stream);
+      e = product<kHidden>(encode, dz, q.ld_dz, wp, D, q.rows, D, n, q.hidden, p, stream);
     }
     if (e == cudaSuccess && dw != nullptr) {
       p.out = static_cast<__nv_bfloat16*>(dw) + v0 * D;
-      e = product<kHead>(encode, dz, q.ld_dz, h, D, n, D, T, share_out(n, D, T, false), p, stream);
+      e = product<kHead>(encode, dz, q.ld_dz, h, D, n, D, T, share_out(n, D, T, kWhole), p, stream);
     }
   }
   // Tiles of dh still in fp32: all of them after several pieces, else the rest.
@@ -812,7 +854,8 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
     const int tile_rows = kBM * pair_of(T);
     e = launch_pdl(rfq_ce_hidden_kernel, dim3(static_cast<unsigned>((q.hidden.tiles - tile0) * (tile_rows / 4))), dim3(256), 0, 1, stream,
                    q.hidden, tile0, tile_rows, static_cast<const float*>(acc), static_cast<const float*>(slots),
-                   static_cast<const float*>(gmax), static_cast<int>(T), static_cast<int>(D), static_cast<__nv_bfloat16*>(dh));
+                   static_cast<const float*>(gmax), static_cast<int>(T), static_cast<int>(D), q.rows > T ? static_cast<int>(T) : 0,
+                   static_cast<__nv_bfloat16*>(dh));
   }
   return e;
 }

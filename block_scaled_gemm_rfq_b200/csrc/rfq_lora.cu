@@ -410,10 +410,13 @@ template <bool kF32>
 __host__ __device__ constexpr int expand_stage_bytes(int r) {
   return kRows * kRowStride + r * kQStride<kF32>;
 }
-// The rank-r vector enters the MMA in bf16: one term (2^-8 of the adapter's share, below the
-// rounding of a bf16 output) or, for an fp32 output, three (24 bits).
+// The rank-r vector enters the MMA in bf16 terms of 8 bits each: three for an fp32 output (24 bits), two
+// for a bf16 one.  One term would add an error as large as the output's own rounding (2^-9 of the adapter's
+// share), in the same direction for a whole row, and the few rows of a short batch do not average it away: dx of
+// two rows of rank 16 was off by 1.6 times its rounding.  The second costs 26.4 -> 27.8 us for 256 rows of 48
+// adapters of rank 32 (4096 -> 12288), nothing for 16 rows.
 template <bool kF32>
-constexpr int kExpandTerms = kF32 ? 3 : 1;
+constexpr int kExpandTerms = kF32 ? 3 : 2;
 template <bool kF32>
 __host__ __device__ constexpr int expand_s_bytes(int r) {
   return kExpandTerms<kF32> * kRows * odd_stride(2 * r);
@@ -617,7 +620,7 @@ struct ForwardParams {
 
 template <int kJ, bool kF32>   // kJ: 8-column tiles of the rank, at most
 __global__ void __launch_bounds__(kThreads, kJ <= 8 ? 2 : 1) rfq_lora_forward_kernel(const ForwardParams p) {
-  constexpr int kT = kF32 ? 3 : 1;   // bf16 terms of s, see rfq_lora_expand_kernel
+  constexpr int kT = kExpandTerms<kF32>;
   constexpr int kSmRow = kJ * 8 + 8;
   constexpr int kRedBytes = 4 * kRows * kJ * 8 * 4, kSmBytes = kT * kRows * kSmRow * 2;
   __shared__ __align__(16) Groups g;

@@ -347,3 +347,19 @@ def test_binding_refuses_what_the_kernel_cannot_read(rfq):
     with pytest.raises(rfq.RFQError) as e:
         rfq.linear_ce(h, w, labels, loss, lse, ws[:100])
     assert e.value.status == 7
+
+
+@pytest.mark.parametrize("T", [1, 2, 16])
+def test_gradients_of_few_rows_are_rounded_once(rfq, T):
+    """Up to 16 rows the softmax's gradient enters the products with 16 bits: what is left is the rounding of the
+    outputs (2^-8 of each entry) and, of the terms that were summed, 2^-14 (2^-17 from the two terms, below 2^-16 from
+    exponentials, the label's p - 1 and fp32 sums of up to 300 terms)."""
+    D, V = 72, 300
+    h, w, labels, dloss = make(T, D, V, seed=40 + T, ignore_share=0)
+    _, lse = rfq.linear_ce_alloc(h, w, labels)
+    dh, dw = rfq.linear_ce_backward_alloc(h, w, labels, lse, dloss)
+    h64, w64 = h.double(), w.double()
+    z = h64 @ w64.t()
+    dz = (torch.softmax(z, 1) - torch.nn.functional.one_hot(labels, V)) * dloss.double()[:, None]
+    for got, want, terms in ((dh, dz @ w64, dz.abs() @ w64.abs()), (dw, dz.t() @ h64, dz.abs().t() @ h64.abs())):
+        assert ((got.double() - want).abs() <= 2.0**-8 * want.abs() + 2.0**-14 * terms).all()
