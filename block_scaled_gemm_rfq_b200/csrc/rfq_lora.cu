@@ -1221,6 +1221,14 @@ bool wide_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
   return M > 64 && M > 32 * n && M * r * (K + N) > 60000000;
 }
 
+// Whether ds of a long batch comes from chunks too: a cluster of eight CTAs works on each, which leaves SMs
+// idle below 2400 rows and passes over N / 8 once for each adapter in it.  Measured, whole backward pass, ds by groups
+// against chunks: 5120 -> 13824, rank 8 of 3 adapters, 1000 rows 48 against 63 us, 2000 rows 69 against 76, 2900 rows 96 against 94; rank 16,
+// 1000 rows 43 against 45, 2000 rows 63 against 57; rank 64, 300 rows 48 against 49, 1000 rows 84 against 71.
+bool wide_ds(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
+  return wide_backward(M, K, N, r, n) && M * r > 20000;
+}
+
 // CTAs that share the groups of one chunk: one for each there can be, up to `most` over all chunks.
 int64_t chunk_ctas(int64_t M, int64_t n, int64_t most) {
   const int64_t chunks = ceil_div(M, kChunk), rows = M < kChunk ? M : kChunk;
@@ -1362,7 +1370,7 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
   };
   b.range = outer_range(M, ceil_div(K, kOuterCols) + ceil_div(N, kOuterCols));
   b.ranges = static_cast<int>(ceil_div(M, b.range));
-  const bool chunks = wide_backward(M, K, N, r, n);
+  const bool chunks = wide_ds(M, K, N, r, n);
   b.table = take(chunks ? 0 : static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4);
   b.part = take(chunks ? 0 : static_cast<size_t>(shrink_splits(M, N, n, &cs, &z)) * M * r * 4);
   b.ds = take(static_cast<size_t>(3) * M * r * 2);
@@ -1433,23 +1441,17 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   int* table = reinterpret_cast<int*>(base + pl.table);
   __nv_bfloat16* ds = reinterpret_cast<__nv_bfloat16*>(base + pl.ds);
   __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(base + pl.s);
-  const bool chunks = wide_backward(M, K, N, r, n);
+  const bool chunks = wide_backward(M, K, N, r, n), chunks_ds = wide_ds(M, K, N, r, n);
   const int terms = grad_bf16 ? 2 : 3;
-  // Terms of ds' as shrink leaves them: what the adapters' gradients or an fp32 dx need.
-  const int ds_terms = dx != nullptr && !dx_bf16 ? 3 : terms;
+  // Terms of ds' for expand and the adapters' gradients: what an fp32 dx or they need.
+  const int ds_terms = chunks && dx != nullptr && !dx_bf16 ? 3 : terms;
   int splits = 1;
   cudaError_t e = cudaSuccess;
   if (dx != nullptr || da != nullptr) {
-    e = chunks ? launch_lora_shrink_wide(dy, b, true, ids, scale, nullptr, ds, ds_terms, M, N, n, r, num_sms, encode_tiled, stream)
-               : shrink(dy, b, ids, table, part, M, N, n, r, &splits, stream);
+    e = chunks_ds ? launch_lora_shrink_wide(dy, b, true, ids, scale, nullptr, ds, ds_terms, M, N, n, r, num_sms, encode_tiled, stream)
+                  : shrink(dy, b, ids, table, part, M, N, n, r, &splits, stream);
     if (e != cudaSuccess) return e;
   }
-  if (dx != nullptr) {
-    e = chunks ? launch_lora_expand_wide(ds, ds_terms, a, true, ids, dx_base, dx, !dx_bf16, M, K, n, r, num_sms, encode_tiled, stream)
-               : expand(part, splits, scale, a, table, dx_base, dx, !dx_bf16, M, K, n, r, stream);
-    if (e != cudaSuccess) return e;
-  }
-  if (da == nullptr && db == nullptr) return e;
   SplitParams sp = {};
   sp.part = part;
   sp.scale = scale;
@@ -1459,23 +1461,34 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   sp.n = static_cast<int>(n);
   sp.r = static_cast<int>(r);
   sp.splits = splits;
-  sp.ds = da != nullptr && !chunks ? ds : nullptr;
+  sp.ds = !chunks_ds && (da != nullptr || (chunks && dx != nullptr)) ? ds : nullptr;
   sp.s = db != nullptr ? s : nullptr;
-  if (sp.ds != nullptr || sp.s != nullptr) {
+  auto split = [&](int kind) {
+    if (sp.ds == nullptr && sp.s == nullptr) return cudaSuccess;
     const int64_t blocks = ceil_div(M * r, kThreads);
     const dim3 sgrid(static_cast<unsigned>(blocks < 8 * kPlanSms ? blocks : 8 * kPlanSms));
-    e = grad_bf16 ? launch(rfq_lora_split_kernel<2>, sp, sgrid, 0, stream) : launch(rfq_lora_split_kernel<3>, sp, sgrid, 0, stream);
+    return kind == 2 ? launch(rfq_lora_split_kernel<2>, sp, sgrid, 0, stream) : launch(rfq_lora_split_kernel<3>, sp, sgrid, 0, stream);
+  };
+  // Expand over chunks reads ds' as terms, expand of groups forms them itself.
+  const bool split_first = chunks && !chunks_ds;
+  const int s_terms = split_first ? ds_terms : terms;
+  if (split_first && (e = split(s_terms)) != cudaSuccess) return e;
+  if (dx != nullptr) {
+    e = chunks ? launch_lora_expand_wide(ds, ds_terms, a, true, ids, dx_base, dx, !dx_bf16, M, K, n, r, num_sms, encode_tiled, stream)
+               : expand(part, splits, scale, a, table, dx_base, dx, !dx_bf16, M, K, n, r, stream);
     if (e != cudaSuccess) return e;
   }
+  if (da == nullptr && db == nullptr) return e;
+  if (!split_first && (e = split(s_terms)) != cudaSuccess) return e;
   OuterParams o = {};
   o.side[0].v = ds;
-  o.side[0].ld = static_cast<int>((chunks ? ds_terms : terms) * r);
+  o.side[0].ld = static_cast<int>(ds_terms * r);
   o.side[0].w = static_cast<const __nv_bfloat16*>(x);
   o.side[0].part = reinterpret_cast<float*>(base + pl.part_a);
   o.side[0].C = K;
   o.side[0].tiles = da != nullptr ? static_cast<int>(ceil_div(K, kOuterCols)) : 0;
   o.side[1].v = s;
-  o.side[1].ld = static_cast<int>(terms * r);
+  o.side[1].ld = static_cast<int>(s_terms * r);
   o.side[1].w = static_cast<const __nv_bfloat16*>(dy);
   o.side[1].part = reinterpret_cast<float*>(base + pl.part_b);
   o.side[1].C = N;

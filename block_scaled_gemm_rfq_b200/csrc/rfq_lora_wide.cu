@@ -16,15 +16,14 @@
 // have adapters of their own, take the kernels of rfq_lora.cu.)
 //
 // shrink: the contraction is split over a cluster of up to 8 CTAs, whose partial sums are added
-// through distributed shared memory in the order of the ranks.  The accumulator takes 1024
-// elements of the contraction at a time (256 for fp32 results: the tensor cores add by
-// truncation) and the epilogue adds those parts with rounding.
-// shrink leaves s as bf16 terms (one for a bf16 output; three, 24 bits, for an fp32 one), which are
-// expand's operand as they are.
-// expand: base tiles come in by TMA, are added to in shared memory and leave from there by TMA.
+// through distributed shared memory in the order of the ranks.  The accumulator takes 256
+// elements of the contraction at a time (the tensor cores add by truncation) and the epilogue adds those
+// parts with rounding.  shrink leaves s as bf16 terms (one for a bf16 output; three, 24 bits, for an fp32
+// one), which are expand's operand as they are.
+// expand: base tiles come in by TMA (by a warp of its own: behind the loads of Q in one queue, chunks of two
+// adapters held the base back and cost 1.3 times those of one), are added to in shared memory and leave from
+// there by TMA.
 //
-// (by a warp of its own: behind the loads of Q in one queue, chunks of two adapters held the base back
-// and cost 1.3 times those of one).
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, the others epilogue.  Every wait on an mbarrier
 // is bounded (rfq_ptx.cuh); after one that ran out the epilogue runs through its loops without
 // waiting, so that no warp is left alone at a barrier.  No TMA multicast.
@@ -48,8 +47,8 @@ constexpr int kChunk = 128;
 constexpr uint32_t kBox = kChunk * 128;    // 128 rows of 128 bytes
 constexpr uint32_t kSmemLimit = 232448;
 constexpr int kMaxStages = 8;
-// k-tiles of 64 per accumulation, for bf16 and for fp32 results.
-constexpr int kPartTiles = 16, kPartTilesF32 = 4;
+// k-tiles of 64 per accumulation.  Whatever the results' types, so that s does not depend on them (16 were no faster).
+constexpr int kPartTiles = 4;
 
 // Shared-memory operand descriptors, 128-byte swizzle (K-major: 8-row groups 1024 bytes apart;
 // M/N-major: chunks of 64 elements `lead` bytes apart, 8 contraction rows 1024 bytes apart).
@@ -142,7 +141,7 @@ struct ShrinkParams {
   __nv_bfloat16* terms;    // [M][num_terms][r]: s as a sum of bf16 terms
   int num_terms;
   int64_t M;
-  int n, r, kt, kt_per_rank, part, cluster, stages;
+  int n, r, kt, kt_per_rank, cluster, stages;
 };
 
 constexpr int kShrinkThreads = 192;   // TMA, MMA, four epilogue warps
@@ -234,12 +233,12 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
     const uint32_t id = idesc(r16, kTrans);
     for (int pass = 0; pass < walk.count && ok; ++pass) {
       if (lane == 0) {
-        for (int kp = kt0; kp < kt1 && ok; kp += p.part) {
+        for (int kp = kt0; kp < kt1 && ok; kp += kPartTiles) {
           ok = mbar_wait(&acc_empty[acc.stage], acc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitAccEmpty);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + acc.stage * acc_cols;
-          for (int kt = kp; kt < min(kp + p.part, kt1); ++kt) {
+          for (int kt = kp; kt < min(kp + kPartTiles, kt1); ++kt) {
             ok = mbar_wait(&full[c.stage], c.phase, abort_flag, &g_lora_error, kErrWaitFull);
             if (!ok) break;
             tc_fence_after();
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
     Cursor acc;
     for (int d = 0; d < walk.count; ++d) {
       const int a = walk.at(d);
-      for (int kp = kt0; kp < kt1; kp += p.part) {
+      for (int kp = kt0; kp < kt1; kp += kPartTiles) {
         mbar_wait(&acc_full[acc.stage], acc.phase, abort_flag, &g_lora_error, kErrWaitAccFull, 2 * kWaitLimitNs);
         tc_fence_after();
         __syncwarp();
@@ -765,7 +764,6 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
   p.s = s;
   p.terms = static_cast<__nv_bfloat16*>(terms);
   p.num_terms = num_terms;
-  p.part = num_terms == 3 ? kPartTilesF32 : kPartTiles;
   p.M = M;
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
