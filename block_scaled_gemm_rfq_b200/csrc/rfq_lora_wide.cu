@@ -24,6 +24,12 @@
 // adapters held the base back and cost 1.3 times those of one), are added to in shared memory and leave from
 // there by TMA.
 //
+// 16384 rows of one adapter of rank 16, 4096 -> 4096: both products 78 us, of which reading src and base and writing
+// out needs 63 (402 MB); alone shrink takes 36 us (134 MB, 3.8 TB/s: some 9 us of it are start, first loads and the
+// cluster's exchange) and expand 44 (268 MB, 6.1 TB/s).  4096 rows of 8 adapters of rank 64, 4096 -> 12288: 55 us where
+// chunks hold one adapter (floor 39), 73 to 80 where requests end inside them, each chunk then being passed over twice.
+// Stages of 128 elements of the contraction in shrink, for longer pieces of a row, were no faster.
+//
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, the others epilogue.  Every wait on an mbarrier
 // is bounded (rfq_ptx.cuh); after one that ran out the epilogue runs through its loops without
 // waiting, so that no warp is left alone at a barrier.  No TMA multicast.

@@ -342,10 +342,12 @@ rfq_status_t rfq_gemm_mxfp8(const void* qx_codes, const void* qx_scales,
  *   workspace   rfq_linear_ce_workspace_bytes(T, D, V, want_dh, want_dw) bytes, 256-byte
  *            aligned (want_* nonzero for the gradients that rfq_linear_ce_backward will be
  *            asked for; both zero: the forward pass alone).  Nothing in it is carried from
- *            one call to the next.
+ *            one call to the next; calls that may run at the same time (other streams, other
+ *            captured graphs) need workspaces of their own.
  * Logits are fp32 sums of exact products; the row maximum and sum are fp32, their last
  * join fp64.  dz is rounded to bf16 relative to the largest |dloss| (so a constant dloss
- * costs no rounding) and both gradients are fp32 sums rounded once to bf16.  A row with a
+ * costs no rounding), to 16 bits for T <= 16, and both gradients are fp32 sums rounded once
+ * to bf16.  A row with a
  * non-finite logit other than -inf has a non-finite loss.  T == 0 launches nothing, except
  * that dw is then zeroed.  Results do not depend on timing: no atomics.
  */
@@ -388,9 +390,12 @@ rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, cons
  *            NULL without da, hidden without db.
  *   workspace   256-byte aligned, rfq_lora_workspace_bytes(...) bytes (backward != 0: enough for
  *            both passes), rfq_linear_lora_workspace_bytes(...) for rfq_linear_lora.  Nothing in
- *            it is carried from one call to the next.
- * All sums are fp32.  s and ds enter the second product in bf16 for a bf16 result (two terms,
- * 16 bits, in dA and dB) and as three bf16 terms (24 bits) for an fp32 result.  rfq_linear_lora
+ *            it is carried from one call to the next; calls that may run at the same time need
+ *            workspaces of their own.
+ * All sums are fp32.  s and ds enter the second product as three bf16 terms (24 bits) for an
+ * fp32 result and, for a bf16 one, as two (16 bits) in dA, dB and short batches or one (8 bits)
+ * in y and dx of long ones (rows there are many, and none is off by more than its own rounding
+ * and that of its s).  rfq_linear_lora
  * with a bf16 Y rounds the projection to bf16 before the adapters are added, as any base is.
  * A row reads its own adapter alone: values that are not finite stay in their row (dx, y) and
  * adapter (dA, dB).  M == 0 launches nothing, except that da and db are then zeroed.  No
@@ -431,7 +436,8 @@ rfq_status_t rfq_linear_lora(const void* x_bf16, int64_t M, int64_t K, const voi
  *                 (RFQ_OUT_F32 or RFQ_OUT_BF16; an output has the type of its input)
  *   max_norm      >= 0; infinity never scales
  *   norm          device pointer to one fp32
- *   workspace     rfq_grad_clip_workspace_bytes(count) bytes, 256-byte aligned
+ *   workspace     rfq_grad_clip_workspace_bytes(count) bytes, 256-byte aligned; calls that may
+ *                 run at the same time need workspaces of their own
  * The host arrays are read before the call returns; a captured graph keeps the addresses in them.
  * 0 <= count <= 2^24, 2^42 elements in all; an empty list has norm 0.  Squares are summed in fp32
  * over 32 elements and in fp64 from there, so the norm of any finite fp32 or bf16 values is right
