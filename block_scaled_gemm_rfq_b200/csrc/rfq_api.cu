@@ -462,7 +462,7 @@ rfq_status_t rfq_lora(const void* x_bf16, int64_t M, int64_t K, const void* a_bf
   if (M == 0) return RFQ_OK;
   if (!x_bf16 || !a_bf16 || !b_bf16 || !scale || !ids || !y) return RFQ_ERR_INVALID_ARG;
   if (!aligned16(x_bf16) || !aligned16(a_bf16) || !aligned16(b_bf16) || !aligned_to(scale, 4) || !aligned_to(ids, 4) ||
-      !aligned16(base) || !aligned16(y) || !aligned_to(hidden, 4))
+      !aligned16(base) || !aligned16(y) || !aligned16(hidden))
     return RFQ_ERR_MISALIGNED;
   rfq_status_t st = check_workspace(workspace, workspace_bytes, rfq::lora_forward_workspace(M, K, N, rank, n_adapters));
   if (st != RFQ_OK) return st;
@@ -493,7 +493,7 @@ rfq_status_t rfq_lora_backward(const void* x_bf16, int64_t M, int64_t K, const v
   }
   if (!a_bf16 || !b_bf16 || !scale || !ids || !dy_bf16 || (da && !x_bf16) || (db && !hidden)) return RFQ_ERR_INVALID_ARG;
   if (!aligned16(x_bf16) || !aligned16(a_bf16) || !aligned16(b_bf16) || !aligned16(dy_bf16) || !aligned_to(scale, 4) ||
-      !aligned_to(ids, 4) || !aligned_to(hidden, 4))
+      !aligned_to(ids, 4) || !aligned16(hidden))
     return RFQ_ERR_MISALIGNED;
   st = check_workspace(workspace, workspace_bytes, rfq::lora_backward_workspace(M, K, N, rank, n_adapters));
   if (st != RFQ_OK) return st;
@@ -521,7 +521,7 @@ rfq_status_t rfq_linear_lora(const void* x_bf16, int64_t M, int64_t K, const voi
   if (M == 0) return RFQ_OK;
   if (!a_bf16 || !b_bf16 || !scale || !ids || !y) return RFQ_ERR_INVALID_ARG;
   if (!aligned16(a_bf16) || !aligned16(b_bf16) || !aligned_to(scale, 4) || !aligned_to(ids, 4) || !aligned16(y) ||
-      !aligned_to(hidden, 4))
+      !aligned16(hidden))
     return RFQ_ERR_MISALIGNED;
   rfq_status_t st = check_workspace(workspace, workspace_bytes,
                                     rfq_linear_lora_workspace_bytes(M, K, N, rank, n_adapters, use_residual));

@@ -338,7 +338,7 @@ rfq_status_t rfq_gemm_mxfp8(const void* qx_codes, const void* qx_scales,
  *            caller's, as dloss (e.g. 1 / counted rows).  Rows of dloss whose label is
  *            ignore_index are not looked at.
  *   dh_bf16  [T][D], dw_bf16 [V][D]: bf16, 16-byte aligned, fully overwritten; either may be
- *            NULL (a frozen head, or scoring).
+ *            NULL (a frozen head, or scoring).  No output overlaps an input or another output.
  *   workspace   rfq_linear_ce_workspace_bytes(T, D, V, want_dh, want_dw) bytes, 256-byte
  *            aligned (want_* nonzero for the gradients that rfq_linear_ce_backward will be
  *            asked for; both zero: the forward pass alone).  Nothing in it is carried from
@@ -384,7 +384,8 @@ rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, cons
  *   base     [M][N] in y_type, NULL for zeros, or y itself (then rows without an adapter are
  *            left as they were).  dx_base [M][K] in dx_type likewise.  Any other overlap of an
  *            output with an input is not allowed.
- *   hidden   [M][rank] fp32 or NULL: rfq_lora writes s, which rfq_lora_backward reads for dB
+ *   hidden   [M][rank] fp32, 16-byte aligned, or NULL: rfq_lora writes s, which
+ *            rfq_lora_backward reads for dB
  *   dx, da, db   any may be NULL.  da [n_adapters][rank][K] and db [n_adapters][N][rank] in
  *            grad_type, fully overwritten (zeros for an adapter without rows).  x_bf16 may be
  *            NULL without da, hidden without db.

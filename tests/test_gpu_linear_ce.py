@@ -363,3 +363,9 @@ def test_gradients_of_few_rows_are_rounded_once(rfq, T):
     dz = (torch.softmax(z, 1) - torch.nn.functional.one_hot(labels, V)) * dloss.double()[:, None]
     for got, want, terms in ((dh, dz @ w64, dz.abs() @ w64.abs()), (dw, dz.t() @ h64, dz.abs().t() @ h64.abs())):
         assert ((got.double() - want).abs() <= 2.0**-8 * want.abs() + 2.0**-14 * terms).all()
+
+
+@pytest.mark.parametrize("T,D,V", [(3, 40008, 300), (16, 65536, 72), (200, 65536, 264), (16, 8, 20001), (17, 8, 20001)])
+def test_more_tiles_than_units(rfq, T, D, V):
+    """Hidden states wider than a round of tiles, and both sides of the border between one and two terms of dz."""
+    test_forward_and_gradients(rfq, T, D, V)

@@ -156,3 +156,9 @@ def test_clipping_refuses_its_own(lib):
 def test_limits_match_the_header():
     src = open(rfq_build.INCLUDE + "/rfq.h").read()
     assert f"#define RFQ_LORA_MAX_RANK {rfq.LORA_MAX_RANK}\n" in src and f"#define RFQ_LORA_MAX_ADAPTERS {rfq.LORA_MAX_ADAPTERS}\n" in src
+
+
+@pytest.mark.parametrize("offset", [4, 8])
+def test_the_saved_rank_vectors_are_aligned(lib, offset):
+    """They are written and read 16 bytes at a time."""
+    assert lora(lib, hidden=A + offset) == 3 and lora_back(lib, hidden=A + offset) == 3 and linear_lora(lib, hidden=A + offset) == 3
