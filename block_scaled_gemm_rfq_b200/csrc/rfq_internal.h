@@ -83,9 +83,9 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
 // (P src) and s as bf16 terms [M][num_terms][r], the pool [n][r][C] or, transposed, [n][C][r].  expand:
 // out = base + Q s from the terms, the pool [n][C][r] or, transposed, [n][r][C].
 cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool trans, const int* ids, const float* scale, float* s,
-                                    void* terms, int num_terms, int64_t M, int64_t C, int64_t n, int64_t r, int num_sms,
+                                    void* terms, int num_terms, int* counts, int64_t M, int64_t C, int64_t n, int64_t r, int num_sms,
                                     void* encode_tiled, cudaStream_t stream);
-cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const void* pool, bool trans, const int* ids,
+cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const int* counts, const void* pool, bool trans, const int* ids,
                                     const void* base, void* out, bool f32, int64_t M, int64_t C, int64_t n, int64_t r,
                                     int num_sms, void* encode_tiled, cudaStream_t stream);
 

@@ -1360,7 +1360,7 @@ int outer_range(int64_t M, int64_t tiles) {
 }
 
 struct BackwardPlan {
-  size_t table, part, ds, s, part_a, part_b, present, bytes;
+  size_t table, part, counts, ds, s, part_a, part_b, present, bytes;
   int range, ranges;
 };
 // fp32 results take three terms, bf16 ones two; the workspace is sized for three.
@@ -1379,6 +1379,7 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
   const bool chunks = wide_ds(M, K, N, r, n);
   b.table = take(chunks ? 0 : static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4);
   b.part = take(chunks ? 0 : static_cast<size_t>(shrink_splits(M, N, n, &cs, &z)) * M * r * 4);
+  b.counts = take(chunks ? static_cast<size_t>(ceil_div(M, 128)) * 4 : 0);
   b.ds = take(static_cast<size_t>(3) * M * r * 2);
   b.s = take(static_cast<size_t>(3) * M * r * 2);
   b.part_a = take(static_cast<size_t>(b.ranges) * n * r * K * 4);
@@ -1390,9 +1391,11 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
 
 }  // namespace
 
-// Long batches leave s as bf16 terms; short ones need nothing (256 bytes, so that a workspace is one).
+// Long batches leave s as bf16 terms, and how many adapters each chunk has; short ones need nothing (256 bytes, so
+// that a workspace is one).
 size_t lora_forward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
-  return wide_forward(M, K, N, r, n, true) ? align256(static_cast<size_t>(3) * M * r * 2) : 256;   // whatever y's type
+  if (!wide_forward(M, K, N, r, n, true)) return 256;   // whatever y's type
+  return align256(static_cast<size_t>(3) * M * r * 2) + align256(static_cast<size_t>(ceil_div(M, 128)) * 4);
 }
 
 size_t lora_backward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
@@ -1405,9 +1408,10 @@ cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, con
   cudaError_t e;
   if (wide_forward(M, K, N, r, n, !y_bf16)) {
     const int terms = y_bf16 ? 1 : 3;
-    e = launch_lora_shrink_wide(x, a, false, ids, scale, hidden, ws, terms, M, K, n, r, num_sms, encode_tiled, stream);
+    int* counts = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(3) * M * r * 2));
+    e = launch_lora_shrink_wide(x, a, false, ids, scale, hidden, ws, terms, counts, M, K, n, r, num_sms, encode_tiled, stream);
     if (e != cudaSuccess) return e;
-    return launch_lora_expand_wide(ws, terms, b, false, ids, base, y, !y_bf16, M, N, n, r, num_sms, encode_tiled, stream);
+    return launch_lora_expand_wide(ws, terms, counts, b, false, ids, base, y, !y_bf16, M, N, n, r, num_sms, encode_tiled, stream);
   }
   ForwardParams p = {};
   p.x = static_cast<const __nv_bfloat16*>(x);
@@ -1445,6 +1449,7 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   uint8_t* base = static_cast<uint8_t*>(ws);
   float* part = reinterpret_cast<float*>(base + pl.part);
   int* table = reinterpret_cast<int*>(base + pl.table);
+  int* counts = reinterpret_cast<int*>(base + pl.counts);
   __nv_bfloat16* ds = reinterpret_cast<__nv_bfloat16*>(base + pl.ds);
   __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(base + pl.s);
   const bool chunks = wide_backward(M, K, N, r, n), chunks_ds = wide_ds(M, K, N, r, n);
@@ -1454,7 +1459,7 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   int splits = 1;
   cudaError_t e = cudaSuccess;
   if (dx != nullptr || da != nullptr) {
-    e = chunks_ds ? launch_lora_shrink_wide(dy, b, true, ids, scale, nullptr, ds, ds_terms, M, N, n, r, num_sms, encode_tiled, stream)
+    e = chunks_ds ? launch_lora_shrink_wide(dy, b, true, ids, scale, nullptr, ds, ds_terms, counts, M, N, n, r, num_sms, encode_tiled, stream)
                   : shrink(dy, b, ids, table, part, M, N, n, r, &splits, stream);
     if (e != cudaSuccess) return e;
   }
@@ -1480,7 +1485,7 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   const int s_terms = split_first ? ds_terms : terms;
   if (split_first && (e = split(s_terms)) != cudaSuccess) return e;
   if (dx != nullptr) {
-    e = chunks ? launch_lora_expand_wide(ds, ds_terms, a, true, ids, dx_base, dx, !dx_bf16, M, K, n, r, num_sms, encode_tiled, stream)
+    e = chunks ? launch_lora_expand_wide(ds, ds_terms, chunks_ds ? counts : nullptr, a, true, ids, dx_base, dx, !dx_bf16, M, K, n, r, num_sms, encode_tiled, stream)
                : expand(part, splits, scale, a, table, dx_base, dx, !dx_bf16, M, K, n, r, stream);
     if (e != cudaSuccess) return e;
   }

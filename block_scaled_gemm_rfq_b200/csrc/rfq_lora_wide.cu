@@ -26,8 +26,8 @@
 //
 // 16384 rows of one adapter of rank 16, 4096 -> 4096: both products 78 us, of which reading src and base and writing
 // out needs 63 (402 MB); alone shrink takes 36 us (134 MB, 3.8 TB/s: some 9 us of it are start, first loads and the
-// cluster's exchange) and expand 44 (268 MB, 6.1 TB/s).  4096 rows of 8 adapters of rank 64, 4096 -> 12288: 55 us where
-// chunks hold one adapter (floor 39), 73 to 80 where requests end inside them, each chunk then being passed over twice.
+// cluster's exchange) and expand 44 (268 MB, 6.1 TB/s).  4096 rows of 8 adapters of rank 64, 4096 -> 12288: 58 us where
+// chunks hold one adapter (floor 39), 61 to 66 where requests end inside them, which are then passed over twice.
 // Stages of 128 elements of the contraction in shrink, for longer pieces of a row, were no faster.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, the others epilogue.  Every wait on an mbarrier
@@ -146,6 +146,7 @@ struct ShrinkParams {
   float* s;                // [M][r] or nullptr
   __nv_bfloat16* terms;    // [M][num_terms][r]: s as a sum of bf16 terms
   int num_terms;
+  int* counts;             // [chunks]
   int64_t M;
   int n, r, kt, kt_per_rank, cluster, stages;
 };
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
   const int kt1 = min(p.kt, kt0 + p.kt_per_rank);
   Adapters walk;
   walk.load(p.ids, row0, p.M, p.n);
+  if (rank == 0 && threadIdx.x == 0) p.counts[row0 / kChunk] = walk.count;
 
   if (warp == 0) {
     Cursor c;
@@ -360,8 +362,11 @@ struct ExpandParams {
   int C;
   int n, r;
   int has_base, in_place;
-  int tiles, unit_tiles, col_units;   // column tiles in all, of one unit; units along the columns
+  int tiles;               // column tiles
+  int unit_tiles, col_units;   // without counts: tiles of a unit, units along the columns
   int64_t units;
+  int64_t chunks;
+  const int* counts;       // [chunks]: adapters of each, from shrink, or nullptr
   int s_stages, base_stages, q_stages;
 };
 
@@ -375,6 +380,91 @@ constexpr int kCols = kF32 ? 64 : 128;
 // output) or, for an fp32 output, as three (24 bits).
 template <bool kF32>
 constexpr int kTerms = kF32 ? 3 : 1;
+
+// What a CTA works on: runs of column tiles of one chunk each.
+// With one adapter (or where shrink left no counts) all chunks are alike: units of 4 to 16 tiles go round the CTAs.
+// Else a chunk is passed over once for each adapter in it, and the tiles of all chunks, one chunk after the other, are
+// cut into one part for each CTA, of equal work: 2 for a tile and 3 for each pass over it (a tile of two adapters took
+// 1.6 times the time of one).  Both products of 4096 rows of 8 requests that end inside chunks, rank 64, 4096 ->
+// 12288: 61 to 66 us with parts against 70 to 79 with units; 8 requests of 512 rows each 58 against 55; one
+// adapter 55 against 53.
+struct Place {
+  int64_t chunk;
+  int tile;
+};
+__device__ __forceinline__ int tile_work(const ExpandParams& p, int64_t chunk) {
+  const int c = p.counts[chunk];
+  return c == 0 && p.in_place ? 0 : 2 + 3 * c;
+}
+// Where this CTA's part begins and ends (end: the first tile that is not its own).  Every warp finds it for itself.
+__device__ __forceinline__ void cut_part(const ExpandParams& p, Place& begin, Place& end) {
+  const int lane = threadIdx.x & 31;
+  const int64_t per = (p.chunks + 31) / 32, first = min(p.chunks, lane * per), last = min(p.chunks, first + per);
+  int64_t sum = 0;
+#pragma unroll 4
+  for (int64_t c = first; c < last; ++c) sum += tile_work(p, c);
+  int64_t upto = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  const uint64_t total = __shfl_sync(0xffffffffu, upto, 31) * p.tiles, each = total / gridDim.x, more = total - each * gridDim.x;
+  const int64_t before = (upto - sum) * p.tiles;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint64_t b = blockIdx.x + e;
+    const int64_t at = static_cast<int64_t>(b * each + min(b, more));
+    const bool mine = at >= before && at < before + sum * p.tiles;
+    Place found = {p.chunks, 0};   // the end of the last run, or nothing to do at all
+    if (mine) {
+      int64_t from = before;
+      for (int64_t c = first; c < last; ++c) {
+        const int w = tile_work(p, c);
+        const int64_t next = from + static_cast<int64_t>(w) * p.tiles;
+        if (at < next) {
+          found = {c, (static_cast<int>(at - from) + w - 1) / w};
+          if (found.tile == p.tiles) found = {c + 1, 0};   // so that a part has no empty run but the last
+          break;
+        }
+        from = next;
+      }
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    const int source = who != 0 ? __ffs(who) - 1 : 0;
+    Place& place = e == 0 ? begin : end;
+    place.chunk = __shfl_sync(0xffffffffu, found.chunk, source);
+    place.tile = __shfl_sync(0xffffffffu, found.tile, source);
+  }
+}
+
+struct Runs {
+  Place begin, end;
+  int64_t at;   // the next chunk of the part, or the next unit
+  __device__ __forceinline__ explicit Runs(const ExpandParams& p) {
+    if (p.counts != nullptr) {
+      cut_part(p, begin, end);
+      at = begin.chunk;
+    } else {
+      at = blockIdx.x;
+    }
+  }
+  __device__ __forceinline__ bool next(const ExpandParams& p, int64_t& row0, int& t0, int& t1) {
+    if (p.counts != nullptr) {
+      if (at > end.chunk) return false;
+      t0 = at == begin.chunk ? begin.tile : 0;
+      t1 = at == end.chunk ? end.tile : p.tiles;
+      row0 = at++ * kChunk;
+      return t0 < t1;
+    }
+    if (at >= p.units) return false;
+    row0 = at / p.col_units * kChunk;
+    t0 = static_cast<int>(at % p.col_units) * p.unit_tiles;
+    t1 = min(p.tiles, t0 + p.unit_tiles);
+    at += gridDim.x;
+    return true;
+  }
+};
 
 template <bool kTrans, bool kF32>
 __host__ __device__ constexpr uint32_t expand_q_bytes(int r) {
@@ -441,16 +531,17 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
   griddep_launch_dependents();
   griddep_wait();
 
-  // A unit is a chunk of rows and a run of column tiles.  Where a chunk has no adapter and the
-  // base is the output, there is nothing to do; every role finds that out for itself.
+  // Where a chunk has no adapter and the base is the output, there is nothing to do; every role finds that out
+  // for itself.
+  Runs runs(p);
+  int64_t row0;
+  int t0, t1;
   Adapters walk;
   if (warp == 0) {
     Cursor sc, qc;
     Filled s_filled, q_filled;
     bool ok = true;
-    for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
-      const int64_t row0 = unit / p.col_units * kChunk;
-      const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
+    while (ok && runs.next(p, row0, t0, t1)) {
       walk.load(p.ids, row0, p.M, p.n);
       if (walk.count == 0) continue;
       if (lane == 0) {
@@ -499,9 +590,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
     Cursor bc;
     Filled b_filled;
     bool ok = p.has_base != 0;
-    for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
-      const int64_t row0 = unit / p.col_units * kChunk;
-      const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
+    while (ok && runs.next(p, row0, t0, t1)) {
       if (p.in_place) {
         walk.load(p.ids, row0, p.M, p.n);
         if (walk.count == 0) continue;
@@ -529,9 +618,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
     uint32_t last_phase = 0;
     bool ok = true;
     const uint32_t id = idesc(kN, kTrans);
-    for (int64_t unit = blockIdx.x; unit < p.units && ok; unit += gridDim.x) {
-      const int64_t row0 = unit / p.col_units * kChunk;
-      const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
+    while (ok && runs.next(p, row0, t0, t1)) {
       walk.load(p.ids, row0, p.M, p.n);
       if (walk.count == 0) continue;
       if (lane == 0) {
@@ -590,9 +677,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
     const int row = quad * 32 + lane;
     Cursor bc, acc;
     int release = -1;   // the stage whose tile may still be on its way out
-    for (int64_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
-      const int64_t row0 = unit / p.col_units * kChunk;
-      const int t0 = static_cast<int>(unit % p.col_units) * p.unit_tiles, t1 = min(p.tiles, t0 + p.unit_tiles);
+    while (runs.next(p, row0, t0, t1)) {
       walk.load(p.ids, row0, p.M, p.n);
       const bool any = walk.count > 0;
       if (!any && p.in_place) continue;
@@ -749,15 +834,16 @@ cudaError_t expand_typed(const ExpandMaps& maps, ExpandParams p, int num_sms, cu
   while (p.base_stages < 4 && (p.base_stages + 1) * 2 * kBox + p.q_stages * q <= room) ++p.base_stages;
   while (p.q_stages < 4 && p.base_stages * 2 * kBox + (p.q_stages + 1) * q <= room) ++p.q_stages;
   const size_t smem = 1024 + p.s_stages * s + p.base_stages * 2 * kBox + p.q_stages * q;
-  const int64_t grid = p.units < num_sms ? p.units : num_sms;
+  const int64_t parts = p.counts != nullptr ? p.chunks * p.tiles : p.units, grid = parts < num_sms ? parts : num_sms;
   return launch(rfq_lora_expand_wide_kernel<kTrans, kF32>, maps, p, grid, kExpandThreads, smem, 1, stream);
 }
 
 }  // namespace
 
-// s [M][r] (or nullptr) = scale (P src), P the pool [n][r][C] or (trans) [n][C][r]; terms [M][num_terms][r].
+// s [M][r] (or nullptr) = scale (P src), P the pool [n][r][C] or (trans) [n][C][r]; terms [M][num_terms][r];
+// counts [chunks of 128 rows]: adapters of each.
 cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool trans, const int* ids, const float* scale, float* s,
-                                    void* terms, int num_terms, int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream) {
+                                    void* terms, int num_terms, int* counts, int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
   ShrinkMaps maps;
   const uint32_t r16 = static_cast<uint32_t>((r + 15) / 16 * 16);
@@ -770,6 +856,7 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
   p.s = s;
   p.terms = static_cast<__nv_bfloat16*>(terms);
   p.num_terms = num_terms;
+  p.counts = counts;
   p.M = M;
   p.n = static_cast<int>(n);
   p.r = static_cast<int>(r);
@@ -797,8 +884,8 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
 }
 
 // out [M][C] = base + Q s, s from its terms (all of num_terms lie there; the output's type says how many
-// are taken), Q the pool [n][C][r] or (trans) [n][r][C].
-cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const void* pool, bool trans, const int* ids, const void* base, void* out, bool f32,
+// are taken), Q the pool [n][C][r] or (trans) [n][r][C].  counts: as left by shrink, or nullptr (only time depends on it).
+cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const int* counts, const void* pool, bool trans, const int* ids, const void* base, void* out, bool f32,
                                     int64_t M, int64_t C, int64_t n, int64_t r, int num_sms, void* encode_tiled, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
   ExpandMaps maps;
@@ -829,20 +916,21 @@ cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const void
   p.has_base = base != nullptr;
   p.in_place = base == out;
   p.tiles = static_cast<int>(ceil_div(C, cols));
+  p.chunks = ceil_div(M, kChunk);
+  p.counts = n > 1 ? counts : nullptr;
   // Column tiles of one unit: the length (4 to 16 tiles) that leaves the fewest tiles to the CTA
   // with the most, each unit charged a quarter of one more for the change of rows.
-  const int64_t chunks = ceil_div(M, kChunk);
   int64_t best = INT64_MAX;
   p.unit_tiles = p.tiles;
   for (int len = 4; len <= 16; ++len) {
-    const int64_t units = chunks * ceil_div(p.tiles, len), cost = ceil_div(units, num_sms) * (4 * len + 1);
+    const int64_t units = p.chunks * ceil_div(p.tiles, len), cost = ceil_div(units, num_sms) * (4 * len + 1);
     if (cost < best) {
       best = cost;
       p.unit_tiles = len;
     }
   }
   p.col_units = static_cast<int>(ceil_div(p.tiles, p.unit_tiles));
-  p.units = chunks * p.col_units;
+  p.units = p.chunks * p.col_units;
   if (trans) return f32 ? expand_typed<true, true>(maps, p, num_sms, stream) : expand_typed<true, false>(maps, p, num_sms, stream);
   return f32 ? expand_typed<false, true>(maps, p, num_sms, stream) : expand_typed<false, false>(maps, p, num_sms, stream);
 }
