@@ -88,6 +88,10 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
 cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const int* counts, const void* pool, bool trans, const int* ids,
                                     const void* base, void* out, bool f32, int64_t M, int64_t C, int64_t n, int64_t r,
                                     int num_sms, void* encode_tiled, cudaStream_t stream);
+constexpr int RFQ_LORA_OUTER_RANGE = 4096;   // rows of one range of launch_lora_outer_wide, at most (a multiple of 64)
+cudaError_t launch_lora_outer_wide(const void* ds, int ds_ld, const void* x, float* part_a, int64_t K, const void* s, int s_ld,
+                                   const void* dy, float* part_b, int64_t N, int terms, const int* ids, int* present, int64_t M,
+                                   int64_t n, int64_t r, int range, void* encode_tiled, cudaStream_t stream);
 
 // Global norm of a list of tensors (host arrays) and, where `scale`, the list scaled to it (rfq_clip.cu).
 // out == nullptr scales in place.

@@ -20,10 +20,9 @@
 //   outer    dA, dB: contraction over rows, split into row ranges
 //   reduce   sums the ranges in order and rounds
 //
-// Long batches take the shrink and expand of rfq_lora_wide.cu (tcgen05, 128 neighbouring
-// rows).  Here are those of short batches, where rows have adapters of their own and time goes
-// into reading the adapters' weights, and the adapters' gradients; all on warp-level m16n8k16
-// MMAs.  The rows of a 256-row chunk are grouped by adapter inside the CTA that works on them (no
+// Long batches take the kernels of rfq_lora_wide.cu (tcgen05; 128 neighbouring rows, or 64 of
+// one adapter).  Here are those of short batches, where rows have adapters of their own and time goes
+// into reading the adapters' weights; all on warp-level m16n8k16 MMAs.  The rows of a 256-row chunk are grouped by adapter inside the CTA that works on them (no
 // host knowledge of the ids, no order asked of them): groups of up to 16 rows share an
 // adapter's weights.
 //
@@ -1235,6 +1234,17 @@ bool wide_ds(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
   return wide_backward(M, K, N, r, n) && M * r > 20000;
 }
 
+// Whether the adapters' gradients of a long batch go over tcgen05 too (rfq_lora_wide.cu): 64 rows of one adapter a
+// stage, where the kernel here takes 32 and is bound by warp-level MMAs as the rank grows.  Measured, whole backward
+// pass, there against here, K = N = 4096: rank 32, 1500 rows 42 against 46 us; rank 64, 2000 rows 51 against 65, 2500
+// rows of 10 adapters 105 against 125, 300 rows of 4 66 against 51; rank 128, 400 rows 47 against 55, 2500 rows of 20
+// 287 against 339.  At rank 16 both read x and dy at nearly the same rate and the one here gathers rows that are
+// not neighbours faster: one adapter, 4000 rows 60 against 59, 8000 rows 86 against 88, 16384 rows 140 against 147; 4
+// adapters row by row, 16384 rows 373 against 286.
+bool wide_outer(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
+  return wide_backward(M, K, N, r, n) && (r > 16 ? M > 96 * n : n == 1 && M > 6000);
+}
+
 // CTAs that share the groups of one chunk: one for each there can be, up to `most` over all chunks.
 int64_t chunk_ctas(int64_t M, int64_t n, int64_t most) {
   const int64_t chunks = ceil_div(M, kChunk), rows = M < kChunk ? M : kChunk;
@@ -1359,6 +1369,15 @@ int outer_range(int64_t M, int64_t tiles) {
   return static_cast<int>(rows);
 }
 
+// The same for the tcgen05 kernel: one wave of one CTA per SM, 256 columns each.
+int outer_range_wide(int64_t M, int64_t tiles) {
+  const int64_t want = tiles < kPlanSms ? kPlanSms / tiles : 1;
+  int64_t rows = ceil_div(ceil_div(M, want), 64) * 64;
+  if (rows < 256) rows = 256;
+  if (rows > RFQ_LORA_OUTER_RANGE) rows = RFQ_LORA_OUTER_RANGE;
+  return static_cast<int>(rows);
+}
+
 struct BackwardPlan {
   size_t table, part, counts, ds, s, part_a, part_b, present, bytes;
   int range, ranges;
@@ -1374,7 +1393,7 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n
     at += align256(bytes);
     return o;
   };
-  b.range = outer_range(M, ceil_div(K, kOuterCols) + ceil_div(N, kOuterCols));
+  b.range = wide_outer(M, K, N, r, n) ? outer_range_wide(M, ceil_div(K, 256) + ceil_div(N, 256)) : outer_range(M, ceil_div(K, kOuterCols) + ceil_div(N, kOuterCols));
   b.ranges = static_cast<int>(ceil_div(M, b.range));
   const bool chunks = wide_ds(M, K, N, r, n);
   b.table = take(chunks ? 0 : static_cast<size_t>(ceil_div(M, kChunk)) * kTable * 4);
@@ -1491,40 +1510,39 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   }
   if (da == nullptr && db == nullptr) return e;
   if (!split_first && (e = split(s_terms)) != cudaSuccess) return e;
-  OuterParams o = {};
-  o.side[0].v = ds;
-  o.side[0].ld = static_cast<int>(ds_terms * r);
-  o.side[0].w = static_cast<const __nv_bfloat16*>(x);
-  o.side[0].part = reinterpret_cast<float*>(base + pl.part_a);
-  o.side[0].C = K;
-  o.side[0].tiles = da != nullptr ? static_cast<int>(ceil_div(K, kOuterCols)) : 0;
-  o.side[1].v = s;
-  o.side[1].ld = static_cast<int>(s_terms * r);
-  o.side[1].w = static_cast<const __nv_bfloat16*>(dy);
-  o.side[1].part = reinterpret_cast<float*>(base + pl.part_b);
-  o.side[1].C = N;
-  o.side[1].tiles = db != nullptr ? static_cast<int>(ceil_div(N, kOuterCols)) : 0;
-  o.ids = ids;
-  o.present = reinterpret_cast<int*>(base + pl.present);
-  o.M = M;
-  o.n = static_cast<int>(n);
-  o.r = static_cast<int>(r);
-  o.range = pl.range;
-  // Few CTAs and several adapters (short batches): the adapters are shared out too.
-  const int64_t ctas = static_cast<int64_t>(o.side[0].tiles + o.side[1].tiles) * pl.ranges;
-  int64_t zs = 2 * kPlanSms / ctas;
-  if (zs > n) zs = n;
-  if (zs < 1) zs = 1;
-  const dim3 grid(static_cast<unsigned>(o.side[0].tiles + o.side[1].tiles), static_cast<unsigned>(pl.ranges), static_cast<unsigned>(zs));
-  e = grad_bf16 ? outer_rank<2>(o, grid, stream) : outer_rank<3>(o, grid, stream);
+  float* part_a = reinterpret_cast<float*>(base + pl.part_a);
+  float* part_b = reinterpret_cast<float*>(base + pl.part_b);
+  int* present = reinterpret_cast<int*>(base + pl.present);
+  const int ds_ld = static_cast<int>(ds_terms * r), s_ld = static_cast<int>(s_terms * r);
+  if (wide_outer(M, K, N, r, n)) {
+    e = launch_lora_outer_wide(ds, ds_ld, da != nullptr ? x : nullptr, part_a, K, s, s_ld, db != nullptr ? dy : nullptr, part_b, N, terms, ids, present,
+                               M, n, r, pl.range, encode_tiled, stream);
+  } else {
+    OuterParams o = {};
+    o.side[0] = {ds, ds_ld, static_cast<const __nv_bfloat16*>(x), part_a, K, da != nullptr ? static_cast<int>(ceil_div(K, kOuterCols)) : 0};
+    o.side[1] = {s, s_ld, static_cast<const __nv_bfloat16*>(dy), part_b, N, db != nullptr ? static_cast<int>(ceil_div(N, kOuterCols)) : 0};
+    o.ids = ids;
+    o.present = present;
+    o.M = M;
+    o.n = static_cast<int>(n);
+    o.r = static_cast<int>(r);
+    o.range = pl.range;
+    // Few CTAs and several adapters (short batches): the adapters are shared out too.
+    const int64_t ctas = static_cast<int64_t>(o.side[0].tiles + o.side[1].tiles) * pl.ranges;
+    int64_t zs = 2 * kPlanSms / ctas;
+    if (zs > n) zs = n;
+    if (zs < 1) zs = 1;
+    const dim3 grid(static_cast<unsigned>(o.side[0].tiles + o.side[1].tiles), static_cast<unsigned>(pl.ranges), static_cast<unsigned>(zs));
+    e = grad_bf16 ? outer_rank<2>(o, grid, stream) : outer_rank<3>(o, grid, stream);
+  }
   if (e != cudaSuccess) return e;
   ReduceParams q = {};
   const int64_t jt = ceil_div(r, 32);
-  q.side[0] = {o.side[0].part, da, K, da != nullptr ? n * jt * ceil_div(K, 32) : 0, 0};
-  q.side[1] = {o.side[1].part, db, N, db != nullptr ? n * jt * ceil_div(N, 32) : 0, 1};
-  q.present = o.present;
-  q.n = o.n;
-  q.r = o.r;
+  q.side[0] = {part_a, da, K, da != nullptr ? n * jt * ceil_div(K, 32) : 0, 0};
+  q.side[1] = {part_b, db, N, db != nullptr ? n * jt * ceil_div(N, 32) : 0, 1};
+  q.present = present;
+  q.n = static_cast<int>(n);
+  q.r = static_cast<int>(r);
   q.ranges = pl.ranges;
   const dim3 rgrid(static_cast<unsigned>(q.side[0].tiles + q.side[1].tiles));
   return grad_bf16 ? launch(rfq_lora_reduce_kernel<false>, q, rgrid, 0, stream) : launch(rfq_lora_reduce_kernel<true>, q, rgrid, 0, stream);

@@ -1,9 +1,10 @@
-// rfq_lora_wide.cu -- the adapters' two products over long batches, on tcgen05.
+// rfq_lora_wide.cu -- the adapters' products over long batches, on tcgen05.
 //
 //   shrink   s[m] = scale_a P_a src[m]      rows x wide -> rank
 //   expand   out[m] = base[m] + Q_a s[m]    rank -> wide
+//   outer    dA, dB                         contraction over rows
 //
-// (rfq_lora.cu has the operator; P, Q = A, B going forward and B^T, A^T going back.)  Both are
+// (rfq_lora.cu has the operator; P, Q = A, B going forward and B^T, A^T going back.)  All are
 // bound by memory: 2 r flops for each element of src, or of base and out, with r <= 128.  What
 // the tensor cores buy here is instructions: with warp-level MMAs a [64 x 128] tile of expand
 // took 7400 warp instructions and ran at 0.7 TB/s; one thread's tcgen05.mma replaces the
@@ -777,6 +778,329 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
   }
 }
 
+// ---------------------------------------------------------------- outer
+// part[range][a][j][c] = sum over the range's rows of adapter a of v[m][j] w[m][c] for the two pairs (v, w) =
+// (ds', x) and (s', dy): products that contract over rows, v^T (rank along M, padded to 128) by w (256
+// columns along N), both M/N-major.  A CTA sorts its range's rows by adapter (a check where they are neighbours)
+// and takes 64 of one adapter a stage: by TMA where they are neighbours, else gathered (the last ones of an adapter too)
+// with 16-byte asynchronous copies that lay down the 128-byte swizzle themselves and zeros behind the last.  So rows
+// of other adapters never enter a product, in whatever order they come.  Bound by reading x and dy up to rank 64:
+// 8192 rows, 4096 -> 12288, rank 64 (268 MB) took 100 us less than on warp-level MMAs (242 -> 142 for the whole pass).
+// Roles: warps 0..2 copies, warp 3 MMA issuer, warps 4..11 epilogue (128 columns of a row of the rank each thread).
+struct OuterMaps {
+  CUtensorMap v[2], w[2];     // of the sides; boxes of 64 elements x 64 rows
+};
+struct OuterSide {
+  const __nv_bfloat16* v;     // [M][ld]: terms of r each, kT or more
+  int ld;
+  const __nv_bfloat16* w;     // [M][C]
+  float* part;                // [ranges][n][r][C]
+  int64_t C;
+  int tiles;                  // column tiles (0: not wanted)
+};
+struct OuterParams {
+  OuterSide side[2];
+  const int* ids;
+  int* present;               // [ranges][n]
+  int64_t M;
+  int n, r, range, stages;
+};
+
+constexpr int kOuterThreads = 384, kCopyWarps = 3;
+constexpr int kOuterN = 256, kOuterK = 64;                 // columns and rows of a stage
+constexpr int kOuterRange = RFQ_LORA_OUTER_RANGE;          // rows of one range, at most
+constexpr uint32_t kOuterChunk = kOuterK * 128u;           // 64 elements along M or N
+constexpr int kOuterPart = 4;                              // stages of one accumulation, see kPartTiles
+static_assert(RFQ_LORA_MAX_ADAPTERS <= 4096 && kOuterRange == 4096, "adapter and row in one key");
+constexpr int kNoAdapter = 1 << 24;
+
+template <int kT>
+__host__ __device__ constexpr uint32_t outer_stage_bytes(int r) {
+  return (kOuterN / 64 + kT * (r > 64 ? 2 : 1)) * kOuterChunk;
+}
+// First of keys[0 .. count) that is not below `key`.
+__device__ __forceinline__ int lower_bound(const int* keys, int count, int key) {
+  int lo = 0, hi = count;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (keys[mid] < key) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {   // zeros (and no read) where not
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+// Waits until at most `groups` (1 to 3, else 0) of this thread's groups of copies are on their way.
+__device__ __forceinline__ void copy_wait(int groups) {
+  if (groups == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (groups == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (groups == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <int kT>
+__global__ void __launch_bounds__(kOuterThreads, 1) rfq_lora_outer_wide_kernel(const __grid_constant__ OuterMaps maps,
+                                                                                const OuterParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int keys[kOuterRange];
+  __shared__ uint64_t full[4], empty[4], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int* abort_flag = &abort_word;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t stage_bytes = outer_stage_bytes<kT>(p.r);
+  const int chunks = p.r > 64 ? 2 : 1;
+
+  if (tid == 0) {
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&full[s], kCopyWarps);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);
+    }
+    mbar_init(&drained, 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  if (warp == kCopyWarps) {
+    tmem_alloc_g<1>(&tmem_slot, 2 * kOuterN);
+    tmem_relinquish_g<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  int tile = static_cast<int>(blockIdx.x);
+  const bool second = tile >= p.side[0].tiles;
+  if (second) tile -= p.side[0].tiles;
+  const OuterSide s = second ? p.side[1] : p.side[0];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * p.range;
+  const int count = static_cast<int>(min(static_cast<int64_t>(p.range), p.M - row0));
+  const int64_t c0 = static_cast<int64_t>(tile) * kOuterN;
+
+  // The range's rows by adapter, then row: keys (adapter << 12) + row, rows without one last.
+  int size = 64;
+  while (size < count) size <<= 1;
+  for (int i = tid; i < size; i += kOuterThreads) {
+    int key = 0x7fffffff;
+    if (i < count) {
+      const int id = p.ids[row0 + i];
+      key = (id >= 0 && id < p.n ? id << 12 : kNoAdapter) + i;
+    }
+    keys[i] = key;
+  }
+  __syncthreads();
+  bool sorted = true;
+  for (int i = tid + 1; i < size; i += kOuterThreads) sorted = sorted && keys[i - 1] <= keys[i];
+  if (!__syncthreads_and(sorted)) {
+    for (int k = 2; k <= size; k <<= 1)
+      for (int j = k >> 1; j > 0; j >>= 1) {   // a bitonic sort
+        for (int i = tid; i < size / 2; i += kOuterThreads) {
+          const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1)), hi = lo | j;
+          const int a = keys[lo], b = keys[hi];
+          if ((a > b) == ((lo & k) == 0)) {
+            keys[lo] = b;
+            keys[hi] = a;
+          }
+        }
+        __syncthreads();
+      }
+  }
+  const int rows = lower_bound(keys, count, kNoAdapter);   // rows with an adapter
+  if (blockIdx.x == 0)
+    for (int i = tid; i < p.n; i += kOuterThreads) {
+      const int at = lower_bound(keys, rows, i << 12);
+      p.present[static_cast<int64_t>(blockIdx.y) * p.n + i] = at < rows && (keys[at] >> 12) == i;
+    }
+
+  if (warp < kCopyWarps) {
+    // ------------------------------------------------------------ copies
+    const int lag = p.stages - 1;   // gathered stages that are on their way while one more is asked for
+    const int per = kT * p.r / 8, r8 = p.r / 8;
+    const bool has_col = c0 + 8 * lane < s.C;
+    const __nv_bfloat16* w = has_col ? s.w + row0 * s.C + c0 + 8 * lane : s.w;   // (read only where has_col)
+    const __nv_bfloat16* v = s.v + row0 * s.ld + 8 * lane;
+    uint32_t v_to[2], v_q[2];       // this lane's pieces of a row of v: chunk, piece in its 128 bytes
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = lane + 32 * u, e = i / r8, j = i - e * r8;
+      v_to[u] = (e * chunks + (j >> 3)) * kOuterChunk;
+      v_q[u] = j & 7;
+    }
+    const CUtensorMap* map_v = &maps.v[second];
+    const CUtensorMap* map_w = &maps.w[second];
+    Cursor c, out;
+    Filled filled;
+    int pending = 0;                // gathered stages not yet handed over
+    bool ok = true;
+    auto give = [&]() {             // the oldest of them has landed
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[out.stage]);
+      out.next(p.stages);
+      --pending;
+    };
+    for (int first = 0; first < rows && ok;) {
+      const int end = lower_bound(keys, rows, ((keys[first] >> 12) + 1) << 12);
+      for (int at = first; at < end; at += kOuterK) {
+        ok = mbar_wait(&empty[c.stage], c.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitEmpty);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* stage = smem + c.stage * stage_bytes;
+        filled.add(c);
+        if (at + kOuterK <= end && keys[at + kOuterK - 1] - keys[at] == kOuterK - 1) {
+          copy_wait(0);
+          while (pending > 0) give();
+          if (lane == 0) {
+            if (warp == 0) {
+              const int row = static_cast<int>(row0) + (keys[at] & (kOuterRange - 1));
+              mbar_arrive_expect_tx(&full[c.stage], stage_bytes);
+              for (int e = 0; e < kT; ++e)
+                for (int h = 0; h < chunks; ++h)
+                  tma_load_2d(stage + (e * chunks + h) * kOuterChunk, map_v, &full[c.stage], e * p.r + 64 * h, row);
+#pragma unroll
+              for (int h = 0; h < kOuterN / 64; ++h)
+                tma_load_2d(stage + (kT * chunks + h) * kOuterChunk, map_w, &full[c.stage], static_cast<int>(c0) + 64 * h, row);
+            } else {
+              mbar_arrive(&full[c.stage]);
+            }
+          }
+          out.next(p.stages);
+        } else {
+          const uint32_t sv = smem_addr(stage), sw = sv + (kT * chunks + (lane >> 3)) * kOuterChunk;
+          // A lane looks up one row for all: their addresses then come by shuffles, not one load after the other.
+          const int mine = warp + kCopyWarps * lane;
+          const int key = mine < kOuterK && at + mine < end ? keys[at + mine] & (kOuterRange - 1) : -1;
+          const uint32_t c_off = static_cast<uint32_t>(s.C), ld = static_cast<uint32_t>(s.ld);
+#pragma unroll 8
+          for (int k = 0; k < (kOuterK + kCopyWarps - 1) / kCopyWarps; ++k) {
+            const int m = warp + kCopyWarps * k, row = __shfl_sync(0xffffffffu, key, k);
+            if (m >= kOuterK) break;
+            const bool has = row >= 0;
+            const uint64_t r = has ? row : 0;
+            copy16(sw + m * 128 + (((lane & 7) ^ (m & 7)) << 4), w + r * c_off, has && has_col);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (lane + 32 * u < per) copy16(sv + v_to[u] + m * 128 + ((v_q[u] ^ (m & 7)) << 4), v + r * ld + 256 * u, has);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (++pending > lag) {
+            copy_wait(lag);
+            give();
+          }
+        }
+        c.next(p.stages);
+      }
+      first = end;
+    }
+    copy_wait(0);
+    while (pending > 0) give();
+    if (tid == 0) filled.drain(full, p.stages);
+    __syncwarp();
+  } else if (warp == kCopyWarps) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t(kOuterN >> 3) << 17) | ((128u >> 4) << 24);
+      Cursor c, acc;
+      bool ok = true;
+      for (int first = 0; first < rows && ok;) {
+        const int end = lower_bound(keys, rows, ((keys[first] >> 12) + 1) << 12);
+        const int iters = (end - first + kOuterK - 1) / kOuterK;
+        for (int i0 = 0; i0 < iters && ok; i0 += kOuterPart) {
+          ok = mbar_wait(&acc_empty[acc.stage], acc.phase ^ 1u, abort_flag, &g_lora_error, kErrWaitAccEmpty);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + acc.stage * kOuterN;
+          for (int i = i0; i < min(i0 + kOuterPart, iters); ++i) {
+            ok = mbar_wait(&full[c.stage], c.phase, abort_flag, &g_lora_error, kErrWaitFull);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sv = smem_addr(smem) + c.stage * stage_bytes, sw = sv + kT * chunks * kOuterChunk;
+            const uint64_t db = mn_major_desc(sw, kOuterChunk);
+#pragma unroll
+            for (uint32_t q = 0; q < kOuterK / 16; ++q)
+#pragma unroll
+              for (int e = kT - 1; e >= 0; --e)   // smallest terms first
+                // Up to rank 64 the other half of M is whatever lies behind (inside the stage): its results are not kept.
+                mma_bf16_g<1>(d, mn_major_desc(sv + e * chunks * kOuterChunk, kOuterChunk) + 128 * q, db + 128 * q, id,
+                              (i != i0 || q != 0 || e != kT - 1) ? 1u : 0u);
+            tc_commit(&empty[c.stage]);
+            c.next(p.stages);
+          }
+          if (!ok) break;
+          tc_commit(&acc_full[acc.stage]);
+          acc.next(2);
+        }
+        first = end;
+      }
+      if (!ok) {   // teardown after an abort: wait for the MMAs already issued
+        tc_commit(&drained);
+        int never = 0;
+        mbar_wait(&drained, 0, &never, &g_lora_error, kErrWaitDrain);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int j = quad * 32 + lane;
+    const bool here = quad * 32 < p.r;
+    Cursor acc;
+    bool ok = true;
+    for (int first = 0; first < rows && ok;) {
+      const int a = keys[first] >> 12;
+      const int end = lower_bound(keys, rows, (a + 1) << 12);
+      const int iters = (end - first + kOuterK - 1) / kOuterK;
+      float sum[128];
+      for (int i0 = 0; i0 < iters && ok; i0 += kOuterPart) {
+        ok = mbar_wait(&acc_full[acc.stage], acc.phase, abort_flag, &g_lora_error, kErrWaitAccFull, 2 * kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (here) {
+          const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc.stage * kOuterN + half * 128;
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            uint32_t u[8];
+            tmem_load_32x32b_x8(at + c, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[c + i] = i0 == 0 ? __uint_as_float(u[i]) : sum[c + i] + __uint_as_float(u[i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[acc.stage]);
+        acc.next(2);
+      }
+      if (ok && j < p.r) {
+        float* out = s.part + ((static_cast<int64_t>(blockIdx.y) * p.n + a) * p.r + j) * s.C;
+        const int64_t col = c0 + half * 128;
+#pragma unroll
+        for (int c = 0; c < 128; c += 4)
+          if (col + c < s.C) *reinterpret_cast<float4*>(out + col + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+      }
+      __syncwarp();
+      first = end;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kCopyWarps) {
+    __syncwarp();
+    tmem_dealloc_g<1>(tmem, 2 * kOuterN);
+  }
+}
+
 // ---------------------------------------------------------------- host
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -933,6 +1257,46 @@ cudaError_t launch_lora_expand_wide(const void* terms, int num_terms, const int*
   p.units = p.chunks * p.col_units;
   if (trans) return f32 ? expand_typed<true, true>(maps, p, num_sms, stream) : expand_typed<true, false>(maps, p, num_sms, stream);
   return f32 ? expand_typed<false, true>(maps, p, num_sms, stream) : expand_typed<false, false>(maps, p, num_sms, stream);
+}
+
+// part of both sides (v [M][ld] of `terms` terms, w [M][C]; a side without w is not wanted), present [ranges][n].
+cudaError_t launch_lora_outer_wide(const void* ds, int ds_ld, const void* x, float* part_a, int64_t K, const void* s, int s_ld, const void* dy,
+                                   float* part_b, int64_t N, int terms, const int* ids, int* present, int64_t M, int64_t n, int64_t r, int range,
+                                   void* encode_tiled, cudaStream_t stream) {
+  EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
+  OuterMaps maps = {};
+  if (x != nullptr && !(encode_bf16_map(encode, &maps.v[0], ds, M, ds_ld, ds_ld, kOuterK) && encode_bf16_map(encode, &maps.w[0], x, M, K, K, kOuterK)))
+    return cudaErrorInvalidValue;
+  if (dy != nullptr && !(encode_bf16_map(encode, &maps.v[1], s, M, s_ld, s_ld, kOuterK) && encode_bf16_map(encode, &maps.w[1], dy, M, N, N, kOuterK)))
+    return cudaErrorInvalidValue;
+  OuterParams p = {};
+  p.side[0] = {static_cast<const __nv_bfloat16*>(ds), ds_ld, static_cast<const __nv_bfloat16*>(x), part_a, K, x != nullptr ? static_cast<int>(ceil_div(K, kOuterN)) : 0};
+  p.side[1] = {static_cast<const __nv_bfloat16*>(s), s_ld, static_cast<const __nv_bfloat16*>(dy), part_b, N, dy != nullptr ? static_cast<int>(ceil_div(N, kOuterN)) : 0};
+  p.ids = ids;
+  p.present = present;
+  p.M = M;
+  p.n = static_cast<int>(n);
+  p.r = static_cast<int>(r);
+  p.range = range;
+  const uint32_t stage = terms == 3 ? outer_stage_bytes<3>(p.r) : outer_stage_bytes<2>(p.r);
+  p.stages = static_cast<int>((kSmemLimit - 1024 - 17 * 1024) / stage);   // 2 to 4 (17 KiB: the keys and barriers)
+  if (p.stages > 4) p.stages = 4;
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * stage;
+  auto kernel = terms == 3 ? rfq_lora_outer_wide_kernel<3> : rfq_lora_outer_wide_kernel<2>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.side[0].tiles + p.side[1].tiles), static_cast<unsigned>(ceil_div(M, range)));
+  cfg.blockDim = dim3(kOuterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see griddep_wait()
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, maps, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t read_and_clear_lora_error(unsigned int* value) {

@@ -1,6 +1,7 @@
 """Adapters over long batches: sizes from which the two products go by chunks of 128 neighbouring rows, forward (about
 rows x (rank + 8) x (K + N) above 3.3e8), backward (rows x rank x (K + N) above 6e7), and there with ds by groups (up to
-20000 rows x rank) or by chunks too.  Same definition, same bounds as for short ones."""
+20000 rows x rank) or by chunks too, and the adapters' gradients by stages of 64 rows of one adapter (from rank 24 and
+96 rows for each adapter on, or one adapter and 6000 rows).  Same definition, same bounds as for short ones."""
 import pytest
 import torch
 
@@ -10,7 +11,8 @@ pytestmark = pytest.mark.gpu
 
 LONG = [(2500, 2056, 2568, 24, 4, "runs"), (1201, 1032, 5128, 40, 3, "runs"), (700, 4104, 4096, 56, 2, "mixed"), (2000, 2048, 2056, 128, 1, "one"),
         (520, 5000, 4008, 128, 12, "mixed"), (300, 4104, 4104, 64, 4, "mixed"), (1111, 5120, 3000, 8, 3, "runs"), (129, 8008, 8200, 72, 2, "runs"),
-        (4100, 3080, 1544, 16, 9, "runs"), (68, 8200, 8200, 80, 1, "one")]
+        (4100, 3080, 1544, 16, 9, "runs"), (68, 8200, 8200, 80, 1, "one"),
+        (8200, 520, 264, 16, 1, "one"), (5000, 8200, 8200, 24, 2, "mixed"), (3000, 264, 2056, 104, 3, "runs")]
 
 
 @pytest.fixture(scope="module")
@@ -30,7 +32,7 @@ def test_forward_and_gradients(rfq, M, K, N, r, n, kind, out, grad):
         check(name, t, want[name])
 
 
-SOME = [LONG[1], LONG[2], LONG[5], LONG[6]]
+SOME = [LONG[1], LONG[2], LONG[5], LONG[6], LONG[12]]
 
 
 @pytest.mark.parametrize("M,K,N,r,n,kind", SOME)
@@ -74,7 +76,7 @@ def test_each_gradient_alone_is_the_same_bits(rfq, M, K, N, r, n, kind):
             assert (t is not None) == w and (t is None or torch.equal(t, all_[name])), name
 
 
-@pytest.mark.parametrize("M,K,N,r,n,kind", [LONG[0], LONG[5], LONG[6]])
+@pytest.mark.parametrize("M,K,N,r,n,kind", [LONG[0], LONG[5], LONG[6], LONG[12]])
 def test_values_that_are_not_finite_stay_where_they_are(rfq, M, K, N, r, n, kind):
     c = make(M, K, N, r, n, kind, seed=10)
     c["ids"][c["ids"] == 1] = 0
