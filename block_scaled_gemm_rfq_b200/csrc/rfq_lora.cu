@@ -880,9 +880,9 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_split_kernel(const SplitPar
 // ---------------------------------------------------------------- outer
 // part[range][a][j][c] = sum over the range's rows of adapter a of v[m][j] w[m][c], for the two
 // pairs (v, w) = (ds', x) and (s', dy).
-// Bound by reading x and dy: 16384 rows of one adapter of rank 16 (4096 -> 4096, 268 MB) take 60 us, 4.5 TB/s with
-// L1 at 66 % (the transposing loads); stages of 64 rows with two CTAs an SM, in
-// place of 32 with three, took 8 us more.
+// Bound by reading x and dy at small ranks: 16384 rows of rank 16 (4096 -> 4096, 268 MB) take 61 us, 4.5 TB/s with
+// L1 at 66 % (the transposing loads); stages of 64 rows with two CTAs an SM, in place of 32 with three, took 8 us
+// more.  By the MMAs at large ones, which rfq_lora_wide.cu takes where batches are long.
 constexpr int kOuterCols = 128;
 constexpr int kOuterRows = 32;        // rows of one stage
 constexpr int kMaxRange = 4096;       // rows of one range

@@ -784,8 +784,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
 // columns along N), both M/N-major.  A CTA sorts its range's rows by adapter (a check where they are neighbours)
 // and takes 64 of one adapter a stage: by TMA where they are neighbours, else gathered (the last ones of an adapter too)
 // with 16-byte asynchronous copies that lay down the 128-byte swizzle themselves and zeros behind the last.  So rows
-// of other adapters never enter a product, in whatever order they come.  Bound by reading x and dy up to rank 64:
-// 8192 rows, 4096 -> 12288, rank 64 (268 MB) took 100 us less than on warp-level MMAs (242 -> 142 for the whole pass).
+// of other adapters never enter a product, in whatever order they come.  Bound by reading x and dy: 8192
+// rows, 4096 -> 12288, rank 64 (268 MB) take 64 us, 4.3 TB/s with the tensor pipe 70 % active, 100 us less than on
+// warp-level MMAs.  Two terms of up to rank 64 in the two halves of one MMA's M: half the MMAs, but twice the partial
+// sums, 147 against 142 us for the whole backward pass.  Seven copy warps for rows that are not neighbours: those 7 %
+// faster, neighbours 2 to 4 % slower.
 // Roles: warps 0..2 copies, warp 3 MMA issuer, warps 4..11 epilogue (128 columns of a row of the rank each thread).
 struct OuterMaps {
   CUtensorMap v[2], w[2];     // of the sides; boxes of 64 elements x 64 rows
