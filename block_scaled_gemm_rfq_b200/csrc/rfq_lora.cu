@@ -1123,62 +1123,106 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
 }
 
 // ---------------------------------------------------------------- reduce
-// dA[a][j][k] and dB[a][c][j] = the ranges' sums in order; an adapter without rows gets zeros.
-// One block per 32 x 32 tile of [r][C] of one adapter; dB is written transposed.
+// dA[a][j][k] and dB[a][c][j] = the ranges' sums in order; an adapter without rows gets zeros.  A block takes
+// kReduceTile elements of one adapter's dA, in the order in which they lie, or all of the rank for 32 columns of its dB,
+// which is written transposed: through shared memory, so that both sides move in whole lines, and each
+// thread's loads are under way together (one element after the other they took 43 us for the 17 MB of 5 adapters of
+// rank 104, 6640 -> 9296, against 8.5 now).
 struct ReduceSide {
   const float* part;
   void* out;
   int64_t C;
-  int64_t tiles;              // blocks of this side
-  int transposed;
+  int64_t tiles;              // blocks of one adapter
 };
 struct ReduceParams {
-  ReduceSide side[2];
+  ReduceSide side[2];         // dA, dB
   const int* present;
   int n, r, ranges;
 };
+constexpr int kReduceVecs = 4, kReduceTile = kThreads * kReduceVecs * 4;
 
 template <bool kF32>
-__device__ __forceinline__ void put(void* out, int64_t at, float v) {
-  if constexpr (kF32) static_cast<float*>(out)[at] = v;
-  else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+__device__ __forceinline__ void put4(void* out, int64_t at, const float4& v) {   // at: a multiple of 4
+  if constexpr (kF32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
 }
 
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) rfq_lora_reduce_kernel(const ReduceParams p) {
-  __shared__ float tile[32][33];
+  __shared__ float tile[RFQ_LORA_MAX_RANK][33];
   griddep_launch_dependents();
   griddep_wait();
+  const int tid = threadIdx.x;
   int64_t b = blockIdx.x;
-  const int which = b >= p.side[0].tiles;
-  if (which) b -= p.side[0].tiles;
-  const ReduceSide s = which ? p.side[1] : p.side[0];
-  const int64_t ct = ceil_div(s.C, 32);
-  const int jt = (p.r + 31) / 32;
-  const int a = static_cast<int>(b / (ct * jt));
-  const int64_t rest = b - a * ct * jt;
-  const int j0 = static_cast<int>(rest / ct) * 32;
-  const int64_t c0 = (rest % ct) * 32;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  for (int y = ty; y < 32; y += 8) {
-    float v = 0.f;
-    const int j = j0 + y;
-    const int64_t c = c0 + tx;
-    if (j < p.r && c < s.C)
-      for (int g = 0; g < p.ranges; ++g)
-        if (p.present[static_cast<int64_t>(g) * p.n + a]) v += s.part[((static_cast<int64_t>(g) * p.n + a) * p.r + j) * s.C + c];
-    if (s.transposed) tile[y][tx] = v;
-    else if (j < p.r && c < s.C) put<kF32>(s.out, (static_cast<int64_t>(a) * p.r + j) * s.C + c, v);
-  }
-  if (s.transposed) {
-    __syncthreads();
-    for (int y = ty; y < 32; y += 8) {
-      const int64_t c = c0 + y;
-      const int j = j0 + tx;
-      if (j < p.r && c < s.C) put<kF32>(s.out, (static_cast<int64_t>(a) * s.C + c) * p.r + j, tile[tx][y]);
+  const bool second = b >= p.side[0].tiles * p.n;
+  if (second) b -= p.side[0].tiles * p.n;
+  const ReduceSide s = second ? p.side[1] : p.side[0];
+  const int a = static_cast<int>(b / s.tiles);
+  const int64_t t = b - a * s.tiles;
+  const int64_t size = p.r * s.C;              // of one adapter
+  const float* part = s.part + a * size;
+  const int64_t step = static_cast<int64_t>(p.n) * size;
+  // This thread's vectors: places in the adapter's [r][C], negative where there is none.  (A vector of four
+  // lies in one row: C is a multiple of 8.)
+  int64_t at[kReduceVecs];
+  float4 sum[kReduceVecs];
+#pragma unroll
+  for (int u = 0; u < kReduceVecs; ++u) {
+    sum[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int i = tid + kThreads * u;
+    if (!second) {
+      at[u] = t * kReduceTile + 4 * i;
+      if (at[u] >= size) at[u] = -1;
+    } else {
+      const int64_t c = t * 32 + (i & 7) * 4;
+      at[u] = i >> 3 < p.r && c < s.C ? (i >> 3) * s.C + c : -1;
     }
   }
+  for (int g = 0; g < p.ranges; ++g) {
+    if (!p.present[static_cast<int64_t>(g) * p.n + a]) continue;
+    const float* from = part + g * step;
+    float4 v[kReduceVecs];
+#pragma unroll
+    for (int u = 0; u < kReduceVecs; ++u) v[u] = at[u] >= 0 ? *reinterpret_cast<const float4*>(from + at[u]) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kReduceVecs; ++u) {
+      sum[u].x += v[u].x;
+      sum[u].y += v[u].y;
+      sum[u].z += v[u].z;
+      sum[u].w += v[u].w;
+    }
+  }
+  if (!second) {
+#pragma unroll
+    for (int u = 0; u < kReduceVecs; ++u)
+      if (at[u] >= 0) put4<kF32>(s.out, a * size + at[u], sum[u]);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < kReduceVecs; ++u) {
+    const int i = tid + kThreads * u;
+    if (i >> 3 < p.r) {
+      float* to = &tile[i >> 3][(i & 7) * 4];
+      to[0] = sum[u].x;
+      to[1] = sum[u].y;
+      to[2] = sum[u].z;
+      to[3] = sum[u].w;
+    }
+  }
+  __syncthreads();
+  const int cols = static_cast<int>(min(static_cast<int64_t>(32), s.C - t * 32)), r4 = p.r / 4;
+  const int64_t base = a * size + t * 32 * p.r;
+  for (int i = tid; i < cols * r4; i += kThreads) {
+    const int c = i / r4, j = (i - c * r4) * 4;
+    put4<kF32>(s.out, base + 4 * i, make_float4(tile[j][c], tile[j + 1][c], tile[j + 2][c], tile[j + 3][c]));
+  }
 }
+static_assert(kThreads * kReduceVecs >= RFQ_LORA_MAX_RANK * 8, "a block's vectors cover the rank for 32 columns");
 
 // ---------------------------------------------------------------- host
 constexpr int kPlanSms = 148;   // the cut does not depend on the device that runs it
@@ -1537,14 +1581,13 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   }
   if (e != cudaSuccess) return e;
   ReduceParams q = {};
-  const int64_t jt = ceil_div(r, 32);
-  q.side[0] = {part_a, da, K, da != nullptr ? n * jt * ceil_div(K, 32) : 0, 0};
-  q.side[1] = {part_b, db, N, db != nullptr ? n * jt * ceil_div(N, 32) : 0, 1};
+  q.side[0] = {part_a, da, K, da != nullptr ? ceil_div(r * K, kReduceTile) : 0};
+  q.side[1] = {part_b, db, N, db != nullptr ? ceil_div(N, 32) : 0};
   q.present = present;
   q.n = static_cast<int>(n);
   q.r = static_cast<int>(r);
   q.ranges = pl.ranges;
-  const dim3 rgrid(static_cast<unsigned>(q.side[0].tiles + q.side[1].tiles));
+  const dim3 rgrid(static_cast<unsigned>((q.side[0].tiles + q.side[1].tiles) * n));
   return grad_bf16 ? launch(rfq_lora_reduce_kernel<false>, q, rgrid, 0, stream) : launch(rfq_lora_reduce_kernel<true>, q, rgrid, 0, stream);
 }
 
