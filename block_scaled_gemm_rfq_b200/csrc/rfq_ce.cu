@@ -9,7 +9,7 @@
 //
 // A logits matrix would be T x V; here a [256 x 256] tile of it exists only as the fp32
 // accumulator of the tensor cores (TMEM).  Forward: the epilogue reduces each tile row to
-// (max, sum of exponentials) over 128 columns and a second kernel joins those parts.
+// (max, sum of exponentials) over 128 (or 32) columns and a second kernel joins those parts.
 // Backward: for one piece of the vocabulary at a time the logits are computed again,
 // turned into dz with the known lse, rounded to bf16 into a workspace of bounded size,
 // and multiplied with w (dh, accumulated over the pieces in fp32) and h (dw, complete).
@@ -26,7 +26,7 @@
 // Roles (per CTA): warp 0 TMA producer, warp 1 MMA issuer (leader CTA of a pair),
 // warps 2..9 epilogue.  Two 256-column accumulators, so that the epilogue of a tile runs
 // under the mainloop of the next.  CTA pairs (256 x 256 tiles) above 128 rows, single
-// CTAs (128 x 256) up to 128, where the rest of a pair's rows would be padding.
+// CTAs (128 x 256, or 128 x 64 against small heads) up to 128, where the rest of a pair's rows would be padding.
 // Every wait on an mbarrier is bounded (rfq_ptx.cuh).  No TMA multicast.
 //
 // Bounds and rates.  With many rows the tensor cores bound all four products: 4096 x 4096 against 8192
@@ -35,8 +35,8 @@
 // 2048 x 4096 against 131072 entries take 1.65 ms (1.33 PFLOP/s).  The backward pass computes the logits
 // once more, a fourth product to the three that training needs (4096 rows against 32768 x 4096: 3.3 ms forward and
 // backward, 1.33 PFLOP/s over the four): the price of holding no T x V matrix between the passes, 537 MB in fp32
-// there.  With few rows reading the head bounds them: 1 row against 131072 x 4096 takes 212 us, 5.1 TB/s; 8
-// rows against 32003 x 1024 22 us, half of it the two kernels' start and end.
+// there.  With few rows reading the head bounds them: 1 row against 131072 x 4096 takes 186 us, 5.8 TB/s; 8
+// rows against 32003 x 1024 20 us, half of it the two kernels' start and end.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -57,17 +57,18 @@ namespace {
 enum Mode { kLogits = 0, kGrad = 1, kHidden = 2, kHead = 3 };
 
 constexpr int kBM = 128;                 // rows of the output per CTA
-constexpr int kBN = 256;                 // columns of the output per tile
+constexpr int kBN = 256;                 // columns of the output per tile,
+constexpr int kNarrow = 64;              // or, for logits of few rows against a small head (see tile_columns())
 constexpr int kBK = 64;                  // contraction elements per stage (128 bytes)
 constexpr int kThreads = 320;            // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
-constexpr uint32_t kTmemCols = 512;      // two accumulators of 256 fp32 columns
+constexpr uint32_t kTmemCols = 512;      // two accumulators of 256 fp32 columns, or four narrow ones
 constexpr uint32_t kSmemLimit = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
 // The tensor cores add into the fp32 accumulator by truncation, so a long contraction drifts
 // towards zero: 3e-6 of lse at D = 4096 when one accumulator takes all of it.  Where the
 // logits themselves are the result (kLogits) the accumulator therefore takes a part of the
 // contraction at a time and the epilogue adds those parts with rounding: 1024 elements above 128 rows (512 cost
-// 4 % of 2048 rows against 131072 x 4096), 128 up to 128 rows, where reading the head hides it (22.0 us both for
+// 4 % of 2048 rows against 131072 x 4096), 128 up to 128 rows, where reading the head hides it (22.0 us both, then, for
 // 8 rows against 32003 x 1024) and a loss of few rows has no others to average with (3e-6 -> 3e-7 for one row).
 template <int kPair>
 constexpr int kLogitsPart = kPair == 2 ? 16 : 2;          // k-tiles
@@ -83,18 +84,19 @@ constexpr int64_t kTwoTermRows = 16;
 // Products that write a matrix pass its rows through 4 KiB of shared memory per epilogue warp, so that
 // they leave in whole 128-byte lines: a thread holds 128 columns of one row, and 16-byte stores of
 // 32 rows at a time held a head gradient of 64 tokens to 2.1 TB/s.
-template <int kPair, int kMode>
+template <int kPair, int kMode, int kN>
 struct Layout {
   static constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KiB
-  static constexpr uint32_t kBTile = (kBN / kPair) * kBK * 2;     // 32 KiB (single) or 16 KiB (pair)
+  static constexpr uint32_t kBTile = (kN / kPair) * kBK * 2;      // 32 KiB (single), 16 KiB (pair) or 8 KiB (narrow)
   static constexpr uint32_t kStage = kATile + kBTile;
   static constexpr uint32_t kBarrierBytes = 256;
   static constexpr uint32_t kOut = kMode == kLogits ? 0u : 8u * 4096u;
-  static constexpr int kStages = static_cast<int>((kSmemLimit - 1024 - kBarrierBytes - kOut) / kStage);   // 4 (single); 7 or 6
+  static constexpr int kStages = static_cast<int>((kSmemLimit - 1024 - kBarrierBytes - kOut) / kStage);   // 4 (single); 7 or 6; 9 or 7 (narrow)
   static constexpr uint32_t kSmem = kStages * kStage + kOut + kBarrierBytes + 1024;
   static_assert(kStage % 1024 == 0, "stage buffers must keep 1 KiB alignment");
   static_assert(kSmem <= kSmemLimit, "exceeds the 227 KiB shared-memory limit");
-  static_assert((2 * kStages + 5) * 8 + 8 <= kBarrierBytes, "barrier area too small");
+  static constexpr int kAccs = kN == kNarrow ? 4 : 2;             // accumulators
+  static_assert((2 * kStages + 2 * kAccs + 1) * 8 + 8 <= kBarrierBytes, "barrier area too small");
 };
 
 struct Maps {
@@ -119,6 +121,7 @@ struct Share {
 struct Params {
   int M, N;               // rows and columns of the product
   int num_kt;             // k-tiles of the contraction
+  uint32_t a_bytes;       // of A in a stage
   Share share;
   // kLogits, kGrad
   const int64_t* labels;  // [M]
@@ -156,12 +159,12 @@ __device__ __forceinline__ uint64_t operand_desc(const void* p) {
 template <bool kMnMajor>
 constexpr uint64_t kDescStep = kMnMajor ? (16u * 128u) >> 4 : 32u >> 4;
 
-template <int kPair, bool kAMn, bool kBMn>
+template <int kPair, bool kAMn, bool kBMn, int kN>
 __device__ __forceinline__ constexpr uint32_t mma_idesc() {
   return (1u << 4)                               // D: fp32
          | (1u << 7) | (1u << 10)                // A, B: bf16
          | (uint32_t(kAMn) << 15) | (uint32_t(kBMn) << 16)
-         | (uint32_t(kBN >> 3) << 17) | (uint32_t((kBM * kPair) >> 4) << 24);
+         | (uint32_t(kN >> 3) << 17) | (uint32_t((kBM * kPair) >> 4) << 24);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -212,18 +215,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-template <int kPair, int kMode>
+template <int kPair, int kMode, int kN>
 __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_constant__ Maps maps, const Params p) {
-  using L = Layout<kPair, kMode>;
+  using L = Layout<kPair, kMode, kN>;
+  constexpr int kC = kN / 2;   // columns of an epilogue thread
   constexpr bool kAMn = kMode == kHead;
   constexpr bool kBMn = kMode == kHidden || kMode == kHead;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kStages * L::kStage + L::kOut);
   uint64_t* empty = full + L::kStages;
-  uint64_t* acc_full = empty + L::kStages;    // [2]
-  uint64_t* acc_empty = acc_full + 2;         // [2]
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* acc_full = empty + L::kStages;    // [kAccs]
+  uint64_t* acc_empty = acc_full + L::kAccs;  // [kAccs]
+  uint64_t* drain = acc_empty + L::kAccs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < L::kAccs; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 8 * kPair);
     }
@@ -272,14 +276,14 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       for (int item = unit; item < items; item += p.share.units) {
         if (!work_at(p, item, t)) continue;
         const int row_a = (t.mb * kPair + static_cast<int>(rank)) * kBM;
-        const int row_b = t.nb * kBN + static_cast<int>(rank) * (kBN / kPair);
+        const int row_b = t.nb * kN + static_cast<int>(rank) * (kN / kPair);
         for (int kt = t.kt0; kt < t.kt1; ++kt) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, &g_ce_error, kErrWaitEmpty)) goto producer_done;
           {
             uint8_t* sa = smem + stage * L::kStage;
             uint8_t* sb = sa + L::kATile;
             const uint32_t bar = kPair == 2 ? map_to_cta(smem_addr(&full[stage]), 0) : 0u;
-            if (leader) mbar_arrive_expect_tx(&full[stage], L::kStage * kPair);
+            if (leader) mbar_arrive_expect_tx(&full[stage], (p.a_bytes + L::kBTile) * kPair);
             auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
               if constexpr (kPair == 2) tma_load_2d_pair(dst, map, bar, x, y);
               else tma_load_2d(dst, map, &full[stage], x, y);
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
             }
             if constexpr (kBMn) {
 #pragma unroll
-              for (int c = 0; c < kBN / kPair / 64; ++c)   // the second terms meet the same rows of h; past its end are zeros
+              for (int c = 0; c < kN / kPair / 64; ++c)   // the second terms meet the same rows of h; past its end are zeros
                 load(sb + c * kChunk, &maps.b, row_b + 64 * c, kMode == kHead && p.term > 0 ? 0 : kt * kBK);
             } else {
               load(sb, &maps.b, kt * kBK, row_b);
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = mma_idesc<kPair, kAMn, kBMn>();
+      constexpr uint32_t idesc = mma_idesc<kPair, kAMn, kBMn, kN>();
       uint32_t stage = 0, phase = 0, buf = 0, acc_phase = 0;
       bool ok = true;
       for (int item = unit; item < items && ok; item += p.share.units) {
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
             break;
           }
           tc_fence_after();
-          const uint32_t acc = tmem + buf * kBN;
+          const uint32_t acc = tmem + buf * (kTmemCols / L::kAccs);
           const int kp1 = min(kp + part, t.kt1);
           for (int kt = kp; kt < kp1; ++kt) {
             if (!mbar_wait(&full[stage], phase, abort_flag, &g_ce_error, kErrWaitFull)) {
@@ -353,8 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
           }
           if (!ok) break;
           tc_commit_g<kPair>(&acc_full[buf]);
-          buf ^= 1u;
-          if (buf == 0) acc_phase ^= 1u;
+          if (++buf == static_cast<uint32_t>(L::kAccs)) {
+            buf = 0;
+            acc_phase ^= 1u;
+          }
         }
       }
       if (!ok) {
@@ -366,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    // 8 warps: two per TMEM lane quadrant, each owning 128 of the 256 columns; a thread
-    // holds 128 columns of one row, so row reductions need no exchange between lanes.
+    // 8 warps: two per TMEM lane quadrant, each owning half of the columns; a thread
+    // holds its (128 or 32) of one row, so row reductions need no exchange between lanes.
     const int quad = warp & 3;
     const int half = (warp - 2) >> 2;
     uint32_t buf = 0, acc_phase = 0;
@@ -376,20 +382,20 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
     for (int item = unit; item < items; item += p.share.units) {
       if (!work_at(p, item, t)) continue;
       const int row = (t.mb * kPair + static_cast<int>(rank)) * kBM + quad * 32 + lane;
-      const int col0 = t.nb * kBN + half * 128;
-      uint32_t v[4][32];
+      const int col0 = t.nb * kN + half * kC;
+      uint32_t v[kC / 32][32];
       auto take = [&](bool first) {
         if (!mbar_wait(&acc_full[buf], acc_phase, abort_flag, &g_ce_error, kErrWaitAccFull, 2 * kWaitLimitNs)) return false;
         tc_fence_after();
         __syncwarp();   // rows past the end leave the loop body early
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBN + half * 128;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * (kTmemCols / L::kAccs) + half * kC;
         if (first) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_load_32x32b_x32(taddr + 32 * c, v[c]);
+          for (int c = 0; c < kC / 32; ++c) tmem_load_32x32b_x32(taddr + 32 * c, v[c]);
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < kC / 16; ++c) {
             uint32_t u[2][8];
             tmem_load_32x32b_x8(taddr + 16 * c, u[0]);
             tmem_load_32x32b_x8(taddr + 16 * c + 8, u[1]);
@@ -407,8 +413,10 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
           if constexpr (kPair == 2) mbar_arrive_remote(map_to_cta(smem_addr(&acc_empty[buf]), 0));
           else mbar_arrive(&acc_empty[buf]);
         }
-        buf ^= 1u;
-        if (buf == 0) acc_phase ^= 1u;
+        if (++buf == static_cast<uint32_t>(L::kAccs)) {
+          buf = 0;
+          acc_phase ^= 1u;
+        }
         return true;
       };
       bool ok = take(true);
@@ -422,12 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
 #pragma unroll
         for (int c0 = 0; c0 < pieces; c0 += 8) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) = fill(c0 + c);
+          for (int c = 0; c < 8; ++c)
+            if (c0 + c < pieces) *reinterpret_cast<uint4*>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) = fill(c0 + c);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + (lane >> 3), c = lane & 7;
-            keep(r, c0 + c, *reinterpret_cast<const uint4*>(mine + r * 128 + ((c ^ (r & 7)) << 4)));
+            if (c0 + c < pieces) keep(r, c0 + c, *reinterpret_cast<const uint4*>(mine + r * 128 + ((c ^ (r & 7)) << 4)));
           }
           __syncwarp();
         }
@@ -437,18 +446,18 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
 
       if constexpr (kMode == kLogits) {
         if (row >= p.M) continue;
-        const int64_t label = p.labels[row] - p.v0 - col0;   // position inside this thread's columns, if 0..127
-        const int cols = min(128, p.N - col0);               // may be <= 0 in the last column tile
+        const int64_t label = p.labels[row] - p.v0 - col0;   // position inside this thread's columns, if 0..kC - 1
+        const int cols = min(kC, p.N - col0);               // may be <= 0 in the last column tile
         float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) {
+        for (int i = 0; i < kC; ++i) {
           const float z = __uint_as_float(v[i >> 5][i & 31]);
           if (i < cols) m = fmaxf(m, z);
         }
         const float c = (m == -INFINITY ? 0.f : m) * kLog2e;
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) {
+        for (int i = 0; i < kC; ++i) {
           const float e = i < cols ? ex2(fmaf(__uint_as_float(v[i >> 5][i & 31]), kLog2e, -c)) : 0.f;
           if ((i & 3) == 0) s0 += e;
           else if ((i & 3) == 1) s1 += e;
@@ -461,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
         if (label >= 0 && label < cols && label + p.v0 + col0 < p.vocab) {
           float z = 0.f;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
+          for (int i = 0; i < kC; ++i)
             if (i == label) z = __uint_as_float(v[i >> 5][i & 31]);
           p.target[row] = z;
         }
@@ -476,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
         const float l2 = p.lse[at_row] * kLog2e;
         auto leave = [&](auto second) {
           constexpr bool kSecond = decltype(second)::value;
-          turn(16, [&](int i) {
+          turn(kC / 8, [&](int i) {
             float d[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -500,9 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
           if (p.term > 0) leave(std::true_type{});
       } else if (kMode == kHidden && (p.out == nullptr || t.slot >= 0)) {
         float* dst = t.slot < 0 ? p.acc + static_cast<int64_t>(row_w) * p.N + col0
-                                : p.slots + (static_cast<int64_t>(t.slot) * (kBM * kPair) + rank * kBM + quad * 32) * kBN + half * 128;
-        const int64_t ld = t.slot < 0 ? p.N : kBN;
-        turn(32, [&](int i) {
+                                : p.slots + (static_cast<int64_t>(t.slot) * (kBM * kPair) + rank * kBM + quad * 32) * kN + half * kC;
+        const int64_t ld = t.slot < 0 ? p.N : kN;
+        turn(kC / 4, [&](int i) {
           return make_uint4(v[i >> 3][(4 * i) & 31], v[i >> 3][(4 * i + 1) & 31], v[i >> 3][(4 * i + 2) & 31], v[i >> 3][(4 * i + 3) & 31]);
         }, [&](int r, int c, const uint4& piece) {
           if (row_w + r >= p.M || col0 + 4 * c >= p.N) return;
@@ -518,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
           *o = f;
         });
       } else {   // kHidden (one piece) and kHead
-        turn(16, [&](int i) {
+        turn(kC / 8, [&](int i) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -687,11 +696,11 @@ int pair_of(int64_t M) { return M > kBM ? 2 : 1; }
 
 enum Cut { kWhole, kCutRest, kAllSlots };
 
-Share share_out(int64_t M, int64_t N, int64_t K, Cut cut) {
+Share share_out(int64_t M, int64_t N, int64_t K, Cut cut, int columns = kBN) {
   const int pair = pair_of(M);
   Share s = {};
   s.num_mb = static_cast<int>(ceil_div(M, kBM * pair));
-  s.num_nb = static_cast<int>(ceil_div(N, kBN));
+  s.num_nb = static_cast<int>(ceil_div(N, columns));
   s.group = 16;
   s.tiles = s.whole = s.num_mb * s.num_nb;
   s.units = kPlanSms / pair;
@@ -718,10 +727,10 @@ Share share_out(int64_t M, int64_t N, int64_t K, Cut cut) {
   return s;
 }
 
-template <int kPair, int kMode>
+template <int kPair, int kMode, int kN>
 cudaError_t launch_mode(const Maps& maps, const Params& p, cudaStream_t stream) {
-  using L = Layout<kPair, kMode>;
-  auto kernel = rfq_ce_kernel<kPair, kMode>;
+  using L = Layout<kPair, kMode, kN>;
+  auto kernel = rfq_ce_kernel<kPair, kMode, kN>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   int units = p.share.units;
@@ -730,24 +739,36 @@ cudaError_t launch_mode(const Maps& maps, const Params& p, cudaStream_t stream) 
   return launch_pdl(kernel, dim3(units * kPair), dim3(kThreads), L::kSmem, kPair, stream, maps, p);
 }
 
+// Columns of a tile of logits of T rows against n entries: narrow where a row of CTAs then holds them all, because few
+// wide tiles leave SMs idle while each CTA waits for its chain of loads.  Measured, narrow against wide: 8 rows, 4096 x
+// 1024 11.7 against 14.1 us, 1000 x 4096 27 against 35; 128 rows, 9400 x 4096 33 against 38; two rounds of narrow
+// tiles lose what one gains (128 rows, 10000 x 4096 55 against 38).
+int tile_columns(int64_t T, int64_t n) { return pair_of(T) == 1 && ceil_div(n, kNarrow) <= kPlanSms ? kNarrow : kBN; }
+
 // A [M] x B [N] product over K; a_ld / b_ld: elements between the rows of the matrix in memory.
 template <int kMode>
 cudaError_t product(EncodeTiledFn encode, const void* a, int64_t a_ld, const void* b, int64_t b_ld, int64_t M, int64_t N,
-                    int64_t K, const Share& share, Params p, cudaStream_t stream) {
+                    int64_t K, const Share& share, Params p, cudaStream_t stream, int columns = kBN) {
   constexpr bool kAMn = kMode == kHead;
   constexpr bool kBMn = kMode == kHidden || kMode == kHead;
   const bool pair = pair_of(M) == 2;
   Maps maps;
   const int64_t a_rows = p.term > 0 ? 2 * K : K;
-  const bool ok = (kAMn ? encode_bf16_map(encode, &maps.a, a, a_rows, M, a_ld, kBK) : encode_bf16_map(encode, &maps.a, a, M, K, a_ld, kBM)) &&
+  // Few rows: A's box has no more of them than there are.  The rest of its tile is whatever it was (rows of the
+  // product that are not kept); as zeros it took its share of the copies' time (1 row against 131072 x 4096 208 us, not 186).
+  const uint32_t box = pair || M > kBM - 8 ? kBM : static_cast<uint32_t>(M + 7) / 8 * 8;
+  p.a_bytes = (kAMn ? kBM : box) * kBK * 2;
+  const bool ok = (kAMn ? encode_bf16_map(encode, &maps.a, a, a_rows, M, a_ld, kBK) : encode_bf16_map(encode, &maps.a, a, M, K, a_ld, box)) &&
                   (kBMn ? encode_bf16_map(encode, &maps.b, b, K, N, b_ld, kBK)
-                        : encode_bf16_map(encode, &maps.b, b, N, K, b_ld, pair ? kBN / 2 : kBN));
+                        : encode_bf16_map(encode, &maps.b, b, N, K, b_ld, pair ? kBN / 2 : columns));
   if (!ok) return cudaErrorInvalidValue;
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.num_kt = kAMn && p.term > 0 ? 2 : static_cast<int>(ceil_div(K, kBK));
   p.share = share;
-  return pair ? launch_mode<2, kMode>(maps, p, stream) : launch_mode<1, kMode>(maps, p, stream);
+  if constexpr (kMode == kLogits || kMode == kGrad)
+    if (columns == kNarrow) return launch_mode<1, kMode, kNarrow>(maps, p, stream);
+  return pair ? launch_mode<2, kMode, kBN>(maps, p, stream) : launch_mode<1, kMode, kBN>(maps, p, stream);
 }
 
 constexpr int64_t kForwardRows = 32768;            // rows of one forward pass (bounds the statistics)
@@ -790,7 +811,7 @@ Plan plan_backward(int64_t T, int64_t D, int64_t V, bool want_dh) {
 
 size_t ce_forward_workspace(int64_t T, int64_t V) {
   const int64_t rows = T < kForwardRows ? T : kForwardRows;
-  return align256(static_cast<size_t>(2 * ceil_div(V, kBN)) * rows * sizeof(float2)) + align256(static_cast<size_t>(rows) * 4);
+  return align256(static_cast<size_t>(2 * ceil_div(V, tile_columns(rows, V))) * rows * sizeof(float2)) + align256(static_cast<size_t>(rows) * 4);
 }
 
 size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh) {
@@ -800,16 +821,16 @@ size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh) {
 cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
                               int64_t ignore, float* loss, float* lse, void* ws, void* encode_tiled, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
-  const int parts = static_cast<int>(2 * ceil_div(V, kBN));
   for (int64_t t0 = 0; t0 < T; t0 += kForwardRows) {
     const int64_t rows = T - t0 < kForwardRows ? T - t0 : kForwardRows;
+    const int columns = tile_columns(rows, V), parts = static_cast<int>(2 * ceil_div(V, columns));
     Params p = {};
     p.labels = labels + t0;
     p.ignore = ignore;
     p.vocab = V;
     p.stats = static_cast<float2*>(ws);
     p.target = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(parts) * rows * sizeof(float2)));
-    cudaError_t e = product<kLogits>(encode, static_cast<const __nv_bfloat16*>(h) + t0 * D, D, w, D, rows, V, D, share_out(rows, V, D, kWhole), p, stream);
+    cudaError_t e = product<kLogits>(encode, static_cast<const __nv_bfloat16*>(h) + t0 * D, D, w, D, rows, V, D, share_out(rows, V, D, kWhole, columns), p, stream, columns);
     if (e != cudaSuccess) return e;
     e = launch_pdl(rfq_ce_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 32))), dim3(32, 32), 0, 1, stream,
                    static_cast<const float2*>(p.stats), static_cast<const float*>(p.target), p.labels, static_cast<int>(rows),
@@ -844,7 +865,8 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
     p.dz = dz;
     p.ld_dz = q.ld_dz;
     p.term = q.rows > T ? static_cast<int>(T) : 0;
-    e = product<kGrad>(encode, h, D, wp, D, T, n, D, share_out(T, n, D, kWhole), p, stream);
+    const int columns = tile_columns(T, n);
+    e = product<kGrad>(encode, h, D, wp, D, T, n, D, share_out(T, n, D, kWhole, columns), p, stream, columns);
     if (e == cudaSuccess && dh != nullptr) {
       p.acc = acc;
       p.slots = slots;
