@@ -61,7 +61,7 @@ constexpr int kBN = 256;                 // columns of the output per tile,
 constexpr int kNarrow = 64;              // or, for logits of few rows against a small head (see tile_columns())
 constexpr int kBK = 64;                  // contraction elements per stage (128 bytes)
 constexpr int kThreads = 320;            // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
-constexpr uint32_t kTmemCols = 512;      // two accumulators of 256 fp32 columns, or four narrow ones
+constexpr uint32_t kTmemCols = 512;      // two accumulators of up to 256 fp32 columns
 constexpr uint32_t kSmemLimit = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
 // The tensor cores add into the fp32 accumulator by truncation, so a long contraction drifts
@@ -95,7 +95,7 @@ struct Layout {
   static constexpr uint32_t kSmem = kStages * kStage + kOut + kBarrierBytes + 1024;
   static_assert(kStage % 1024 == 0, "stage buffers must keep 1 KiB alignment");
   static_assert(kSmem <= kSmemLimit, "exceeds the 227 KiB shared-memory limit");
-  static constexpr int kAccs = kN == kNarrow ? 4 : 2;             // accumulators
+  static constexpr int kAccs = 2;                                 // accumulators
   static_assert((2 * kStages + 2 * kAccs + 1) * 8 + 8 <= kBarrierBytes, "barrier area too small");
 };
 
