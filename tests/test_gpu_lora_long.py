@@ -138,3 +138,44 @@ def test_repeats_bit_for_bit(rfq):
         for _ in range(3):
             again = run_all(rfq, c)
             assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+@pytest.mark.parametrize("M,K,N,r,n,kind", [LONG[1], LONG[5], LONG[6]])
+def test_two_captured_graphs_follow_their_inputs_at_once(rfq, M, K, N, r, n, kind):
+    """Two graphs of a forward and a backward pass, each with tensors and a workspace of its own, replayed on two streams
+    at the same time with other inputs than they were captured with."""
+    names = ("y", "hidden", "dx", "da", "db")
+    sets = []
+    for i in range(2):
+        c = make(M, K, N, r, n, kind, seed=50 + i)
+        o = {"y": torch.empty_like(c["base"]), "hidden": torch.empty((M, r), device="cuda"), "dx": torch.empty_like(c["dx_base"]),
+             "da": torch.empty_like(c["a"]), "db": torch.empty_like(c["b"])}
+        ws = torch.empty(rfq.lora_workspace_bytes(M, K, N, r, n, backward=True), dtype=torch.uint8, device="cuda")
+
+        def run(c=c, o=o, ws=ws):
+            rfq.lora(c["x"], c["a"], c["b"], c["scale"], c["ids"], o["y"], ws, base=c["base"], hidden=o["hidden"])
+            rfq.lora_backward(c["x"], c["a"], c["b"], c["scale"], c["ids"], c["dy"], o["hidden"], ws, dx=o["dx"], dx_base=c["dx_base"], da=o["da"],
+                              db=o["db"])
+
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        sets.append((c, o, graph, torch.cuda.Stream(), ws))   # a graph's workspace lives as long as the graph
+    want = []
+    for i, (c, o, _, _, _) in enumerate(sets):
+        new = make(M, K, N, r, n, "mixed" if kind == "runs" else "runs", seed=60 + i)
+        for k in c:
+            c[k].copy_(new[k])
+        want.append(run_all(rfq, new))
+        for t in o.values():
+            t.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _, _, graph, stream, _ in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, o, _, _, _), w in zip(sets, want):
+        assert [k for k in names if not torch.equal(o[k], w[k])] == []
