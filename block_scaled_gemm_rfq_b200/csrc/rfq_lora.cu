@@ -1470,7 +1470,7 @@ cudaError_t launch_lora_forward(const void* x, const void* a, const void* b, con
                                 void* ws, int num_sms, void* encode_tiled, cudaStream_t stream) {
   cudaError_t e;
   if (wide_forward(M, K, N, r, n, !y_bf16)) {
-    const int terms = y_bf16 ? 1 : 3;
+    const int terms = y_bf16 ? 2 : 3;
     int* counts = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(3) * M * r * 2));
     e = launch_lora_shrink_wide(x, a, false, ids, scale, hidden, ws, terms, counts, M, K, n, r, num_sms, encode_tiled, stream);
     if (e != cudaSuccess) return e;

@@ -19,8 +19,8 @@
 // shrink: the contraction is split over a cluster of up to 8 CTAs, whose partial sums are added
 // through distributed shared memory in the order of the ranks.  The accumulator takes 256
 // elements of the contraction at a time (the tensor cores add by truncation) and the epilogue adds those
-// parts with rounding.  shrink leaves s as bf16 terms (one for a bf16 output; three, 24 bits, for an fp32
-// one), which are expand's operand as they are.
+// parts with rounding.  shrink leaves s as bf16 terms (two, 16 bits, for a bf16 output; three, 24 bits, for an
+// fp32 one), which are expand's operand as they are.
 // expand: base tiles come in by TMA (by a warp of its own: behind the loads of Q in one queue, chunks of two
 // adapters held the base back and cost 1.3 times those of one), are added to in shared memory and leave from
 // there by TMA.
@@ -377,10 +377,11 @@ constexpr int kAccs = 4;               // accumulators of 128 columns in tensor 
 // Columns of a tile: 256 bytes of a row, two boxes of 128 bytes.
 template <bool kF32>
 constexpr int kCols = kF32 ? 64 : 128;
-// s enters the MMA as one bf16 term (2^-8 of the adapter's share, below the rounding of a bf16
-// output) or, for an fp32 output, as three (24 bits).
+// Bf16 terms in which s enters the MMA, as in short batches (kExpandTerms in rfq_lora.cu): one term would add an error as
+// large as a bf16 output's own rounding, in the same direction for a whole row.  The second costs 1 to 5 % (both products of 4096
+// rows, 4096 -> 12288: rank 16 51.8 -> 52.0 us, rank 128 84.4 -> 86.1, 8 requests of rank 64 63 -> 66).
 template <bool kF32>
-constexpr int kTerms = kF32 ? 3 : 1;
+constexpr int kTerms = kF32 ? 3 : 2;
 
 // What a CTA works on: runs of column tiles of one chunk each.
 // With one adapter (or where shrink left no counts) all chunks are alike: units of 4 to 16 tiles go round the CTAs.
@@ -1150,9 +1151,13 @@ cudaError_t launch(Kernel kernel, const Maps& maps, const Params& p, int64_t gri
 template <bool kTrans, bool kF32>
 cudaError_t expand_typed(const ExpandMaps& maps, ExpandParams p, int num_sms, cudaStream_t stream) {
   const uint32_t q = expand_q_bytes<kTrans, kF32>(p.r), s = expand_s_bytes<kF32>(p.r);
-  uint32_t room = kSmemLimit - 4096 - s;   // 4 KiB: alignment and the static part
+  // 2 KiB: alignment and the static part (368 bytes).  With them four base stages fit beside two of s up to rank 64, three
+  // beside one above; with 4 KiB kept back there is one less of each, and 4096 rows of rank 128, 4096 -> 12288, take 111 us, not 86.
+  uint32_t room = kSmemLimit - 2048 - s;
+  // One stage of s where chunks may hold several adapters: a CTA's part touches few chunks, and the room goes to Q, which
+  // then comes once for each adapter (4096 rows of 8 requests of rank 64: 66 us, with two stages of s 70).
   p.s_stages = 1;
-  if (room >= s + 3 * 2 * kBox + 2 * q) {
+  if (p.counts == nullptr && room >= s + 3 * 2 * kBox + 2 * q) {
     p.s_stages = 2;
     room -= s;
   }

@@ -393,10 +393,8 @@ rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, cons
  *            both passes), rfq_linear_lora_workspace_bytes(...) for rfq_linear_lora.  Nothing in
  *            it is carried from one call to the next; calls that may run at the same time need
  *            workspaces of their own.
- * All sums are fp32.  s and ds enter the second product as three bf16 terms (24 bits) for an
- * fp32 result and, for a bf16 one, as two (16 bits) in dA, dB and short batches or one (8 bits)
- * in y and dx of long ones (rows there are many, and none is off by more than its own rounding
- * and that of its s).  rfq_linear_lora
+ * All sums are fp32.  s and ds enter the second product as bf16 terms: three (24 bits) for an
+ * fp32 result, two (16 bits) for a bf16 one, whatever the batch's length.  rfq_linear_lora
  * with a bf16 Y rounds the projection to bf16 before the adapters are added, as any base is.
  * A row reads its own adapter alone: values that are not finite stay in their row (dx, y) and
  * adapter (dA, dB).  M == 0 launches nothing, except that da and db are then zeroed.  No
