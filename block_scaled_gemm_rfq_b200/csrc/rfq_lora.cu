@@ -45,6 +45,7 @@
 
 #include "rfq_internal.h"
 #include "rfq_ptx.cuh"
+#include "rfq_terms.cuh"
 
 namespace rfq {
 namespace {
@@ -377,10 +378,7 @@ __device__ __forceinline__ float join_parts(const float* part, int splits, int64
 template <int kT>
 __device__ __forceinline__ void split_terms(float v, __nv_bfloat16 (&t)[kT]) {
 #pragma unroll
-  for (int i = 0; i < kT; ++i) {
-    t[i] = __float2bfloat16_rn(v);
-    if (i + 1 < kT) v -= __bfloat162float(t[i]);
-  }
+  for (int i = 0; i < kT; ++i) t[i] = take_term(v);
 }
 
 // ---------------------------------------------------------------- expand

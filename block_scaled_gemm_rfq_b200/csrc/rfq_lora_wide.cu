@@ -42,6 +42,7 @@
 
 #include "rfq_internal.h"
 #include "rfq_ptx.cuh"
+#include "rfq_terms.cuh"
 #include "rfq_tmap.h"
 
 namespace rfq {
@@ -341,13 +342,8 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
     if (p.s != nullptr) *reinterpret_cast<float4*>(p.s + row * p.r + j) = v;
     __nv_bfloat16* t = p.terms + row * p.num_terms * p.r + j;
     for (int e = 0; e < p.num_terms; ++e) {   // 8 bits each
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-      const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      *reinterpret_cast<uint2*>(t + e * p.r) = w;
-      v.x -= __uint_as_float(w.x << 16);
-      v.y -= __uint_as_float(w.x & 0xffff0000u);
-      v.z -= __uint_as_float(w.y << 16);
-      v.w -= __uint_as_float(w.y & 0xffff0000u);
+      const __nv_bfloat162 lo = {take_term(v.x), take_term(v.y)}, hi = {take_term(v.z), take_term(v.w)};
+      *reinterpret_cast<uint2*>(t + e * p.r) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   }
   cluster_sync();   // the others may still be reading this CTA's sums
