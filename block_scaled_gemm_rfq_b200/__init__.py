@@ -550,7 +550,7 @@ def check_device_error(stream=None):
 
 
 def debug_skip_next_fill(fill_index: int):
-    """rfq_debug_skip_next_fill: test hook; the next GEMM's first CTA skips stage
+    """rfq_debug_skip_next_fill: test hook; the first CTA of the next GEMM (or loss at the output head) skips stage
     fill `fill_index` (its bounded wait then runs out)."""
     load_library().rfq_debug_skip_next_fill(int(fill_index))
 

@@ -418,7 +418,7 @@ rfq_status_t rfq_linear_ce(const void* h_bf16, const void* w_bf16, const int64_t
   int sms = 0;
   if ((st = current_device(&sms)) != RFQ_OK) return st;
   return from_cuda(rfq::launch_ce_forward(h_bf16, w_bf16, labels, T, D, V, ignore_index, loss, lse, workspace,
-                                          g_encode_tiled, stream));
+                                          g_encode_tiled, g_skip_fill.exchange(-1), stream));
 }
 
 rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, const int64_t* labels, const float* lse,
@@ -443,7 +443,7 @@ rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, cons
   if (st != RFQ_OK) return st;
   if ((st = current_device(&sms)) != RFQ_OK) return st;
   return from_cuda(rfq::launch_ce_backward(h_bf16, w_bf16, labels, lse, dloss, T, D, V, ignore_index, dh_bf16, dw_bf16,
-                                           workspace, g_encode_tiled, stream));
+                                           workspace, g_encode_tiled, g_skip_fill.exchange(-1), stream));
 }
 
 size_t rfq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank, int64_t n_adapters, int backward) {

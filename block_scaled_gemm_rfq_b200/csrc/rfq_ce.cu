@@ -142,6 +142,7 @@ struct Params {
   // kHidden and kHead
   __nv_bfloat16* out;     // [M][N]
   int term;               // kGrad and kHead: rows of dz before its second terms begin, or 0: it has none
+  int skip;               // fault injection: 1 + the stage fill that the first CTA leaves out, or 0
 };
 
 // Shared-memory operand descriptors (128-byte swizzle).  K-major: rows of 128 bytes, 8-row
@@ -273,13 +274,14 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
     if (lane == 0) {
       // ------------------------------------------------------------ TMA producer
       uint32_t stage = 0, phase = 0, filled = 0, last_parity = 0;
+      int fill = 0;
       for (int item = unit; item < items; item += p.share.units) {
         if (!work_at(p, item, t)) continue;
         const int row_a = (t.mb * kPair + static_cast<int>(rank)) * kBM;
         const int row_b = t.nb * kN + static_cast<int>(rank) * (kN / kPair);
         for (int kt = t.kt0; kt < t.kt1; ++kt) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, &g_ce_error, kErrWaitEmpty)) goto producer_done;
-          {
+          if (++fill != p.skip || blockIdx.x != 0) {
             uint8_t* sa = smem + stage * L::kStage;
             uint8_t* sb = sa + L::kATile;
             const uint32_t bar = kPair == 2 ? map_to_cta(smem_addr(&full[stage]), 0) : 0u;
@@ -301,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
             } else {
               load(sb, &maps.b, kt * kBK, row_b);
             }
+            filled |= 1u << stage;
+            last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           }
-          filled |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == static_cast<uint32_t>(L::kStages)) {
             stage = 0;
             phase ^= 1u;
@@ -385,9 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       const int col0 = t.nb * kN + half * kC;
       uint32_t v[kC / 32][32];
       auto take = [&](bool first) {
-        if (!mbar_wait(&acc_full[buf], acc_phase, abort_flag, &g_ce_error, kErrWaitAccFull, 2 * kWaitLimitNs)) return false;
+        // The lanes agree, so that none waits below for one that gave up; and rows past the end, which leave the loop body
+        // early, are with the others again.
+        const bool full_now = mbar_wait(&acc_full[buf], acc_phase, abort_flag, &g_ce_error, kErrWaitAccFull, 2 * kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, full_now)) return false;
         tc_fence_after();
-        __syncwarp();   // rows past the end leave the loop body early
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * (kTmemCols / L::kAccs) + half * kC;
         if (first) {
 #pragma unroll
@@ -543,14 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
     }
   }
 
+  __syncwarp();   // one lane alone had the work, or rows past the end left early: the barrier below takes whole warps
   tc_fence_before();
   if (kPair == 2) cluster_sync();
   else __syncthreads();
   tc_fence_after();
-  if (warp == 1) {
-    __syncwarp();
-    tmem_dealloc_g<kPair>(tmem, kTmemCols);
-  }
+  if (warp == 1) tmem_dealloc_g<kPair>(tmem, kTmemCols);
 }
 
 // Joins the parts of each row: C = max c, lse = C ln 2 + log sum s 2^(c - C).  One block per
@@ -819,7 +821,7 @@ size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh) {
 }
 
 cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
-                              int64_t ignore, float* loss, float* lse, void* ws, void* encode_tiled, cudaStream_t stream) {
+                              int64_t ignore, float* loss, float* lse, void* ws, void* encode_tiled, int skip_fill, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
   for (int64_t t0 = 0; t0 < T; t0 += kForwardRows) {
     const int64_t rows = T - t0 < kForwardRows ? T - t0 : kForwardRows;
@@ -829,6 +831,7 @@ cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* label
     p.ignore = ignore;
     p.vocab = V;
     p.stats = static_cast<float2*>(ws);
+    p.skip = t0 == 0 ? skip_fill + 1 : 0;
     p.target = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(static_cast<size_t>(parts) * rows * sizeof(float2)));
     cudaError_t e = product<kLogits>(encode, static_cast<const __nv_bfloat16*>(h) + t0 * D, D, w, D, rows, V, D, share_out(rows, V, D, kWhole, columns), p, stream, columns);
     if (e != cudaSuccess) return e;
@@ -842,7 +845,7 @@ cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* label
 
 cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labels, const float* lse, const float* dloss,
                                int64_t T, int64_t D, int64_t V, int64_t ignore, void* dh, void* dw, void* ws, void* encode_tiled,
-                               cudaStream_t stream) {
+                               int skip_fill, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
   const Plan q = plan_backward(T, D, V, dh != nullptr);
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -866,7 +869,9 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
     p.ld_dz = q.ld_dz;
     p.term = q.rows > T ? static_cast<int>(T) : 0;
     const int columns = tile_columns(T, n);
+    p.skip = v0 == 0 ? skip_fill + 1 : 0;
     e = product<kGrad>(encode, h, D, wp, D, T, n, D, share_out(T, n, D, kWhole, columns), p, stream, columns);
+    p.skip = 0;
     if (e == cudaSuccess && dh != nullptr) {
       p.acc = acc;
       p.slots = slots;

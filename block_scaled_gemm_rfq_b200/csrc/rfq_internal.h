@@ -60,14 +60,15 @@ cudaError_t launch_gemm_mxfp8(const void* qx_codes, const void* qx_scales, const
 cudaError_t launch_mma_rate_probe(int variant, int iters, unsigned long long* cycles, int max_clusters,
                                   int* clusters_used, cudaStream_t stream);
 
-// Softmax cross entropy at the output head (rfq_ce.cu).  dh / dw may be nullptr.
+// Softmax cross entropy at the output head (rfq_ce.cu).  dh / dw may be nullptr.  `skip_fill` as for launch_gemm, in the
+// product that forms the logits.
 size_t ce_forward_workspace(int64_t T, int64_t V);
 size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh);
 cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
-                              int64_t ignore, float* loss, float* lse, void* ws, void* encode_tiled, cudaStream_t stream);
+                              int64_t ignore, float* loss, float* lse, void* ws, void* encode_tiled, int skip_fill, cudaStream_t stream);
 cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labels, const float* lse, const float* dloss,
                                int64_t T, int64_t D, int64_t V, int64_t ignore, void* dh, void* dw, void* ws, void* encode_tiled,
-                               cudaStream_t stream);
+                               int skip_fill, cudaStream_t stream);
 
 // Low-rank adapters beside a projection (rfq_lora.cu).  base, hidden, dx, da, db may be nullptr.
 size_t lora_forward_workspace(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n);

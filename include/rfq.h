@@ -495,7 +495,8 @@ rfq_status_t rfq_check_device_error(cudaStream_t stream, int* detail);
 
 /*
  * Testing hook for the bounded waits (no counterpart in the paper): the next
- * rfq_gemm launched by this process makes the producer of its first CTA skip
+ * rfq_gemm, rfq_linear_ce or rfq_linear_ce_backward (of the head's calls: the product
+ * that forms the logits) launched by this process makes the producer of its first CTA skip
  * stage fill number `fill_index` (counted from 0 over that CTA's k-tiles), so
  * the MMA warp's wait for that stage runs out after about 1.5 s; the kernel then
  * drains its own copies and MMAs, frees its TMEM and returns, and
