@@ -56,7 +56,6 @@ constexpr int kRows = 16;                  // rows of one group
 constexpr int kMaxAdapters = RFQ_LORA_MAX_ADAPTERS;
 constexpr int kMaxStages = 6;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kStaticSmem = 21 * 1024;     // as much as any kernel here has besides its dynamic part
 
 __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Row stride in shared memory of rows of `bytes` bytes: an odd number of 16-byte units, so that
@@ -915,7 +914,8 @@ __host__ __device__ constexpr int outer_stage_bytes(int r) {
 // Stages of the ring (four of the largest, rank 128 in three terms, fill one SM's shared memory).
 template <int kJ16, int kT>
 constexpr int kOuterStages = 4;
-static_assert(4 * outer_stage_bytes<3>(128) + kOuterStatic + 1088 <= kSmemLimit, "the largest ring fits");
+constexpr int kMostBesideOuter = 4 * outer_stage_bytes<3>(128) + 64;
+static_assert(kMostBesideOuter + kOuterStatic + 1024 <= kSmemLimit, "the largest ring fits");
 
 template <int kJ16, int kT>   // kJ16: 16-row tiles of the rank, at most
 __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterParams p) {
@@ -1225,10 +1225,13 @@ static_assert(kThreads * kReduceVecs >= RFQ_LORA_MAX_RANK * 8, "a block's vector
 // ---------------------------------------------------------------- host
 constexpr int kPlanSms = 148;   // the cut does not depend on the device that runs it
 
+// `most`: the dynamic shared memory that any call may ask of this kernel.  The limit that it sets belongs to the kernel, not to
+// the launch: set to each launch's own size, a call of a smaller rank on another host thread could lower it between
+// the two and make this launch fail.
 template <class Kernel, class Params>
-cudaError_t launch(Kernel kernel, const Params& p, dim3 grid, size_t smem, cudaStream_t stream) {
-  if (smem > 48 * 1024 - kStaticSmem) {   // with the static part it may pass the default limit
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+cudaError_t launch(Kernel kernel, const Params& p, dim3 grid, size_t smem, int most, cudaStream_t stream) {
+  if (most > 0) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -1245,11 +1248,14 @@ cudaError_t launch(Kernel kernel, const Params& p, dim3 grid, size_t smem, cudaS
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Dynamic shared memory of the kernels that have a Groups beside it, at most (1 KiB is the system's).
+constexpr int kMostBesideGroups = kSmemLimit - 1024 - static_cast<int>(sizeof(Groups));
+
 // Stages of a ring: three or four if two CTAs then share an SM, else as many as fit one (2 to 6).
-int ring_stages(int stage_bytes, int other_bytes) {
-  const int half = (kSmemLimit / 2 - 1024 - other_bytes) / stage_bytes;
+int ring_stages(int stage_bytes, int other_bytes) {   // other_bytes: besides the ring and the Groups
+  const int half = (kSmemLimit / 2 - 1024 - static_cast<int>(sizeof(Groups)) - other_bytes) / stage_bytes;
   if (half >= 3) return half < 4 ? half : 4;
-  const int whole = (kSmemLimit - 1024 - other_bytes) / stage_bytes;
+  const int whole = (kMostBesideGroups - other_bytes) / stage_bytes;
   return whole < kMaxStages ? whole : kMaxStages;
 }
 
@@ -1324,12 +1330,12 @@ cudaError_t shrink(const void* src, const void* w, const int* ids, int* table, f
   *splits = shrink_splits(M, C, n, &p.c_split, &p.zs);
   const dim3 grid(static_cast<unsigned>(ceil_div(M, kChunk) * p.zs), static_cast<unsigned>(*splits));
   const int stage = kRows * kRowStride + shrink_p_bytes(p.r), red = shrink_red_bytes(p.r);
-  p.stages = ring_stages(stage, red + static_cast<int>(sizeof(Groups)));
+  p.stages = ring_stages(stage, red);
   const size_t smem = static_cast<size_t>(p.stages) * stage + red;
-  if (r <= 16) return launch(rfq_lora_shrink_kernel<2>, p, grid, smem, stream);
-  if (r <= 32) return launch(rfq_lora_shrink_kernel<4>, p, grid, smem, stream);
-  if (r <= 64) return launch(rfq_lora_shrink_kernel<8>, p, grid, smem, stream);
-  return launch(rfq_lora_shrink_kernel<16>, p, grid, smem, stream);
+  if (r <= 16) return launch(rfq_lora_shrink_kernel<2>, p, grid, smem, kMostBesideGroups, stream);
+  if (r <= 32) return launch(rfq_lora_shrink_kernel<4>, p, grid, smem, kMostBesideGroups, stream);
+  if (r <= 64) return launch(rfq_lora_shrink_kernel<8>, p, grid, smem, kMostBesideGroups, stream);
+  return launch(rfq_lora_shrink_kernel<16>, p, grid, smem, kMostBesideGroups, stream);
 }
 
 template <bool kF32>
@@ -1344,8 +1350,8 @@ cudaError_t expand_typed(ExpandParams p, cudaStream_t stream) {
   p.tiles = static_cast<int>(ceil_div(tiles, parts));
   const dim3 grid(static_cast<unsigned>(chunks * z), static_cast<unsigned>(ceil_div(tiles, p.tiles)));
   const int stage = expand_stage_bytes<kF32>(p.r), other = expand_s_bytes<kF32>(p.r);
-  p.stages = ring_stages(stage, other + static_cast<int>(sizeof(Groups)));
-  return launch(rfq_lora_expand_kernel<kF32>, p, grid, static_cast<size_t>(p.stages) * stage + other, stream);
+  p.stages = ring_stages(stage, other);
+  return launch(rfq_lora_expand_kernel<kF32>, p, grid, static_cast<size_t>(p.stages) * stage + other, kMostBesideGroups, stream);
 }
 
 cudaError_t expand(const float* part, int splits, const float* scale, const void* w, const int* table, const void* base, void* out,
@@ -1390,7 +1396,8 @@ cudaError_t forward_typed(const ForwardParams& p, int64_t clusters, cudaStream_t
 template <int kJ16, int kT>
 cudaError_t outer_typed(const OuterParams& p, dim3 grid, cudaStream_t stream) {
   // The last row's fragments may reach past its end.
-  return launch(rfq_lora_outer_kernel<kJ16, kT>, p, grid, static_cast<size_t>(kOuterStages<kJ16, kT>) * outer_stage_bytes<kT>(p.r) + 64, stream);
+  return launch(rfq_lora_outer_kernel<kJ16, kT>, p, grid, static_cast<size_t>(kOuterStages<kJ16, kT>) * outer_stage_bytes<kT>(p.r) + 64,
+                kMostBesideOuter, stream);
 }
 template <int kT>
 cudaError_t outer_rank(const OuterParams& p, dim3 grid, cudaStream_t stream) {
@@ -1539,7 +1546,7 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
     if (sp.ds == nullptr && sp.s == nullptr) return cudaSuccess;
     const int64_t blocks = ceil_div(M * r, kThreads);
     const dim3 sgrid(static_cast<unsigned>(blocks < 8 * kPlanSms ? blocks : 8 * kPlanSms));
-    return kind == 2 ? launch(rfq_lora_split_kernel<2>, sp, sgrid, 0, stream) : launch(rfq_lora_split_kernel<3>, sp, sgrid, 0, stream);
+    return kind == 2 ? launch(rfq_lora_split_kernel<2>, sp, sgrid, 0, 0, stream) : launch(rfq_lora_split_kernel<3>, sp, sgrid, 0, 0, stream);
   };
   // Expand over chunks reads ds' as terms, expand of groups forms them itself.
   const bool split_first = chunks && !chunks_ds;
@@ -1586,7 +1593,7 @@ cudaError_t launch_lora_backward(const void* x, const void* a, const void* b, co
   q.r = static_cast<int>(r);
   q.ranges = pl.ranges;
   const dim3 rgrid(static_cast<unsigned>((q.side[0].tiles + q.side[1].tiles) * n));
-  return grad_bf16 ? launch(rfq_lora_reduce_kernel<false>, q, rgrid, 0, stream) : launch(rfq_lora_reduce_kernel<true>, q, rgrid, 0, stream);
+  return grad_bf16 ? launch(rfq_lora_reduce_kernel<false>, q, rgrid, 0, 0, stream) : launch(rfq_lora_reduce_kernel<true>, q, rgrid, 0, 0, stream);
 }
 
 }  // namespace rfq

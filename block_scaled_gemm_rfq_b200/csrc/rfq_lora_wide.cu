@@ -1122,9 +1122,13 @@ bool encode_f32_map(EncodeTiledFn encode, CUtensorMap* map, const void* base, in
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Dynamic shared memory that any call may ask of shrink and expand, and of outer.  What is set here belongs to the kernel, not to the
+// launch: set to each launch's own size, a smaller call on another host thread could lower it before this one's launch.
+constexpr int kMostSmem = kSmemLimit - 1024, kMostOuterSmem = kSmemLimit - 17 * 1024;
+
 template <class Kernel, class Maps, class Params>
 cudaError_t launch(Kernel kernel, const Maps& maps, const Params& p, int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -1147,7 +1151,7 @@ cudaError_t launch(Kernel kernel, const Maps& maps, const Params& p, int64_t gri
 template <bool kTrans, bool kF32>
 cudaError_t expand_typed(const ExpandMaps& maps, ExpandParams p, int num_sms, cudaStream_t stream) {
   const uint32_t q = expand_q_bytes<kTrans, kF32>(p.r), s = expand_s_bytes<kF32>(p.r);
-  // 2 KiB: alignment and the static part (368 bytes).  With them four base stages fit beside two of s up to rank 64, three
+  // 2 KiB: alignment (in the dynamic part) and the static part (368 bytes).  With them four base stages fit beside two of s up to rank 64, three
   // beside one above; with 4 KiB kept back there is one less of each, and 4096 rows of rank 128, 4096 -> 12288, take 111 us, not 86.
   uint32_t room = kSmemLimit - 2048 - s;
   // One stage of s where chunks may hold several adapters: a CTA's part touches few chunks, and the room goes to Q, which
@@ -1283,11 +1287,11 @@ cudaError_t launch_lora_outer_wide(const void* ds, int ds_ld, const void* x, flo
   p.r = static_cast<int>(r);
   p.range = range;
   const uint32_t stage = terms == 3 ? outer_stage_bytes<3>(p.r) : outer_stage_bytes<2>(p.r);
-  p.stages = static_cast<int>((kSmemLimit - 1024 - 17 * 1024) / stage);   // 2 to 4 (17 KiB: the keys and barriers)
+  p.stages = static_cast<int>((kMostOuterSmem - 1024) / stage);   // 2 to 4 (beside 17 KiB: the keys and barriers)
   if (p.stages > 4) p.stages = 4;
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * stage;
   auto kernel = terms == 3 ? rfq_lora_outer_wide_kernel<3> : rfq_lora_outer_wide_kernel<2>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostOuterSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.side[0].tiles + p.side[1].tiles), static_cast<unsigned>(ceil_div(M, range)));
