@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
     tmem_alloc_g<kPair>(tmem_slot, kTmemCols);
     tmem_relinquish_g<kPair>();
   }
+  __syncwarp();
   tc_fence_before();
   if (kPair == 2) cluster_sync();
   else __syncthreads();

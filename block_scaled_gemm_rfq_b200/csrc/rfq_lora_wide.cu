@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kShrinkThreads) rfq_lora_shrink_wide_kernel(co
       *reinterpret_cast<uint2*>(t + e * p.r) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   }
+  __syncwarp();     // rows past the end left the loop body early; the barrier takes whole warps
   cluster_sync();   // the others may still be reading this CTA's sums
 }
 
@@ -687,6 +688,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
         if (!p.has_base) {
           // The stage is free once its last tile has left (one thread waits, all learn of it at the barrier).
           if (threadIdx.x == 64 && release >= 0) bulk_wait_read_all();
+          __syncwarp();
           asm volatile("bar.sync 1, 256;" ::: "memory");
           if (mine < 0)
 #pragma unroll
@@ -745,6 +747,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) rfq_lora_expand_wide_kernel
           acc.next(kAccs);
         }
         fence_proxy_async_smem();
+        __syncwarp();
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (threadIdx.x == 64) {
           if (*abort_flag == 0) {

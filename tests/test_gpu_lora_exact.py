@@ -65,3 +65,15 @@ def test_whole_numbers_are_exact(rfq, M, K, N, r, n, kind, out, grad):
     got = run_all(rfq, c, out, grad)
     for name, t in got.items():
         assert torch.equal(t, want[name].float().to(t.dtype)), name
+
+
+@pytest.mark.parametrize("M", [65, 97, 129, 161, 255, 257, 383, 1025])
+def test_rows_that_end_inside_a_warp(rfq, M):
+    """Long batches whose last chunk ends inside a warp: the lanes of the rows past the end have nothing to write and come
+    together with the others again at the cluster's barrier."""
+    c = make(M, 8200, 8200, 72, 1, "one", M, BF16)
+    want = exact(c)
+    for _ in range(3):
+        got = run_all(rfq, c)
+        for name, t in got.items():
+            assert torch.equal(t, want[name].float().to(t.dtype)), name
