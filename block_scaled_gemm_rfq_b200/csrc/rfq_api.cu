@@ -400,7 +400,7 @@ rfq_status_t rfq_gemm_mxfp8(const void* qx_codes, const void* qx_scales, const v
 size_t rfq_linear_ce_workspace_bytes(int64_t T, int64_t D, int64_t V, int want_dh, int want_dw) {
   if (!ce_shape_ok(T, D, V) || T == 0) return 0;
   const size_t f = rfq::ce_forward_workspace(T, V);
-  const size_t b = want_dh || want_dw ? rfq::ce_backward_workspace(T, D, V, want_dh != 0) : 0;
+  const size_t b = want_dh || want_dw ? rfq::ce_backward_workspace(T, D, V, want_dh != 0, want_dw != 0) : 0;
   return f > b ? f : b;
 }
 
@@ -439,7 +439,7 @@ rfq_status_t rfq_linear_ce_backward(const void* h_bf16, const void* w_bf16, cons
   if (!h_bf16 || !w_bf16 || !labels || !lse || !dloss) return RFQ_ERR_INVALID_ARG;
   if (!aligned16(h_bf16) || !aligned16(w_bf16) || !aligned_to(labels, 8) || !aligned_to(lse, 4) || !aligned_to(dloss, 4))
     return RFQ_ERR_MISALIGNED;
-  st = check_workspace(workspace, workspace_bytes, rfq::ce_backward_workspace(T, D, V, dh_bf16 != nullptr));
+  st = check_workspace(workspace, workspace_bytes, rfq::ce_backward_workspace(T, D, V, dh_bf16 != nullptr, dw_bf16 != nullptr));
   if (st != RFQ_OK) return st;
   if ((st = current_device(&sms)) != RFQ_OK) return st;
   return from_cuda(rfq::launch_ce_backward(h_bf16, w_bf16, labels, lse, dloss, T, D, V, ignore_index, dh_bf16, dw_bf16,

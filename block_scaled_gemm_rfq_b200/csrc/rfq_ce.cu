@@ -604,19 +604,39 @@ __global__ void __launch_bounds__(1024) rfq_ce_join_kernel(const float2* stats, 
   }
 }
 
-// gmax = largest finite |dloss| over the rows that count (one block).
-__global__ void __launch_bounds__(1024) rfq_ce_gmax_kernel(const float* dloss, const int64_t* labels, int M, int64_t ignore,
-                                                           float* gmax) {
+// Before the products.  Block 0: gmax = largest finite |dloss| over the rows that count.  The others, where dw is wanted:
+// a copy of h whose ignored rows are zero.  dz of such a row is zero, but dw = dz^T h would still take 0 x NaN or
+// 0 x inf from padding that nobody wrote.  (A warp for each 2 KiB of a row: both gradients of 4096 x 4096 against 32768 take 2.56 ms
+// with the copy and without, dw of 16 rows 126 us and 125; a warp for each row took 7 us more for one row.)
+constexpr int kCopyRun = 128;   // 16-byte vectors
+__global__ void __launch_bounds__(1024) rfq_ce_prepare_kernel(const float* dloss, const int64_t* labels, int M, int64_t ignore, float* gmax,
+                                                              const uint4* h, uint4* clean, int vecs) {
   __shared__ float part[32];
   griddep_launch_dependents();
   griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x > 0) {
+    const int runs = (vecs + kCopyRun - 1) / kCopyRun;   // of a row; M * runs < 2^30
+    for (int i = (static_cast<int>(blockIdx.x) - 1) * 32 + warp; i < M * runs; i += (static_cast<int>(gridDim.x) - 1) * 32) {
+      const int row = i / runs, c0 = (i - row * runs) * kCopyRun + lane;
+      const bool keep = labels[row] != ignore;
+      const int64_t at = static_cast<int64_t>(row) * vecs + c0;
+      uint4 v[kCopyRun / 32];
+#pragma unroll
+      for (int u = 0; u < kCopyRun / 32; ++u) v[u] = keep && c0 + 32 * u < vecs ? h[at + 32 * u] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int u = 0; u < kCopyRun / 32; ++u)
+        if (c0 + 32 * u < vecs) clean[at + 32 * u] = v[u];
+    }
+    return;
+  }
   float m = 0.f;
   for (int i = threadIdx.x; i < M; i += 1024) {
     const float g = fabsf(dloss[i]);
     if (labels[i] != ignore && g <= 3.402823466e38f) m = fmaxf(m, g);
   }
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  if (lane == 0) part[warp] = m;
   __syncthreads();
   if (threadIdx.x < 32) {
     m = part[threadIdx.x];
@@ -786,10 +806,10 @@ struct Plan {
   int64_t piece, pieces, ld_dz;
   int64_t rows;           // of dz
   Share hidden;
-  size_t off_acc, off_slots, off_gmax, bytes;
+  size_t off_acc, off_slots, off_clean, off_gmax, bytes;
 };
 
-Plan plan_backward(int64_t T, int64_t D, int64_t V, bool want_dh) {
+Plan plan_backward(int64_t T, int64_t D, int64_t V, bool want_dh, bool want_dw) {
   Plan q;
   q.rows = T <= kTwoTermRows ? 2 * T : T;
   q.piece = kPieceBytes / 2 / q.rows / kBN * kBN;
@@ -805,6 +825,8 @@ Plan plan_backward(int64_t T, int64_t D, int64_t V, bool want_dh) {
   if (want_dh && q.pieces > 1 && q.hidden.whole > 0) at += align256(static_cast<size_t>(T) * D * 4);
   q.off_slots = at;
   if (want_dh) at += static_cast<size_t>(q.hidden.tiles - q.hidden.whole) * q.hidden.slices * (kBM * pair_of(T)) * kBN * 4;
+  q.off_clean = at;
+  if (want_dw) at += align256(static_cast<size_t>(T) * D * 2);
   q.off_gmax = at;
   q.bytes = at + 256;
   return q;
@@ -817,8 +839,8 @@ size_t ce_forward_workspace(int64_t T, int64_t V) {
   return align256(static_cast<size_t>(2 * ceil_div(V, tile_columns(rows, V))) * rows * sizeof(float2)) + align256(static_cast<size_t>(rows) * 4);
 }
 
-size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh) {
-  return plan_backward(T, D, V, want_dh).bytes;
+size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh, bool want_dw) {
+  return plan_backward(T, D, V, want_dh, want_dw).bytes;
 }
 
 cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
@@ -848,13 +870,16 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
                                int64_t T, int64_t D, int64_t V, int64_t ignore, void* dh, void* dw, void* ws, void* encode_tiled,
                                int skip_fill, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
-  const Plan q = plan_backward(T, D, V, dh != nullptr);
+  const Plan q = plan_backward(T, D, V, dh != nullptr, dw != nullptr);
   uint8_t* base = static_cast<uint8_t*>(ws);
   __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
   float* acc = reinterpret_cast<float*>(base + q.off_acc);
   float* slots = reinterpret_cast<float*>(base + q.off_slots);
   float* gmax = reinterpret_cast<float*>(base + q.off_gmax);
-  cudaError_t e = launch_pdl(rfq_ce_gmax_kernel, dim3(1), dim3(1024), 0, 1, stream, dloss, labels, static_cast<int>(T), ignore, gmax);
+  uint4* clean = reinterpret_cast<uint4*>(base + q.off_clean);
+  const int64_t copies = dw == nullptr ? 0 : ceil_div(T * ceil_div(D / 8, kCopyRun), 32);   // blocks of 32 warps, at most two of them an SM
+  cudaError_t e = launch_pdl(rfq_ce_prepare_kernel, dim3(static_cast<unsigned>(1 + (copies < 2 * kPlanSms ? copies : 2 * kPlanSms))), dim3(1024), 0, 1, stream, dloss,
+                             labels, static_cast<int>(T), ignore, gmax, static_cast<const uint4*>(h), clean, static_cast<int>(D / 8));
   for (int64_t v0 = 0; v0 < V && e == cudaSuccess; v0 += q.piece) {
     const int64_t n = V - v0 < q.piece ? V - v0 : q.piece;
     const __nv_bfloat16* wp = static_cast<const __nv_bfloat16*>(w) + v0 * D;
@@ -882,7 +907,7 @@ cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labe
     }
     if (e == cudaSuccess && dw != nullptr) {
       p.out = static_cast<__nv_bfloat16*>(dw) + v0 * D;
-      e = product<kHead>(encode, dz, q.ld_dz, h, D, n, D, T, share_out(n, D, T, kWhole), p, stream);
+      e = product<kHead>(encode, dz, q.ld_dz, clean, D, n, D, T, share_out(n, D, T, kWhole), p, stream);
     }
   }
   // Tiles of dh still in fp32: all of them after several pieces, else the rest.

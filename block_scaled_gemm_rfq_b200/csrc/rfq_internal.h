@@ -63,7 +63,7 @@ cudaError_t launch_mma_rate_probe(int variant, int iters, unsigned long long* cy
 // Softmax cross entropy at the output head (rfq_ce.cu).  dh / dw may be nullptr.  `skip_fill` as for launch_gemm, in the
 // product that forms the logits.
 size_t ce_forward_workspace(int64_t T, int64_t V);
-size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh);
+size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh, bool want_dw);
 cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
                               int64_t ignore, float* loss, float* lse, void* ws, void* encode_tiled, int skip_fill, cudaStream_t stream);
 cudaError_t launch_ce_backward(const void* h, const void* w, const int64_t* labels, const float* lse, const float* dloss,

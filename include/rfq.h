@@ -336,7 +336,8 @@ rfq_status_t rfq_gemm_mxfp8(const void* qx_codes, const void* qx_scales,
  *            caller's: its loss is NaN, and so are its gradients.
  *   loss, lse, dloss   [T] fp32.  loss is per row: a mean or sum over the rows is the
  *            caller's, as dloss (e.g. 1 / counted rows).  Rows of dloss whose label is
- *            ignore_index are not looked at.
+ *            ignore_index are not looked at, and rows of h may hold anything there (NaN in padding
+ *            reaches neither loss, dh of other rows nor dw).
  *   dh_bf16  [T][D], dw_bf16 [V][D]: bf16, 16-byte aligned, fully overwritten; either may be
  *            NULL (a frozen head, or scoring).  No output overlaps an input or another output.
  *   workspace   rfq_linear_ce_workspace_bytes(T, D, V, want_dh, want_dw) bytes, 256-byte
