@@ -41,6 +41,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 #include <type_traits>
 
@@ -70,8 +71,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // contraction at a time and the epilogue adds those parts with rounding: 1024 elements above 128 rows (512 cost
 // 4 % of 2048 rows against 131072 x 4096), 128 up to 128 rows, where reading the head hides it (22.0 us both, then, for
 // 8 rows against 32003 x 1024) and a loss of few rows has no others to average with (3e-6 -> 3e-7 for one row).
-template <int kPair>
-constexpr int kLogitsPart = kPair == 2 ? 16 : 2;          // k-tiles
+// The backward pass (kGrad) takes the same parts, so that its logits are those that lse is of: where a label is nearly
+// certain p - 1 cancels, and a drift between the two was 17 % of 1 - p = 1e-3 at D = 4096.  It costs dh of 64 rows against 50000 x
+// 2048 94 -> 100 us (the epilogue of a tile holds up the parts of the next), of 1000 rows against 50001 x 2048 330 -> 335.
+template <int kPair, int kMode>
+constexpr int kPart = kMode == kLogits || kMode == kGrad ? (kPair == 2 ? 16 : 2) : INT_MAX;   // k-tiles
 // dz is rounded to bf16 for the next products.  Over many rows those roundings average out; a few rows leave
 // a gradient that is off by one rounding of its largest entries, beside its own.  Up to 16 rows dz is therefore
 // kept as the sum of two bf16 terms: rows T .. 2 T - 1 of dz are what rows 0 .. T - 1 left out.  dh takes both
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       bool ok = true;
       for (int item = unit; item < items && ok; item += p.share.units) {
         if (!work_at(p, item, t)) continue;
-        const int part = kMode == kLogits ? kLogitsPart<kPair> : t.kt1 - t.kt0;
+        const int part = min(kPart<kPair, kMode>, t.kt1 - t.kt0);
         for (int kp = t.kt0; kp < t.kt1 && ok; kp += part) {
           if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, &g_ce_error, kErrWaitAccEmpty)) {
             ok = false;
@@ -425,12 +429,14 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
         return true;
       };
       bool ok = take(true);
-      if constexpr (kMode == kLogits)
-        for (int kp = t.kt0 + kLogitsPart<kPair>; kp < t.kt1 && ok; kp += kLogitsPart<kPair>) ok = take(false);
+      if constexpr (kPart<kPair, kMode> != INT_MAX)
+        for (int kp = t.kt0 + kPart<kPair, kMode>; kp < t.kt1 && ok; kp += kPart<kPair, kMode>) ok = take(false);
       if (!ok) break;
       // Hands this warp's rows over for storing, 128 bytes of each at a time: fill(c) gives this thread's
       // 16-byte piece c, keep(r, c, piece) stores piece c of row r of the warp's 32.
       auto turn = [&](int pieces, auto fill, auto keep) {
+        int lane = static_cast<int>(threadIdx.x & 31);
+        asm volatile("" : "+r"(lane));   // so that no address formed of it is kept (in local memory) from tile to tile
         uint8_t* mine = smem + L::kStages * L::kStage + (warp - 2) * 4096;
 #pragma unroll
         for (int c0 = 0; c0 < pieces; c0 += 8) {
@@ -482,28 +488,36 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       } else if constexpr (kMode == kGrad) {
         const int at_row = min(row, p.M - 1);
         const int64_t label = p.labels[at_row];
-        const int64_t at = label - p.v0 - col0;
+        const int64_t from = label - p.v0 - col0;
+        const int at = from >= 0 && from < kC ? static_cast<int>(from) : -1;   // the label's place among this thread's columns
         const bool counted = label != p.ignore;
         float g = p.dloss[at_row];
         g = gmax > 0.f ? g / gmax : g;          // gmax == 0: every finite entry is zero
         if (label < 0 || label >= p.vocab) g = NAN;
         const float l2 = p.lse[at_row] * kLog2e;
-        auto leave = [&](auto second) {
-          constexpr bool kSecond = decltype(second)::value;
-          turn(kC / 8, [&](int i) {
-            float d[8];
+        // dz in the logits' place: of two neighbours the bf16 pair in the first one's register, and what it left out in the second's
+        // (of an infinite or NaN entry the first term says all).
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int k = 8 * i + e;
-              float q = ex2(fmaf(__uint_as_float(v[k >> 5][k & 31]), kLog2e, -l2));
-              if (k == at) q -= 1.f;
-              d[e] = counted ? q * g : 0.f;
-              if constexpr (kSecond) {   // of an infinite or NaN entry the first term says all
-                const float left = d[e] - __bfloat162float(__float2bfloat16_rn(d[e]));
-                d[e] = fabsf(left) <= 1.f ? left : 0.f;
-              }
-            }
-            return make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+        for (int k = 0; k < kC; k += 2) {
+          float d[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float q = ex2(fmaf(__uint_as_float(v[k >> 5][(k + e) & 31]), kLog2e, -l2));
+            if (k + e == at) q -= 1.f;
+            d[e] = counted ? q * g : 0.f;
+          }
+          const uint32_t pair = pack_bf16(d[0], d[1]);
+          v[k >> 5][k & 31] = pair;
+          if constexpr (kPair == 1) {
+            const float l0 = d[0] - __uint_as_float(pair << 16), l1 = d[1] - __uint_as_float(pair & 0xffff0000u);
+            v[k >> 5][(k + 1) & 31] = pack_bf16(fabsf(l0) <= 1.f ? l0 : 0.f, fabsf(l1) <= 1.f ? l1 : 0.f);
+          }
+        }
+        auto leave = [&](auto second) {
+          constexpr int kSecond = decltype(second)::value;
+          turn(kC / 8, [&](int i) {
+            const int k = 8 * i + kSecond;
+            return make_uint4(v[k >> 5][k & 31], v[k >> 5][(k + 2) & 31], v[k >> 5][(k + 4) & 31], v[k >> 5][(k + 6) & 31]);
           }, [&](int r, int c, const uint4& piece) {
             if (row_w + r < p.M && col0 + 8 * c < p.N)
               *reinterpret_cast<uint4*>(p.dz + static_cast<int64_t>(row_w + r + (kSecond ? p.term : 0)) * p.ld_dz + col0 + 8 * c) = piece;

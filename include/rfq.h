@@ -345,12 +345,13 @@ rfq_status_t rfq_gemm_mxfp8(const void* qx_codes, const void* qx_scales,
  *            asked for; both zero: the forward pass alone).  Nothing in it is carried from
  *            one call to the next; calls that may run at the same time (other streams, other
  *            captured graphs) need workspaces of their own.
- * Logits are fp32 sums of exact products; the row maximum and sum are fp32, their last
- * join fp64.  dz is rounded to bf16 relative to the largest |dloss| (so a constant dloss
- * costs no rounding), to 16 bits for T <= 16, and both gradients are fp32 sums rounded once
- * to bf16.  A row with a
- * non-finite logit other than -inf has a non-finite loss.  T == 0 launches nothing, except
- * that dw is then zeroed.  Results do not depend on timing: no atomics.
+ * Logits are fp32 sums of exact products, the same in both passes; the row maximum and sum are fp32,
+ * their last join fp64.  exp(z - lse) is off by 2 |lse| 2^-24 + 2^-22 of itself (lse is passed in fp32); dz is
+ * rounded to bf16 relative to the largest |dloss| (so a constant dloss costs no rounding), to
+ * 16 bits for T <= 16, and both gradients are fp32 sums rounded once to bf16.  Logits have to
+ * stay below 2^127 in size (-inf aside).  A row with a non-finite logit other than -inf has a
+ * non-finite loss.  T == 0 launches nothing, except that dw is then zeroed.  Results do not
+ * depend on timing: no atomics.
  */
 size_t rfq_linear_ce_workspace_bytes(int64_t T, int64_t D, int64_t V, int want_dh, int want_dw);
 rfq_status_t rfq_linear_ce(const void* h_bf16, const void* w_bf16, const int64_t* labels, int64_t T, int64_t D,

@@ -26,3 +26,38 @@ def test_ignored_rows_of_hidden_states_may_hold_anything(rfq, T, D, V, bad):
     assert torch.equal(got[1], want[1])
     _, dw = rfq.linear_ce_backward_alloc(h, w, labels, lse2, dloss, want_dh=False)
     assert torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("T", [8, 20, 200])
+@pytest.mark.parametrize("D", [4096, 65536])
+def test_certain_labels(rfq, T, D):
+    """Rows whose label has p = 1 - 1e-3: the label's term of the gradient is held to its own size, 1 - p.
+
+    By arithmetic: 1 - p is off by 2 |dz| (1 - p) where every logit is off by dz <= 1e-5 sum |h w| in the same way in both
+    passes, and by p (2 |lse| 2^-24 + 2^-22): lse is kept in fp32, scaled by log2 e in fp32, and the exponential has 2^-22.
+    (The two passes' logits differing by 3e-6 of their size, as sums of 4096 and of 1024 terms do, would be 4e-5 here: 4 % of 1 - p.)
+    dz is rounded to bf16 (2^-8), dw and dh are fp32 sums (1e-5 of their terms) rounded once."""
+    V, y0 = 300, 7
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    h = (0.5 + torch.rand((T, D), generator=g, device="cuda")).bfloat16()
+    w = torch.randn((V, D), generator=g, device="cuda") / D ** 0.5
+    w[y0] = 12.8 / D * (0.5 + torch.rand((D,), generator=g, device="cuda"))
+    w = w.bfloat16()
+    labels = torch.full((T,), y0, device="cuda")
+    dloss = torch.ones(T, device="cuda")
+    h64, w64 = h.double(), w.double()
+    z = h64 @ w64.T
+    lse64 = torch.logsumexp(z, 1)
+    p = torch.exp(z - lse64[:, None])
+    dz = p.clone()
+    others = p.clone()
+    others[:, y0] = 0
+    dz[:, y0] = -others.sum(1)   # p - 1 without the cancellation
+    assert ((-dz[:, y0] > 1e-4) & (-dz[:, y0] < 1e-2)).all()
+    z_tol = 1e-5 * float((h64.abs() @ w64.abs().T).max())
+    term = (2.0 ** -8 + 2 * z_tol + 2e-5) * dz.abs() + p * (2 * lse64.abs()[:, None] * 2.0 ** -24 + 2.0 ** -22)
+    _, lse = rfq.linear_ce_alloc(h, w, labels)
+    dh, dw = rfq.linear_ce_backward_alloc(h, w, labels, lse, dloss)
+    check("dw", dw, (dz.T @ h64, term.T @ h64.abs() + 2.0 ** -8 * (dz.T @ h64).abs()))
+    check("dh", dh, (dz @ w64, term @ w64.abs() + 2.0 ** -8 * (dz @ w64).abs()))
