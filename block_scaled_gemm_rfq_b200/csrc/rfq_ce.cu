@@ -41,7 +41,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <climits>
 #include <cstdint>
 #include <type_traits>
 
@@ -74,8 +73,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The backward pass (kGrad) takes the same parts, so that its logits are those that lse is of: where a label is nearly
 // certain p - 1 cancels, and a drift between the two was 17 % of 1 - p = 1e-3 at D = 4096.  It costs dh of 64 rows against 50000 x
 // 2048 94 -> 100 us (the epilogue of a tile holds up the parts of the next), of 1000 rows against 50001 x 2048 330 -> 335.
+// The gradients are rounded to bf16, but dw sums over up to 2^24 rows and dh over pieces of millions of entries: a sum of one
+// sign over 2^24 rows lost 1 %.  They take 4096 at a time.
 template <int kPair, int kMode>
-constexpr int kPart = kMode == kLogits || kMode == kGrad ? (kPair == 2 ? 16 : 2) : INT_MAX;   // k-tiles
+constexpr int kPart = kMode == kLogits || kMode == kGrad ? (kPair == 2 ? 16 : 2) : 64;   // k-tiles
+// Contractions that fit one part have kernels of their own (kParts false): the sums over parts cost the epilogue registers, and
+// where it bounds the product that shows (dw of 64 rows of 50000 x 2048 110 -> 160 us).  Not the forward logits, which have
+// registers left, and the backward ones of few rows, whose parts are short.
+template <int kPair, int kMode>
+constexpr bool kAlwaysParts = kMode == kLogits || (kMode == kGrad && kPair == 1);
 // dz is rounded to bf16 for the next products.  Over many rows those roundings average out; a few rows leave
 // a gradient that is off by one rounding of its largest entries, beside its own.  Up to 16 rows dz is therefore
 // kept as the sum of two bf16 terms: rows T .. 2 T - 1 of dz are what rows 0 .. T - 1 left out.  dh takes both
@@ -220,7 +226,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-template <int kPair, int kMode, int kN>
+template <int kPair, int kMode, int kN, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_constant__ Maps maps, const Params p) {
   using L = Layout<kPair, kMode, kN>;
   constexpr int kC = kN / 2;   // columns of an epilogue thread
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       bool ok = true;
       for (int item = unit; item < items && ok; item += p.share.units) {
         if (!work_at(p, item, t)) continue;
-        const int part = min(kPart<kPair, kMode>, t.kt1 - t.kt0);
+        const int part = kParts ? kPart<kPair, kMode> : t.kt1 - t.kt0;
         for (int kp = t.kt0; kp < t.kt1 && ok; kp += part) {
           if (!mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag, &g_ce_error, kErrWaitAccEmpty)) {
             ok = false;
@@ -429,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
         return true;
       };
       bool ok = take(true);
-      if constexpr (kPart<kPair, kMode> != INT_MAX)
+      if constexpr (kParts)
         for (int kp = t.kt0 + kPart<kPair, kMode>; kp < t.kt1 && ok; kp += kPart<kPair, kMode>) ok = take(false);
       if (!ok) break;
       // Hands this warp's rows over for storing, 128 bytes of each at a time: fill(c) gives this thread's
@@ -767,7 +773,10 @@ Share share_out(int64_t M, int64_t N, int64_t K, Cut cut, int columns = kBN) {
 template <int kPair, int kMode, int kN>
 cudaError_t launch_mode(const Maps& maps, const Params& p, cudaStream_t stream) {
   using L = Layout<kPair, kMode, kN>;
-  auto kernel = rfq_ce_kernel<kPair, kMode, kN>;
+  const int longest = p.share.whole > 0 ? p.num_kt : p.share.slice_kt;
+  auto kernel = rfq_ce_kernel<kPair, kMode, kN, true>;
+  if constexpr (!kAlwaysParts<kPair, kMode>)
+    if (longest <= kPart<kPair, kMode>) kernel = rfq_ce_kernel<kPair, kMode, kN, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   int units = p.share.units;

@@ -61,3 +61,21 @@ def test_certain_labels(rfq, T, D):
     dh, dw = rfq.linear_ce_backward_alloc(h, w, labels, lse, dloss)
     check("dw", dw, (dz.T @ h64, term.T @ h64.abs() + 2.0 ** -8 * (dz.T @ h64).abs()))
     check("dh", dh, (dz @ w64, term @ w64.abs() + 2.0 ** -8 * (dz @ w64).abs()))
+
+
+def test_head_gradient_of_very_many_rows(rfq):
+    """2^24 - 3 rows, as many as a call takes: with equal logits dz is 1/64 (exact in bf16) for all entries but the label's, and
+    all terms of dw have one sign.  p is off by 1e-5 at most (lse of 64 equal logits), dw is rounded once, and its
+    sum over the rows may lose 2^-12 (one accumulator that truncates at every step loses 1 %)."""
+    T, D, V = (1 << 24) - 3, 8, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    h = (0.5 + torch.rand((T, D), generator=g, device="cuda")).bfloat16()
+    w = torch.zeros((V, D), dtype=torch.bfloat16, device="cuda")
+    labels = torch.zeros(T, dtype=torch.int64, device="cuda")
+    lse = torch.full((T,), 64.0, device="cuda").log_()
+    dloss = torch.ones(T, device="cuda")
+    _, dw = rfq.linear_ce_backward_alloc(h, w, labels, lse, dloss, want_dh=False)
+    total = sum(part.double().sum(0) for part in h.split(1 << 22))
+    want = total[None, :] * torch.cat([torch.full((1, 1), 1 / 64 - 1.0), torch.full((V - 1, 1), 1 / 64)]).double().cuda()
+    assert ((dw.double() - want).abs() <= (2.0 ** -8 + 1e-5 + 2.0 ** -12) * want.abs()).all()
