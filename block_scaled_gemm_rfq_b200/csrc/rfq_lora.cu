@@ -214,16 +214,12 @@ struct ShrinkParams {
 constexpr int kBK = 128;                         // contraction elements of one stage
 constexpr int kRowStride = odd_stride(kBK * 2);  // of a 256-byte row segment
 __host__ __device__ constexpr int shrink_p_bytes(int r) { return kBK * rank_stride(r); }
-__host__ __device__ constexpr int shrink_red_bytes(int r) {
-  return (8 / (kRows / 16) - 1) * kRows * r * 4;
-}
+constexpr int kWarps = kThreads / 32;
+static_assert(kRows == 16 && kBK / 16 == kWarps, "an item is one MMA tile of rows; each warp takes one k16 step of a stage");
+__host__ __device__ constexpr int shrink_red_bytes(int r) { return (kWarps - 1) * kRows * r * 4; }
 
 template <int kJ>   // 8-column tiles of the rank, at most
 __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkParams p) {
-  constexpr int kWm = kRows / 16;               // warps along the rows
-  constexpr int kWk = 8 / kWm;                  // warps along a stage's contraction
-  constexpr int kSteps = kBK / 16 / kWk;        // k16 steps of a warp in one stage
-  constexpr int kXCopies = kRows / 16;          // row pieces of 16 bytes a thread copies per stage
   constexpr int kPCopies = kJ * 8 * (kBK / 8) / kThreads;   // of the adapter's weights, at most
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) Groups g;
@@ -235,30 +231,22 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
   if (z == 0 && blockIdx.y == 0) leave_groups(g, p.table + (blockIdx.x / p.zs) * kTable);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wm = warp % kWm, wk = warp / kWm;
   const int jt = p.r / 8;
   const int p_stride = rank_stride(p.r);
   const int stage_bytes = kRows * kRowStride + shrink_p_bytes(p.r);
   const uint32_t base = smem_addr(smem);
-  float* red = reinterpret_cast<float*>(smem + p.stages * stage_bytes);   // [kWk - 1][kRows][r]
+  float* red = reinterpret_cast<float*>(smem + p.stages * stage_bytes);   // [kWarps - 1][kRows][r]
   const int64_t c0 = static_cast<int64_t>(blockIdx.y) * p.c_split;
   const int64_t c1 = min(p.C, c0 + p.c_split);
   const int iters = static_cast<int>(ceil_div(c1 - c0, kBK));
-  const int qx = tid & 15;                      // this thread's 16-byte piece of a 256-byte row segment
+  const int xm = tid >> 4, qx = tid & 15;       // this thread's 16-byte piece of a stage: row, place in its 256 bytes
 
   for (int item = z; item < g.items; item += p.zs) {
     const int first = g.start[item], rows = g.start[item + 1] - first;
     const int a = g.ids[g.order[first]];
     if (a == INT_MAX) break;   // rows without an adapter come last
-    const __nv_bfloat16* x_at[kXCopies];
-    unsigned x_row = 0;
-#pragma unroll
-    for (int u = 0; u < kXCopies; ++u) {
-      const int m = (tid >> 4) + 16 * u;
-      const bool has = m < rows;
-      x_row |= static_cast<unsigned>(has) << u;
-      x_at[u] = p.src + (row0 + g.order[has ? first + m : first]) * p.C + c0 + 8 * qx;
-    }
+    const bool has_x = xm < rows;
+    const __nv_bfloat16* x_at = p.src + (row0 + g.order[has_x ? first + xm : first]) * p.C + c0 + 8 * qx;
     const __nv_bfloat16* pa = p.p + static_cast<int64_t>(a) * p.r * p.C;
     const __nv_bfloat16* p_at[kPCopies];
     uint32_t p_to[kPCopies];
@@ -275,12 +263,9 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
     auto load = [&]() {
       if (load_left > 0) {
         const uint32_t sx = base + load_stage * stage_bytes, sp = sx + kRows * kRowStride;
-#pragma unroll
-        for (int u = 0; u < kXCopies; ++u) {
-          const bool ok = (x_row >> u & 1u) && 8 * qx < load_left;
-          cp_async16(sx + ((tid >> 4) + 16 * u) * kRowStride + 16 * qx, ok ? x_at[u] : p.src, ok);
-          x_at[u] += kBK;
-        }
+        const bool ok_x = has_x && 8 * qx < load_left;
+        cp_async16(sx + xm * kRowStride + 16 * qx, ok_x ? x_at : p.src, ok_x);
+        x_at += kBK;
 #pragma unroll
         for (int u = 0; u < kPCopies; ++u)
           if (p_k[u] < kBK) {
@@ -306,42 +291,36 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
       __syncthreads();
       load();
       const uint32_t sx = base + stage * stage_bytes, sp = sx + kRows * kRowStride;
-      if (wm * 16 < rows) {
+      uint32_t fa[4];
+      ldsm4<false>(fa, sx + (lane & 15) * kRowStride + 32 * warp + (lane >> 4) * 16);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const int ks = wk * kSteps + s;
-          uint32_t fa[4];
-          ldsm4<false>(fa, sx + (wm * 16 + (lane & 15)) * kRowStride + 32 * ks + (lane >> 4) * 16);
-#pragma unroll
-          for (int j = 0; j < kJ; j += 2) {
-            if (j + 1 < jt) {
-              uint32_t fb[4];
-              ldsm4<true>(fb, sp + (ks * 16 + (lane & 15)) * p_stride + (j + (lane >> 4)) * 16);
-              mma16816(acc[j], fa, fb[0], fb[1]);
-              mma16816(acc[j + 1], fa, fb[2], fb[3]);
-            } else if (j < jt) {
-              uint32_t fb[2];
-              ldsm2<true>(fb, sp + (ks * 16 + (lane & 15)) * p_stride + j * 16);
-              mma16816(acc[j], fa, fb[0], fb[1]);
-            }
-          }
+      for (int j = 0; j < kJ; j += 2) {
+        if (j + 1 < jt) {
+          uint32_t fb[4];
+          ldsm4<true>(fb, sp + (warp * 16 + (lane & 15)) * p_stride + (j + (lane >> 4)) * 16);
+          mma16816(acc[j], fa, fb[0], fb[1]);
+          mma16816(acc[j + 1], fa, fb[2], fb[3]);
+        } else if (j < jt) {
+          uint32_t fb[2];
+          ldsm2<true>(fb, sp + (warp * 16 + (lane & 15)) * p_stride + j * 16);
+          mma16816(acc[j], fa, fb[0], fb[1]);
         }
       }
       if (++stage == p.stages) stage = 0;
     }
-    // Join the warps that shared a row tile, in order; the first of them writes [rows][r].
-    const int ra = wm * 16 + (lane >> 2), rb = ra + 8;
-    if (wk > 0) {
+    // Join the warps, in order; the first of them writes [rows][r].
+    const int ra = lane >> 2, rb = ra + 8;
+    if (warp > 0) {
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
         if (j < jt) {
-          float* at = red + ((wk - 1) * kRows + ra) * p.r + j * 8 + 2 * (lane & 3);
+          float* at = red + ((warp - 1) * kRows + ra) * p.r + j * 8 + 2 * (lane & 3);
           *reinterpret_cast<float2*>(at) = make_float2(acc[j][0], acc[j][1]);
           *reinterpret_cast<float2*>(at + 8 * p.r) = make_float2(acc[j][2], acc[j][3]);
         }
     }
     __syncthreads();
-    if (wk == 0) {
+    if (warp == 0) {
       float* out = p.part + static_cast<int64_t>(blockIdx.y) * p.M * p.r;
       const int64_t row_a = ra < rows ? row0 + g.order[first + ra] : -1, row_b = rb < rows ? row0 + g.order[first + rb] : -1;
 #pragma unroll
@@ -350,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_shrink_kernel(const ShrinkP
           const int col = j * 8 + 2 * (lane & 3);
           float2 va = make_float2(acc[j][0], acc[j][1]), vb = make_float2(acc[j][2], acc[j][3]);
 #pragma unroll
-          for (int w = 0; w < kWk - 1; ++w) {
+          for (int w = 0; w < kWarps - 1; ++w) {
             const float2 ua = *reinterpret_cast<const float2*>(red + (w * kRows + ra) * p.r + col);
             const float2 ub = *reinterpret_cast<const float2*>(red + (w * kRows + rb) * p.r + col);
             va.x += ua.x;
@@ -421,12 +400,9 @@ __host__ __device__ constexpr int expand_s_bytes(int r) {
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandParams p) {
   constexpr int kT = kExpandTerms<kF32>;
-  constexpr int kWm = kRows / 16, kWn = 8 / kWm;
   constexpr int kCols = kBN<kF32>;
-  constexpr int kWarpCols = kCols / kWn;
-  constexpr int kPairs = kWarpCols >= 16 ? 2 : 1;      // 8-column tiles a warp takes at once
+  constexpr int kPairs = kCols / kWarps / 8;           // 8-column tiles of a warp: two, or one of fp32
   constexpr int kSize = kF32 ? 4 : 2;
-  constexpr int kCopies = kRows / 16;                  // row pieces of 16 bytes a thread copies per tile
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) Groups g;
   griddep_launch_dependents();
@@ -436,7 +412,6 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
   take_groups(g, p.table + (blockIdx.x / p.zs) * kTable);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wm = warp % kWm, wn = warp / kWm;
   constexpr int q_stride = kQStride<kF32>;
   const int s_stride = odd_stride(2 * p.r);
   const int stage_bytes = expand_stage_bytes<kF32>(p.r);
@@ -445,8 +420,8 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
   const int64_t begin = static_cast<int64_t>(blockIdx.y) * p.tiles * kCols;
   const int64_t end = min(p.C, begin + static_cast<int64_t>(p.tiles) * kCols);
   const int iters = static_cast<int>(ceil_div(end - begin, kCols));
-  const int qx = tid & 15;
-  constexpr int kPiece = 16 / kSize;                   // columns of a 16-byte piece
+  const int xm = tid >> 4, qx = tid & 15;              // this thread's 16-byte piece of a tile
+  constexpr int kPiece = 16 / kSize;                   // its columns
   const uint8_t* from = static_cast<const uint8_t*>(p.base);
   uint8_t* to = static_cast<uint8_t*>(p.out);
 
@@ -456,26 +431,19 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
     const bool with = a != INT_MAX;
     // Rows without an adapter (they come last) keep what they have where the base is the output itself.
     if (!with && p.base == p.out) continue;
-    int64_t at[kCopies];        // byte offset of this thread's pieces, in the base and in the output
-    unsigned has = 0;
-#pragma unroll
-    for (int u = 0; u < kCopies; ++u) {
-      const int m = (tid >> 4) + 16 * u;
-      has |= static_cast<unsigned>(m < rows) << u;
-      at[u] = ((row0 + g.order[m < rows ? first + m : first]) * p.C + begin) * kSize + 16 * qx;
-    }
+    const bool has = xm < rows;
+    // Byte offset of this thread's piece, in the base and in the output.
+    const int64_t at = ((row0 + g.order[has ? first + xm : first]) * p.C + begin) * kSize + 16 * qx;
     const __nv_bfloat16* qa = p.q + (with ? static_cast<int64_t>(a) * p.r * p.C : 0);
     int load_stage = 0, load_it = 0;
     auto load = [&]() {
       if (load_it < iters) {
         const uint32_t sb = base + load_stage * stage_bytes, sq = sb + kRows * kRowStride;
         const int left = static_cast<int>(min(static_cast<int64_t>(kCols), end - begin - static_cast<int64_t>(load_it) * kCols));
-        if (from != nullptr)
-#pragma unroll
-          for (int u = 0; u < kCopies; ++u) {
-            const bool ok = (has >> u & 1u) && kPiece * qx < left;
-            cp_async16(sb + ((tid >> 4) + 16 * u) * kRowStride + 16 * qx, ok ? from + at[u] + load_it * 256 : from, ok);
-          }
+        if (from != nullptr) {
+          const bool ok = has && kPiece * qx < left;
+          cp_async16(sb + xm * kRowStride + 16 * qx, ok ? from + at + load_it * 256 : from, ok);
+        }
         if (with) {
           const int64_t c = begin + static_cast<int64_t>(load_it) * kCols;
           constexpr int kQ = kCols / 8;
@@ -511,78 +479,72 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
       uint8_t* sb = smem + stage * stage_bytes;
       const uint32_t sq = base + stage * stage_bytes + kRows * kRowStride;
       const int left = static_cast<int>(min(static_cast<int64_t>(kCols), end - begin - static_cast<int64_t>(it) * kCols));
-      if (wm * 16 < rows && (with || from == nullptr)) {
+      const int col = warp * (8 * kPairs);
+      if (col < left && (with || from == nullptr)) {
+        float acc[2][4];
 #pragma unroll
-        for (int col = wn * kWarpCols; col < (wn + 1) * kWarpCols; col += 8 * kPairs) {
-          if (col >= left) break;
-          float acc[2][4];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-          if (with) {
-            int ks = 0;
-            for (; ks < p.r / 16; ++ks) {
-              uint32_t fb[4];
-              if constexpr (kPairs == 2) {
-                ldsm4<true>(fb, sq + (ks * 16 + (lane & 15)) * q_stride + col * 2 + (lane >> 4) * 16);
-              } else {
-                uint32_t f2[2];
-                ldsm2<true>(f2, sq + (ks * 16 + (lane & 15)) * q_stride + col * 2);
-                fb[0] = f2[0];
-                fb[1] = f2[1];
-              }
-#pragma unroll
-              for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
-                uint32_t fa[4];
-                ldsm4<false>(fa, s_base + (e * kRows + wm * 16 + (lane & 15)) * s_stride + 32 * ks + (lane >> 4) * 16);
-                mma16816(acc[0], fa, fb[0], fb[1]);
-                if constexpr (kPairs == 2) mma16816(acc[1], fa, fb[2], fb[3]);
-              }
+          for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+        if (with) {
+          int ks = 0;
+          for (; ks < p.r / 16; ++ks) {
+            uint32_t fb[4];
+            if constexpr (kPairs == 2) {
+              ldsm4<true>(fb, sq + (ks * 16 + (lane & 15)) * q_stride + col * 2 + (lane >> 4) * 16);
+            } else {
+              uint32_t f2[2];
+              ldsm2<true>(f2, sq + (ks * 16 + (lane & 15)) * q_stride + col * 2);
+              fb[0] = f2[0];
+              fb[1] = f2[1];
             }
-            if (p.r & 8) {   // the last eight of the rank
-              uint32_t fb[2];
-              // With one 8-column tile both halves of the load read it.
-              ldsm2<true>(fb, sq + (ks * 16 + (lane & 7)) * q_stride + col * 2 + (kPairs == 2 ? (lane >> 3) & 1 : 0) * 16);
 #pragma unroll
-              for (int e = kT - 1; e >= 0; --e) {
-                uint32_t fa[2];
-                ldsm2<false>(fa, s_base + (e * kRows + wm * 16 + (lane & 15)) * s_stride + 32 * ks);
-                mma1688(acc[0], fa, fb[0]);
-                if constexpr (kPairs == 2) mma1688(acc[1], fa, fb[1]);
-              }
+            for (int e = kT - 1; e >= 0; --e) {   // smallest terms first
+              uint32_t fa[4];
+              ldsm4<false>(fa, s_base + (e * kRows + (lane & 15)) * s_stride + 32 * ks + (lane >> 4) * 16);
+              mma16816(acc[0], fa, fb[0], fb[1]);
+              if constexpr (kPairs == 2) mma16816(acc[1], fa, fb[2], fb[3]);
             }
           }
+          if (p.r & 8) {   // the last eight of the rank
+            uint32_t fb[2];
+            // With one 8-column tile both halves of the load read it.
+            ldsm2<true>(fb, sq + (ks * 16 + (lane & 7)) * q_stride + col * 2 + (kPairs == 2 ? (lane >> 3) & 1 : 0) * 16);
 #pragma unroll
-          for (int i = 0; i < kPairs; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint8_t* o = sb + (wm * 16 + 8 * h + (lane >> 2)) * kRowStride + (col + 8 * i + 2 * (lane & 3)) * kSize;
-              float x = acc[i][2 * h], y = acc[i][2 * h + 1];
-              if constexpr (kF32) {
-                if (from != nullptr) {
-                  const float2 b = *reinterpret_cast<const float2*>(o);
-                  x += b.x;
-                  y += b.y;
-                }
-                *reinterpret_cast<float2*>(o) = make_float2(x, y);
-              } else {
-                if (from != nullptr) {
-                  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o));
-                  x += b.x;
-                  y += b.y;
-                }
-                *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(x, y);
-              }
+            for (int e = kT - 1; e >= 0; --e) {
+              uint32_t fa[2];
+              ldsm2<false>(fa, s_base + (e * kRows + (lane & 15)) * s_stride + 32 * ks);
+              mma1688(acc[0], fa, fb[0]);
+              if constexpr (kPairs == 2) mma1688(acc[1], fa, fb[1]);
             }
+          }
         }
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint8_t* o = sb + (8 * h + (lane >> 2)) * kRowStride + (col + 8 * i + 2 * (lane & 3)) * kSize;
+            float x = acc[i][2 * h], y = acc[i][2 * h + 1];
+            if constexpr (kF32) {
+              if (from != nullptr) {
+                const float2 b = *reinterpret_cast<const float2*>(o);
+                x += b.x;
+                y += b.y;
+              }
+              *reinterpret_cast<float2*>(o) = make_float2(x, y);
+            } else {
+              if (from != nullptr) {
+                const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o));
+                x += b.x;
+                y += b.y;
+              }
+              *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(x, y);
+            }
+          }
       }
       __syncthreads();
-      if (kPiece * qx < left)
-#pragma unroll
-        for (int u = 0; u < kCopies; ++u)
-          if (has >> u & 1u)
-            *reinterpret_cast<uint4*>(to + at[u] + it * 256) = *reinterpret_cast<const uint4*>(sb + ((tid >> 4) + 16 * u) * kRowStride + 16 * qx);
+      if (has && kPiece * qx < left)
+        *reinterpret_cast<uint4*>(to + at + it * 256) = *reinterpret_cast<const uint4*>(sb + xm * kRowStride + 16 * qx);
       if (++stage == p.stages) stage = 0;
     }
     __syncthreads();   // the next group's copies and s' go where this one's were
@@ -912,9 +874,8 @@ __host__ __device__ constexpr int outer_stage_bytes(int r) {
   return kOuterRows * (kWStride + outer_v_stride<kT>(r));
 }
 // Stages of the ring (four of the largest, rank 128 in three terms, fill one SM's shared memory).
-template <int kJ16, int kT>
 constexpr int kOuterStages = 4;
-constexpr int kMostBesideOuter = 4 * outer_stage_bytes<3>(128) + 64;
+constexpr int kMostBesideOuter = kOuterStages * outer_stage_bytes<3>(128) + 64;
 static_assert(kMostBesideOuter + kOuterStatic + 1024 <= kSmemLimit, "the largest ring fits");
 
 template <int kJ16, int kT>   // kJ16: 16-row tiles of the rank, at most
@@ -942,7 +903,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
   const int qx = tid & 15;
   const bool qx_ok = c0 + 8 * qx < s.C;
   // This thread's 16-byte pieces of a stage's v: row, element in v, place in the stage.
-  constexpr int kS = kOuterStages<kJ16, kT>;
+  constexpr int kS = kOuterStages;
   const uint32_t w_to = (tid >> 4) * kWStride + 16 * qx;
   const int w_size = qx_ok ? 16 : 0;
   const int64_t w_step = 16 * s.C;
@@ -1041,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_outer_kernel(const OuterPar
         load_to = base;
       }
     };
-    // fp32 results: the MMAs add by truncation, so each stage's 64 rows are summed on their own and
+    // fp32 results: the MMAs add by truncation, so each stage's 32 rows are summed on their own and
     // added to the rest with rounding.
     constexpr bool kFlush = kT == 3;
     float acc[kJ16][2][4], sum[kFlush ? kJ16 : 1][2][4];
@@ -1396,7 +1357,7 @@ cudaError_t forward_typed(const ForwardParams& p, int64_t clusters, cudaStream_t
 template <int kJ16, int kT>
 cudaError_t outer_typed(const OuterParams& p, dim3 grid, cudaStream_t stream) {
   // The last row's fragments may reach past its end.
-  return launch(rfq_lora_outer_kernel<kJ16, kT>, p, grid, static_cast<size_t>(kOuterStages<kJ16, kT>) * outer_stage_bytes<kT>(p.r) + 64,
+  return launch(rfq_lora_outer_kernel<kJ16, kT>, p, grid, static_cast<size_t>(kOuterStages) * outer_stage_bytes<kT>(p.r) + 64,
                 kMostBesideOuter, stream);
 }
 template <int kT>
