@@ -101,7 +101,7 @@ struct Layout {
   static constexpr uint32_t kStage = kATile + kBTile;
   static constexpr uint32_t kBarrierBytes = 256;
   static constexpr uint32_t kOut = kMode == kLogits ? 0u : 8u * 4096u;
-  static constexpr int kStages = static_cast<int>((kSmemLimit - 1024 - kBarrierBytes - kOut) / kStage);   // 4 (single); 7 or 6; 9 or 7 (narrow)
+  static constexpr int kStages = static_cast<int>((kSmemLimit - 1024 - kBarrierBytes - kOut) / kStage);   // 4 (single), 7 or 6 (pair), 9 or 8 (narrow)
   static constexpr uint32_t kSmem = kStages * kStage + kOut + kBarrierBytes + 1024;
   static_assert(kStage % 1024 == 0, "stage buffers must keep 1 KiB alignment");
   static_assert(kSmem <= kSmemLimit, "exceeds the 227 KiB shared-memory limit");
