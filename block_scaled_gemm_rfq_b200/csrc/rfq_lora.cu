@@ -579,6 +579,8 @@ struct ForwardParams {
   int cluster, parts;         // parts: clusters that share the columns of one item, each with all of its shrink
 };
 
+constexpr int64_t kSumPart = 16384;   // contraction elements that a CTA adds up in the MMAs' accumulators
+
 template <int kJ, bool kF32>   // kJ: 8-column tiles of the rank, at most
 __global__ void __launch_bounds__(kThreads, kJ <= 8 ? 2 : 1) rfq_lora_forward_kernel(const ForwardParams p) {
   constexpr int kT = kExpandTerms<kF32>;
@@ -618,64 +620,77 @@ __global__ void __launch_bounds__(kThreads, kJ <= 8 ? 2 : 1) rfq_lora_forward_ke
     // Column of this lane's fragment row in tile i of expand: 8 (g / 2) + 2 i + (g & 1).
     const __nv_bfloat16* qa = with ? p.b + (static_cast<int64_t>(a) * p.N + 8 * (line >> 1) + (line & 1)) * p.r : p.b;
     if (with) {
-      float acc[kJ][4];
-#pragma unroll
-      for (int j = 0; j < kJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
       const __nv_bfloat16* xa = p.x + row[0] * p.K;
       const __nv_bfloat16* xb = p.x + row[1] * p.K;
       const __nv_bfloat16* pa = p.a + (static_cast<int64_t>(a) * p.r + line) * p.K;
-#pragma unroll(kJ <= 4 ? 2 : 1)
-      for (int64_t c = k0 + 32 * warp + 8 * quad; c < k1 + 8 * quad; c += 8 * 32) {
-        const bool ok = c < k1;
-        const uint4 ua = ok && has[0] ? *reinterpret_cast<const uint4*>(xa + c) : zero4;
-        const uint4 ub = ok && has[1] ? *reinterpret_cast<const uint4*>(xb + c) : zero4;
-        const uint32_t f0[4] = {ua.x, ub.x, ua.y, ub.y}, f1[4] = {ua.z, ub.z, ua.w, ub.w};
-        uint4 w[kJ];
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) w[j] = ok && j < jt ? *reinterpret_cast<const uint4*>(pa + 8 * j * p.K + c) : zero4;
+      // The MMAs add by truncation (7e-4 of a sum of one sign over 2^20 elements, 2.7e-6 in parts of 16384): a part at a time, added with rounding.
+      for (int64_t s0 = k0; s0 == k0 || s0 < k1; s0 += kSumPart) {
+        const int64_t s1 = min(k1, s0 + kSumPart);
+        float acc[kJ][4];
 #pragma unroll
         for (int j = 0; j < kJ; ++j)
-          if (j < jt) {
-            mma16816(acc[j], f0, w[j].x, w[j].y);
-            mma16816(acc[j], f1, w[j].z, w[j].w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll(kJ <= 4 ? 2 : 1)
+        for (int64_t c = s0 + 32 * warp + 8 * quad; c < s1 + 8 * quad; c += 8 * 32) {
+          const bool ok = c < s1;
+          const uint4 ua = ok && has[0] ? *reinterpret_cast<const uint4*>(xa + c) : zero4;
+          const uint4 ub = ok && has[1] ? *reinterpret_cast<const uint4*>(xb + c) : zero4;
+          const uint32_t f0[4] = {ua.x, ub.x, ua.y, ub.y}, f1[4] = {ua.z, ub.z, ua.w, ub.w};
+          uint4 w[kJ];
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) w[j] = ok && j < jt ? *reinterpret_cast<const uint4*>(pa + 8 * j * p.K + c) : zero4;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+            if (j < jt) {
+              mma16816(acc[j], f0, w[j].x, w[j].y);
+              mma16816(acc[j], f1, w[j].z, w[j].w);
+            }
+        }
+        // The warps' sums: four and four, then the others to the first.
+        auto give = [&](int slot) {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            const int col = j * 8 + 2 * quad;
+            *reinterpret_cast<float2*>(&red[slot][line][col]) = make_float2(acc[j][0], acc[j][1]);
+            *reinterpret_cast<float2*>(&red[slot][line + 8][col]) = make_float2(acc[j][2], acc[j][3]);
           }
-      }
-      // The warps' sums: four and four, then the others to the first.
-      auto give = [&](int slot) {
+        };
+        auto take = [&](int slot) {
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const int col = j * 8 + 2 * quad;
-          *reinterpret_cast<float2*>(&red[slot][line][col]) = make_float2(acc[j][0], acc[j][1]);
-          *reinterpret_cast<float2*>(&red[slot][line + 8][col]) = make_float2(acc[j][2], acc[j][3]);
-        }
-      };
-      auto take = [&](int slot) {
+          for (int j = 0; j < kJ; ++j) {
+            const int col = j * 8 + 2 * quad;
+            const float2 ua = *reinterpret_cast<const float2*>(&red[slot][line][col]);
+            const float2 ub = *reinterpret_cast<const float2*>(&red[slot][line + 8][col]);
+            acc[j][0] += ua.x;
+            acc[j][1] += ua.y;
+            acc[j][2] += ub.x;
+            acc[j][3] += ub.y;
+          }
+        };
+        if (s0 > k0) __syncthreads();   // the first warp is done with the part before
+        if (warp >= 4) give(warp - 4);
+        __syncthreads();
+        if (warp < 4) take(warp);
+        __syncthreads();
+        if (warp > 0 && warp < 4) give(warp);
+        __syncthreads();
+        if (warp == 0) {
+          for (int w = 1; w < 4; ++w) take(w);
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const int col = j * 8 + 2 * quad;
-          const float2 ua = *reinterpret_cast<const float2*>(&red[slot][line][col]);
-          const float2 ub = *reinterpret_cast<const float2*>(&red[slot][line + 8][col]);
-          acc[j][0] += ua.x;
-          acc[j][1] += ua.y;
-          acc[j][2] += ub.x;
-          acc[j][3] += ub.y;
-        }
-      };
-      if (warp >= 4) give(warp - 4);
-      __syncthreads();
-      if (warp < 4) take(warp);
-      __syncthreads();
-      if (warp > 0 && warp < 4) give(warp);
-      __syncthreads();
-      if (warp == 0) {
-        for (int w = 1; w < 4; ++w) take(w);
+          for (int j = 0; j < kJ; ++j) {
+            const int col = j * 8 + 2 * quad;
+            float2* at[2] = {reinterpret_cast<float2*>(&sums[line * kJ * 8 + col]), reinterpret_cast<float2*>(&sums[(line + 8) * kJ * 8 + col])};
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const int col = j * 8 + 2 * quad;
-          *reinterpret_cast<float2*>(&sums[line * kJ * 8 + col]) = make_float2(acc[j][0], acc[j][1]);
-          *reinterpret_cast<float2*>(&sums[(line + 8) * kJ * 8 + col]) = make_float2(acc[j][2], acc[j][3]);
+            for (int h = 0; h < 2; ++h) {
+              float2 v = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+              if (s0 > k0) {
+                v.x += at[h]->x;
+                v.y += at[h]->y;
+              }
+              *at[h] = v;
+            }
+          }
         }
       }
       cluster_sync();   // every rank's sums are there
@@ -1263,14 +1278,14 @@ int64_t chunk_ctas(int64_t M, int64_t n, int64_t most) {
   return z > 1 ? z : 1;
 }
 
-// Splits of the shrink product's contraction: one wave of three CTAs per SM, 256 elements each at least.
+// Splits of the shrink product's contraction: one wave of three CTAs per SM, 256 elements each at least, kSumPart at most.
 int shrink_splits(int64_t M, int64_t C, int64_t n, int64_t* c_split, int* zs) {
   const int64_t chunks = ceil_div(M, kChunk), z = chunk_ctas(M, n, 2 * kPlanSms);
   const int64_t most = ceil_div(C, 256);
   int64_t s = 3 * kPlanSms / (chunks * z);
   if (s > most) s = most;
   if (s > 32) s = 32;
-  if (s < 1) s = 1;
+  if (s < ceil_div(C, kSumPart)) s = ceil_div(C, kSumPart);
   *c_split = ceil_div(ceil_div(C, s), 256) * 256;
   *zs = static_cast<int>(z);
   return static_cast<int>(ceil_div(C, *c_split));
