@@ -72,7 +72,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 8 rows against 32003 x 1024) and a loss of few rows has no others to average with (3e-6 -> 3e-7 for one row).
 // The backward pass (kGrad) takes the same parts, so that its logits are those that lse is of: where a label is nearly
 // certain p - 1 cancels, and a drift between the two was 17 % of 1 - p = 1e-3 at D = 4096.  It costs dh of 64 rows against 50000 x
-// 2048 94 -> 100 us (the epilogue of a tile holds up the parts of the next), of 1000 rows against 50001 x 2048 330 -> 335.
+// 2048 94 -> 97 us (the epilogue of a tile holds up the parts of the next), of 1000 rows against 50001 x 2048 nothing that shows.
 // The gradients are rounded to bf16, but dw sums over up to 2^24 rows and dh over pieces of millions of entries: a sum of one
 // sign over 2^24 rows lost 1 %.  They take 4096 at a time.
 template <int kPair, int kMode>
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
       // 16-byte piece c, keep(r, c, piece) stores piece c of row r of the warp's 32.
       auto turn = [&](int pieces, auto fill, auto keep) {
         int lane = static_cast<int>(threadIdx.x & 31);
-        asm volatile("" : "+r"(lane));   // so that no address formed of it is kept (in local memory) from tile to tile
+        if constexpr (kParts) asm volatile("" : "+r"(lane));   // no address formed of it is kept from tile to tile: registers are short
         uint8_t* mine = smem + L::kStages * L::kStage + (warp - 2) * 4096;
 #pragma unroll
         for (int c0 = 0; c0 < pieces; c0 += 8) {
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) rfq_ce_kernel(const __grid_consta
           for (int c = 0; c < 8; ++c)
             if (c0 + c < pieces) *reinterpret_cast<uint4*>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) = fill(c0 + c);
           __syncwarp();
-#pragma unroll
+#pragma unroll(kParts ? 4 : 8)
           for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + (lane >> 3), c = lane & 7;
             if (c0 + c < pieces) keep(r, c0 + c, *reinterpret_cast<const uint4*>(mine + r * 128 + ((c ^ (r & 7)) << 4)));
@@ -626,8 +626,9 @@ __global__ void __launch_bounds__(1024) rfq_ce_join_kernel(const float2* stats, 
 
 // Before the products.  Block 0: gmax = largest finite |dloss| over the rows that count.  The others, where dw is wanted:
 // a copy of h whose ignored rows are zero.  dz of such a row is zero, but dw = dz^T h would still take 0 x NaN or
-// 0 x inf from padding that nobody wrote.  (A warp for each 2 KiB of a row: both gradients of 4096 x 4096 against 32768 take 2.56 ms
-// with the copy and without, dw of 16 rows 126 us and 125; a warp for each row took 7 us more for one row.)
+// 0 x inf from padding that nobody wrote.  (A warp for each 2 KiB of a row.  dw of 300 rows against 5000 x 1024 25 -> 28 us, of 64
+// against 50000 x 2048 97 -> 104 with the logits' parts, of 4096 against 8192 x 4096 415 -> 435, both gradients against 32768 x 4096
+// 2.56 ms as before; a warp for each row took 7 us more for one row.)
 constexpr int kCopyRun = 128;   // 16-byte vectors
 __global__ void __launch_bounds__(1024) rfq_ce_prepare_kernel(const float* dloss, const int64_t* labels, int M, int64_t ignore, float* gmax,
                                                               const uint4* h, uint4* clean, int vecs) {
@@ -639,14 +640,14 @@ __global__ void __launch_bounds__(1024) rfq_ce_prepare_kernel(const float* dloss
     const int runs = (vecs + kCopyRun - 1) / kCopyRun;   // of a row; M * runs < 2^30
     for (int i = (static_cast<int>(blockIdx.x) - 1) * 32 + warp; i < M * runs; i += (static_cast<int>(gridDim.x) - 1) * 32) {
       const int row = i / runs, c0 = (i - row * runs) * kCopyRun + lane;
-      const bool keep = labels[row] != ignore;
+      const int64_t label = labels[row];
       const int64_t at = static_cast<int64_t>(row) * vecs + c0;
-      uint4 v[kCopyRun / 32];
+      uint4 v[kCopyRun / 32];   // asked for beside the label, not after it
 #pragma unroll
-      for (int u = 0; u < kCopyRun / 32; ++u) v[u] = keep && c0 + 32 * u < vecs ? h[at + 32 * u] : make_uint4(0u, 0u, 0u, 0u);
+      for (int u = 0; u < kCopyRun / 32; ++u) v[u] = c0 + 32 * u < vecs ? h[at + 32 * u] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int u = 0; u < kCopyRun / 32; ++u)
-        if (c0 + 32 * u < vecs) clean[at + 32 * u] = v[u];
+        if (c0 + 32 * u < vecs) clean[at + 32 * u] = label != ignore ? v[u] : make_uint4(0u, 0u, 0u, 0u);
     }
     return;
   }
