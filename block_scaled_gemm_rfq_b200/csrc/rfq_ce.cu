@@ -11,8 +11,8 @@
 // accumulator of the tensor cores (TMEM).  Forward: the epilogue reduces each tile row to
 // (max, sum of exponentials) over 128 (or 32) columns and a second kernel joins those parts.
 // Backward: for one piece of the vocabulary at a time the logits are computed again,
-// turned into dz with the known lse, rounded to bf16 into a workspace of bounded size,
-// and multiplied with w (dh, accumulated over the pieces in fp32) and h (dw, complete).
+// turned into dz with the known lse, rounded to bf16 into the workspace, and multiplied with
+// w (dh, accumulated over the pieces in fp32) and h (dw, complete).
 //
 // All four products run in one persistent, warp-specialized kernel on tcgen05 kind::f16
 // MMAs; what differs is how the operands lie in shared memory (along K, or along M/N for
@@ -21,7 +21,7 @@
 //   kLogits  A = h (K-major)          B = w piece (K-major)     row statistics
 //   kGrad    A = h (K-major)          B = w piece (K-major)     dz in bf16
 //   kHidden  A = dz (K-major)         B = w piece (N-major)     dh, fp32 sums or bf16
-//   kHead    A = dz (M-major)         B = h (N-major)           dw in bf16
+//   kHead    A = dz (M-major)         B = h (N-major, a copy)   dw in bf16
 //
 // Roles (per CTA): warp 0 TMA producer, warp 1 MMA issuer (leader CTA of a pair),
 // warps 2..9 epilogue.  Two 256-column accumulators, so that the epilogue of a tile runs
@@ -29,13 +29,13 @@
 // CTAs (128 x 256, or 128 x 64 against small heads) up to 128, where the rest of a pair's rows would be padding.
 // Every wait on an mbarrier is bounded (rfq_ptx.cuh).  No TMA multicast.
 //
-// Bounds and rates.  With many rows the tensor cores bound all four products: 4096 x 4096 against 8192
-// entries keeps the tensor pipe 87 % (kLogits), 91 % (kGrad), 91 % (kHidden) and 92 % (kHead) active, 1.53 to
-// 1.60 PFLOP/s with a cold start, a single launch each; under minutes of such load the card lowers its clock and
-// 2048 x 4096 against 131072 entries take 1.65 ms (1.33 PFLOP/s).  The backward pass computes the logits
-// once more, a fourth product to the three that training needs (4096 rows against 32768 x 4096: 3.3 ms forward and
-// backward, 1.33 PFLOP/s over the four): the price of holding no T x V matrix between the passes, 537 MB in fp32
-// there.  With few rows reading the head bounds them: 1 row against 131072 x 4096 takes 186 us, 5.8 TB/s; 8
+// Bounds and rates (a range is that of several cards).  With many rows the tensor cores bound all four products: 4096 x 4096 against
+// 8192 entries keeps the tensor pipe 88 % (kLogits), 83 % (kGrad), 90 % (kHidden) and 83 % (kHead) active, 1.45 to
+// 1.55 PFLOP/s with a cold start, a single launch each; under seconds of such load the card lowers its clock and
+// 2048 x 4096 against 131072 entries take 1.65 to 1.72 ms (1.28 to 1.33 PFLOP/s).  The backward pass computes the logits
+// once more, a fourth product to the three that training needs (4096 rows against 32768 x 4096: 3.36 to 3.48 ms forward and
+// backward, 1.26 to 1.31 PFLOP/s over the four): the price of holding no T x V matrix between the passes, 537 MB in fp32
+// there.  With few rows reading the head bounds them: 1 row against 131072 x 4096 takes 186 to 191 us, 5.6 to 5.8 TB/s; 8
 // rows against 32003 x 1024 20 us, half of it the two kernels' start and end.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -78,7 +78,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 template <int kPair, int kMode>
 constexpr int kPart = kMode == kLogits || kMode == kGrad ? (kPair == 2 ? 16 : 2) : 64;   // k-tiles
 // Contractions that fit one part have kernels of their own (kParts false): the sums over parts cost the epilogue registers, and
-// where it bounds the product that shows (dw of 64 rows of 50000 x 2048 110 -> 160 us).  Not the forward logits, which have
+// where it bounds the product that shows (dw of 64 rows of 50000 x 2048 104 -> 111 us, of 128 of 32768 x 4096 128 -> 141; of
+// 1000 rows the same).  Not the forward logits, which have
 // registers left, and the backward ones of few rows, whose parts are short.
 template <int kPair, int kMode>
 constexpr bool kAlwaysParts = kMode == kLogits || (kMode == kGrad && kPair == 1);
@@ -87,8 +88,9 @@ constexpr bool kAlwaysParts = kMode == kLogits || (kMode == kGrad && kPair == 1)
 // kept as the sum of two bf16 terms: rows T .. 2 T - 1 of dz are what rows 0 .. T - 1 left out.  dh takes both
 // in the one tile of 128 rows that it fills anyway and adds its rows at the end; dw takes a second k-tile.  Error
 // of dh against 64 bits with one and with two terms: 1 row 0.0031 and 0.0018, 6 rows 0.0020 and 0.0017 (a bf16
-// rounding alone is 0.0017).  It costs 1 row of 112492 x 2824 nothing (557 us), 3 of 3863 x 3112 72 -> 82 us; at 64
-// rows of 50000 x 2048 189 -> 217 us, for an error that is 0.0020 without.
+// rounding alone is 0.0017).  It cost 1 row of 112492 x 2824 nothing (557 us), 3 of 3863 x 3112 72 -> 82 us; at 64
+// rows of 50000 x 2048 189 -> 217 us, for an error that is 0.0020 without.  With more rows (0.0019 at
+// 4096) it would be two products beside the four.
 constexpr int64_t kTwoTermRows = 16;
 
 // Products that write a matrix pass its rows through 4 KiB of shared memory per epilogue warp, so that

@@ -15,7 +15,7 @@
 // Where the fp32 sum leaves [1e-30, 1e37] (values near 1e19 or below 1e-15) the piece is
 // added again in fp64, so the norm neither overflows nor underflows before its own value does.
 //
-// 40 tensors of 1.87 GB of bf16 in all: 0.93 to 0.95 ms for the three passes (5.6 GB), 5.9 to 6.0 TB/s; a shorter
+// 40 tensors of 1.87 GB of bf16 in all: 0.93 to 0.97 ms for the three passes (5.6 GB), 5.75 to 6.0 TB/s by the card; a shorter
 // list stays in L2 between the norm and the scaling (37 tensors of 90 MB, odd sizes and both types: 51 us).
 // Whole pieces go without a check at their vectors: with one at each, the same list took 1.22 ms.
 #include <cuda_bf16.h>

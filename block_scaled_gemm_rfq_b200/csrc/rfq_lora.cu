@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads) rfq_lora_expand_kernel(const ExpandP
 // the columns of expand by ranges.  (Asking for the weights' way to L2 ahead of time made it slower, 29.6
 // against 26.6 us for 256 rows of 48 adapters: the loads of 16 warps an SM keep memory as busy.)
 // 16 rows of 16 adapters of rank 16 (4096 -> 4096, 4.6 MB) take 7.0 us, nearly all of it start, two chains of
-// loads and the cluster's exchange; 256 rows of 48 of rank 32 (4096 -> 12288, 65 MB) 27.8 us, 2.3 TB/s: an item is a
+// loads and the cluster's exchange; 256 rows of 48 of rank 32 (4096 -> 12288, 65 MB) 27.8 to 28.9 us, 2.3 TB/s: an item is a
 // chain of grouping, shrink, exchange and expand, and there are too few of them to hide one's waits under another's.
 //
 // shrink: each warp takes 32 elements of the contraction at a time: lane (g, q) loads elements
@@ -1243,6 +1243,9 @@ int ring_stages(int stage_bytes, int other_bytes) {   // other_bytes: besides th
 // 1000 rows 21 against 18; 5120 -> 13824, rank 8, 1111 rows 30 against 25; an fp32 y counts half as
 // much again (rank 16, 1000 rows 15 against 19 us, 2000 rows 24 against 26).  Backward (dx), K = N =
 // 4096: rank 16, 128 rows 12 against 15 us, 1000 rows 25 against 16; rank 64, 128 rows 19 against 17.
+// Rows sorted by adapter, that is.  The ids are on the device, so a batch whose rows are not goes by the same rule, and a chunk of it costs a
+// pass for each adapter that it happens to hold: 4096 rows of 8 adapters of rank 16 in random order, 4096 -> 12288, 204 us against 60 sorted,
+// of 100 adapters 1493 against 106 (include/rfq.h asks for sorted rows).
 bool wide_forward(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n, bool f32) {
   return M > 64 && M > 32 * n && M * (r + 8) * (K + N) / 2 * (f32 ? 3 : 2) > 330000000;
 }
@@ -1262,7 +1265,8 @@ bool wide_ds(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {
 // stage, where the kernel here takes 32 and is bound by warp-level MMAs as the rank grows.  Measured, whole backward
 // pass, there against here, K = N = 4096: rank 32, 1500 rows 42 against 46 us; rank 64, 2000 rows 51 against 65, 2500
 // rows of 10 adapters 105 against 125, 300 rows of 4 66 against 51; rank 128, 400 rows 47 against 55, 2500 rows of 20
-// 287 against 339.  At rank 16 both read x and dy at nearly the same rate and the one here gathers rows that are
+// 287 against 339; rows in random order are gathered and want the kernel here (dB alone, 16384 rows of 8 adapters, rank 32 209
+// against 105, rank 64 224 against 153; of 16, rank 128 354 against 377).  At rank 16 both read x and dy at nearly the same rate and the one here gathers rows that are
 // not neighbours faster: one adapter, 4000 rows 60 against 59, 8000 rows 86 against 88, 16384 rows 140 against 147; 4
 // adapters row by row, 16384 rows 373 against 286.
 bool wide_outer(int64_t M, int64_t K, int64_t N, int64_t r, int64_t n) {

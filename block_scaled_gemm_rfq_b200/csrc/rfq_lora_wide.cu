@@ -25,10 +25,11 @@
 // adapters held the base back and cost 1.3 times those of one), are added to in shared memory and leave from
 // there by TMA.
 //
-// 16384 rows of one adapter of rank 16, 4096 -> 4096: both products 78 us, of which reading src and base and writing
+// 16384 rows of one adapter of rank 16, 4096 -> 4096: both products 81 us, of which reading src and base and writing
 // out needs 63 (402 MB); alone shrink takes 36 us (134 MB, 3.8 TB/s: some 9 us of it are start, first loads and the
-// cluster's exchange) and expand 44 (268 MB, 6.1 TB/s).  4096 rows of 8 adapters of rank 64, 4096 -> 12288: 58 us where
-// chunks hold one adapter (floor 39), 61 to 66 where requests end inside them, which are then passed over twice.
+// cluster's exchange) and expand 45 (268 MB, 6 TB/s).  4096 rows of 8 adapters of rank 64, 4096 -> 12288: 61 us where
+// chunks hold one adapter (floor 39), 65 to 68 where requests end inside them, which are then passed over twice.  What a chunk
+// holds decides: in random order 16384 rows of 8, 16, 64 adapters of rank 16 take 362, 680 and 2220 us, sorted 96, 98 and 106.
 // Stages of 128 elements of the contraction in shrink, for longer pieces of a row, were no faster.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, the others epilogue.  Every wait on an mbarrier
@@ -384,8 +385,8 @@ constexpr int kTerms = kF32 ? 3 : 2;
 // With one adapter (or where shrink left no counts) all chunks are alike: units of 4 to 16 tiles go round the CTAs.
 // Else a chunk is passed over once for each adapter in it, and the tiles of all chunks, one chunk after the other, are
 // cut into one part for each CTA, of equal work: 2 for a tile and 3 for each pass over it (a tile of two adapters took
-// 1.6 times the time of one).  Both products of 4096 rows of 8 requests that end inside chunks, rank 64, 4096 ->
-// 12288: 61 to 66 us with parts against 70 to 79 with units; 8 requests of 512 rows each 58 against 55; one
+// 1.6 times the time of one).  Measured with s in one term, both products of 4096 rows of 8 requests that end inside chunks, rank 64,
+// 4096 -> 12288: 61 to 66 us with parts against 70 to 79 with units; 8 requests of 512 rows each 58 against 55; one
 // adapter 55 against 53.
 struct Place {
   int64_t chunk;
