@@ -1214,7 +1214,12 @@ cudaError_t launch_lora_shrink_wide(const void* src, const void* pool, bool tran
   p.stages = sums + 2048 < room ? static_cast<int>((room - 2048 - sums) / stage) : 0;
   if (p.stages < 3) p.stages = static_cast<int>((kSmemLimit - 2048 - sums) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * stage + sums;
+  // Never less than 112 KiB.  CTAs that share an SM share its tensor memory too: two of this kernel fit there by their columns, but one
+  // beside a CTA of the short-batch GEMM (all 512 columns, 120 KiB, a cluster as well) on another stream would let each of two clusters
+  // hold what a CTA of the other waits for, for good.
+  constexpr size_t kLeastSmem = 112 * 1024;
+  static_assert(2 * (kLeastSmem + 2048) <= 228 * 1024 && kLeastSmem + 120 * 1024 > 228 * 1024, "two of these an SM, none beside a 120 KiB one");
+  const size_t need = 1024 + static_cast<size_t>(p.stages) * stage + sums, smem = need > kLeastSmem ? need : kLeastSmem;
   return trans ? launch(rfq_lora_shrink_wide_kernel<true>, maps, p, chunks * p.cluster, kShrinkThreads, smem, p.cluster, stream)
                : launch(rfq_lora_shrink_wide_kernel<false>, maps, p, chunks * p.cluster, kShrinkThreads, smem, p.cluster, stream);
 }

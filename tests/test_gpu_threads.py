@@ -52,3 +52,34 @@ def test_adapters_of_other_ranks_at_once(rfq, shapes, dtype):
     assert not any(t.is_alive() for t in threads)
     assert wrong == []
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("r", [8, 32, 56])
+def test_long_adapter_batches_beside_short_projections(rfq, r):
+    """The adapters' shrink and the short-batch GEMM both run in clusters and hold tensor memory; on two streams at once they must
+    not wait for one another (a CTA of the one never shares an SM with one of the other)."""
+    M, K, N, n = 4096, 4096, 2048, 3
+    c = make(M, K, N, r, n, "runs", seed=r)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(r)
+    qw = rfq.quantize_weight_alloc((torch.randn((4096, 4096), generator=g, device="cuda") * 0.02).bfloat16())
+    xs = [torch.randn((rows, 4096), generator=g, device="cuda").bfloat16() for rows in (40, 64, 100)]
+    want_y = [rfq.linear_alloc(x, qw, use_residual=False) for x in xs]
+    want = rfq.lora_alloc(c["x"], c["a"], c["b"], c["scale"], c["ids"], base=c["base"], want_hidden=True)
+    want_b = rfq.lora_backward_alloc(c["x"], c["a"], c["b"], c["scale"], c["ids"], c["dy"], want[1], dx_base=c["dx_base"], want_da=False, want_db=False)
+    y, hidden, dx = torch.empty_like(c["base"]), torch.empty_like(want[1]), torch.empty_like(c["dx_base"])
+    ws = torch.empty(rfq.lora_workspace_bytes(M, K, N, r, n, backward=True), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(t) for t in want_y]
+    ws_y = [torch.empty(rfq.linear_workspace_bytes(x.shape[0], 4096), dtype=torch.uint8, device="cuda") for x in xs]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(60):
+        rfq.lora(c["x"], c["a"], c["b"], c["scale"], c["ids"], y, ws, base=c["base"], hidden=hidden, stream=a)
+        rfq.lora_backward(c["x"], c["a"], c["b"], c["scale"], c["ids"], c["dy"], hidden, ws, dx=dx, dx_base=c["dx_base"], stream=a)
+        for _ in range(4):
+            for x, out, w in zip(xs, outs, ws_y):
+                rfq.linear(x, qw.codes, qw.scales, 4096, out, w, use_residual=False, stream=b)
+    torch.cuda.synchronize()
+    rfq.check_device_error()
+    assert torch.equal(y, want[0]) and torch.equal(hidden, want[1]) and torch.equal(dx, want_b[0])
+    assert all(torch.equal(p, q) for p, q in zip(outs, want_y))
