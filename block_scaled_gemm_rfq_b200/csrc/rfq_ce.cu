@@ -820,7 +820,7 @@ cudaError_t product(EncodeTiledFn encode, const void* a, int64_t a_ld, const voi
   return pair ? launch_mode<2, kMode, kBN>(maps, p, stream) : launch_mode<1, kMode, kBN>(maps, p, stream);
 }
 
-constexpr int64_t kForwardRows = 32768;            // rows of one forward pass (bounds the statistics)
+constexpr int64_t kForwardRows = 32768;            // rows of one forward pass, at most (bounds the statistics)
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 constexpr int64_t kMinPiece = 2048;
 
@@ -872,8 +872,11 @@ size_t ce_backward_workspace(int64_t T, int64_t D, int64_t V, bool want_dh, bool
 cudaError_t launch_ce_forward(const void* h, const void* w, const int64_t* labels, int64_t T, int64_t D, int64_t V,
                               int64_t ignore, float* loss, float* lse, void* ws, void* encode_tiled, int skip_fill, cudaStream_t stream) {
   EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(encode_tiled);
-  for (int64_t t0 = 0; t0 < T; t0 += kForwardRows) {
-    const int64_t rows = T - t0 < kForwardRows ? T - t0 : kForwardRows;
+  // Even groups: a last one of few rows would be summed in the parts of few rows (kPart), and the backward pass, which takes all rows at
+  // once, would not find the logits that its lse is of (10 % of 1 - p = 1e-3 for logits near 100).
+  const int64_t group = ceil_div(T, ceil_div(T, kForwardRows));
+  for (int64_t t0 = 0; t0 < T; t0 += group) {
+    const int64_t rows = T - t0 < group ? T - t0 : group;
     const int columns = tile_columns(rows, V), parts = static_cast<int>(2 * ceil_div(V, columns));
     Params p = {};
     p.labels = labels + t0;

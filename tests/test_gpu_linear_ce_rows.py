@@ -79,3 +79,36 @@ def test_head_gradient_of_very_many_rows(rfq):
     total = sum(part.double().sum(0) for part in h.split(1 << 22))
     want = total[None, :] * torch.cat([torch.full((1, 1), 1 / 64 - 1.0), torch.full((V - 1, 1), 1 / 64)]).double().cuda()
     assert ((dw.double() - want).abs() <= (2.0 ** -8 + 1e-5 + 2.0 ** -12) * want.abs()).all()
+
+
+@pytest.mark.parametrize("T", [32868, 65537])
+def test_certain_labels_of_the_last_rows(rfq, T):
+    """The forward pass takes long batches in groups of rows, and a last group of few rows is still summed as the backward pass sums
+    it.  Logits near 100, of which the label's leads by 12.6: a difference of 1e-6 of the logits between the passes would be 10 % of
+    1 - p.  Only the last 100 rows count (or the one past two full groups).  Same bounds as in test_certain_labels."""
+    D, V, y0 = 4096, 300, 7
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    h = torch.empty((T, D), dtype=torch.bfloat16, device="cuda")
+    for part in h.split(8192):
+        part.copy_(0.5 + torch.rand(part.shape, generator=g, device="cuda"))
+    w = torch.randn((V, D), generator=g, device="cuda") / D ** 0.5 + 87.2 / D
+    w[y0] = 100.0 / D * (0.5 + torch.rand((D,), generator=g, device="cuda"))
+    w = w.bfloat16()
+    last = slice(T - (T % 32768 if T % 32768 > 1 else 1), T)
+    labels = torch.full((T,), IGNORE, device="cuda")
+    labels[last] = y0
+    h64, w64 = h[last].double(), w.double()
+    z = h64 @ w64.T
+    lse64 = torch.logsumexp(z, 1)
+    p = torch.exp(z - lse64[:, None])
+    dz, others = p.clone(), p.clone()
+    others[:, y0] = 0
+    dz[:, y0] = -others.sum(1)
+    assert ((-dz[:, y0] > 1e-5) & (-dz[:, y0] < 1e-1)).all()
+    # every logit is off by dz in the same way in both passes, those of a row by nearly the same share: 2 dz of the logits' spread
+    spread = 1e-5 * float((z.amax(1) - z.amin(1)).max())
+    term = (2.0 ** -8 + 2 * spread + 2e-5) * dz.abs() + p * (2 * lse64.abs()[:, None] * 2.0 ** -24 + 2.0 ** -22)
+    _, lse = rfq.linear_ce_alloc(h, w, labels)
+    _, dw = rfq.linear_ce_backward_alloc(h, w, labels, lse, torch.ones(T, device="cuda"), want_dh=False)
+    check("dw", dw, (dz.T @ h64, term.T @ h64.abs() + 2.0 ** -8 * (dz.T @ h64).abs()))
