@@ -5,6 +5,7 @@ import threading
 import pytest
 import torch
 
+from tests.test_gpu_linear_ce import make as make_head
 from tests.test_gpu_lora import BF16, F32, make
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +84,49 @@ def test_long_adapter_batches_beside_short_projections(rfq, r):
     rfq.check_device_error()
     assert torch.equal(y, want[0]) and torch.equal(hidden, want[1]) and torch.equal(dx, want_b[0])
     assert all(torch.equal(p, q) for p, q in zip(outs, want_y))
+
+
+def head(rfq, shape, stream, rounds, wrong, barrier):
+    try:
+        torch.cuda.set_device(0)
+        with torch.cuda.stream(stream):
+            T, D, V = shape
+            h, w, labels, dloss = make_head(T, D, V, seed=T)
+            loss, lse, dh, dw = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(h), torch.empty_like(w)
+            ws = torch.empty(rfq.linear_ce_workspace_bytes(T, D, V, True, True), dtype=torch.uint8, device="cuda")
+            grads = [torch.empty_like(dh), torch.empty_like(dw)]
+            norm, clip_ws = torch.empty(1, device="cuda"), torch.empty(rfq.grad_clip_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+            stream.synchronize()
+            first = None
+            barrier.wait()
+            for i in range(rounds):
+                rfq.linear_ce(h, w, labels, loss, lse, ws)
+                rfq.linear_ce_backward(h, w, labels, lse, dloss, dh, dw, ws)
+                rfq.grad_clip([dh, dw], 0.5, norm, clip_ws, outs=grads)
+                if i == 0 or i == rounds - 1:
+                    stream.synchronize()
+                    now = [t.clone() for t in (loss, lse, dh, dw, norm, *grads)]
+                    if first is None:
+                        first = now
+                    elif not all(torch.equal(a, b) for a, b in zip(first, now)):
+                        wrong.append((shape, "results differ"))
+            stream.synchronize()
+    except Exception as e:   # noqa: BLE001 (reported by the test)
+        wrong.append((shape, repr(e)))
+        barrier.abort()
+
+
+def test_every_operator_at_once(rfq):
+    """Heads of few and many rows with their gradients clipped, adapters of short and long batches: a thread and a stream each."""
+    heads, batches = [(9, 264, 3000), (100, 520, 20000), (600, 256, 5000)], [(40, 264, 312, 72, 3), (1201, 1032, 5128, 40, 3)]
+    wrong, barrier = [], threading.Barrier(len(heads) + len(batches))
+    threads = [threading.Thread(target=head, args=(rfq, s, torch.cuda.Stream(), 100, wrong, barrier)) for s in heads]
+    threads += [threading.Thread(target=adapters, args=(rfq, s, BF16, torch.cuda.Stream(), 100, wrong, barrier)) for s in batches]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not any(t.is_alive() for t in threads)
+    assert wrong == []
+    torch.cuda.synchronize()
+    rfq.check_device_error()
